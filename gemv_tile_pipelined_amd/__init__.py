@@ -3,6 +3,10 @@
     gemm_f16(A, B, D=None)   D = A · Bᵀ   A [M,K], B [N,K], D [M,N]  (fp16, FP32 accumulate)
     gemv_f16(x, W, y=None)   y = x · Wᵀ   x [K],   W [N,K], y [N]
 
+Block-scaled 8-bit products, their quantisers and products grouped by expert
+(gemm_fp8_*, quantize_fp8_*, gemm_grouped_*) are in blocks.py and reached from
+here as well.
+
 This module only marshals arguments: it checks tensor dtypes, devices and
 shapes, passes raw device pointers, sizes and the current HIP stream to
 libgemvtile.so (see include/gemvtile.h), and turns a nonzero status into an
@@ -50,6 +54,9 @@ __all__ = [
     "device_caps",
     "ring_trace",
     "alloc_splitk_workspace",
+    "xcd_block_id",
+    "grouped_plan",
+    "group_unit",
 ]
 
 LIBRARY_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgemvtile.so")
@@ -79,6 +86,23 @@ EXPORTED_SYMBOLS = (
     "gemvtile_gemm_f16_timed",
     "gemvtile_gemv_f16_variant",
     "gemvtile_xcd_logical_id",
+    "quantize_fp8_rows_f16",
+    "quantize_fp8_rows_bf16",
+    "quantize_fp8_tiles_f16",
+    "quantize_fp8_tiles_bf16",
+    "gemm_fp8_f16",
+    "gemm_fp8_bf16",
+    "gemm_grouped_f16",
+    "gemm_grouped_bf16",
+    "gemm_grouped_dgrad_f16",
+    "gemm_grouped_dgrad_bf16",
+    "gemm_grouped_wgrad_f16",
+    "gemm_grouped_wgrad_bf16",
+    "gemm_grouped_fp8_f16",
+    "gemm_grouped_fp8_bf16",
+    "gemvtile_xcd_block_id",
+    "gemvtile_grouped_plan",
+    "gemvtile_group_unit",
 )
 
 STATUS_NAMES = {
@@ -163,6 +187,20 @@ def load_library(path: str = LIBRARY_PATH) -> ctypes.CDLL:
     lib.gemvtile_device_caps.restype = c_int
     lib.gemvtile_ring_trace.argtypes = [c_int, i64, ctypes.POINTER(ctypes.c_int32), i64, intp]
     lib.gemvtile_ring_trace.restype = i64
+    for fmt in ("f16", "bf16"):
+        for name, args in (("quantize_fp8_rows", [vp] * 3 + [i64] * 2), ("quantize_fp8_tiles", [vp] * 3 + [i64] * 3),
+                           ("gemm_fp8", [vp] * 5 + [i64] * 4), ("gemm_grouped", [vp] * 4 + [i64] * 4),
+                           ("gemm_grouped_dgrad", [vp] * 4 + [i64] * 4), ("gemm_grouped_wgrad", [vp] * 4 + [i64] * 4),
+                           ("gemm_grouped_fp8", [vp] * 6 + [i64] * 4)):
+            call = getattr(lib, f"{name}_{fmt}")
+            call.argtypes = [*args, vp]
+            call.restype = c_int
+    lib.gemvtile_xcd_block_id.argtypes = [i64, i64]
+    lib.gemvtile_xcd_block_id.restype = i64
+    lib.gemvtile_grouped_plan.argtypes = [c_int] + [i64] * 5 + [intp] * 2
+    lib.gemvtile_grouped_plan.restype = c_int
+    lib.gemvtile_group_unit.argtypes = [ctypes.POINTER(ctypes.c_int32)] + [i64] * 4 + [i64p] * 3
+    lib.gemvtile_group_unit.restype = i64
     if path == LIBRARY_PATH:
         _lib = lib
     return lib
@@ -433,6 +471,10 @@ def xcd_logical_id(w: int, grid: int) -> int:
     return int(load_library().gemvtile_xcd_logical_id(w, grid))
 
 
+def xcd_block_id(w: int, grid: int) -> int:
+    return int(load_library().gemvtile_xcd_block_id(w, grid))
+
+
 def gemm_config() -> dict:
     vals = [ctypes.c_int() for _ in range(6)]
     load_library().gemvtile_gemm_config(*[ctypes.byref(v) for v in vals])
@@ -485,3 +527,43 @@ def device_caps() -> dict:
     _check(load_library().gemvtile_device_caps(*[ctypes.byref(v) for v in vals]))
     keys = ("num_cus", "clock_khz", "mem_clock_khz", "mem_bus_bits")
     return {k: v.value for k, v in zip(keys, vals)}
+
+
+GROUPED_OPS = {"forward": 0, "dgrad": 1, "wgrad": 2, "fp8": 3}
+
+
+def grouped_plan(op: str, T: int, N: int, K: int, E: int, num_cus: int):
+    """("stream" or "tiled", rows, cols): the kernel a grouped product (op "forward", "dgrad", "wgrad" or "fp8") runs
+    on num_cus CUs, and the rows and columns of the output that a workgroup takes at a time."""
+    rows, cols = ctypes.c_int(), ctypes.c_int()
+    kind = int(load_library().gemvtile_grouped_plan(GROUPED_OPS[op], T, N, K, E, num_cus, ctypes.byref(rows),
+                                                    ctypes.byref(cols)))
+    if kind < 0:
+        raise GemvTileError(1, "sizes out of range")
+    return ("stream" if kind else "tiled"), rows.value, cols.value
+
+
+def group_unit(offsets, T: int, rows: int, unit: int):
+    """(group, first row, one past the last row, units allowed for) of unit `unit` of the groups that `offsets` (a
+    sequence of ints) makes of T rows, cut into units of `rows` rows; None past the last unit."""
+    arr = (ctypes.c_int32 * len(offsets))(*offsets)
+    vals = [ctypes.c_int64() for _ in range(3)]
+    n = int(load_library().gemvtile_group_unit(arr, len(offsets) - 1, T, rows, unit, *[ctypes.byref(v) for v in vals]))
+    if n == -2:
+        raise GemvTileError(1, "sizes out of range")
+    return None if n < 0 else (*(v.value for v in vals), n)
+
+
+def __getattr__(name):
+    # The 8-bit and grouped products (blocks.py) need torch to be imported; the
+    # rest of the module imports it only when a tensor is passed.
+    if name == "blocks" or name.endswith(("_f16", "_bf16")):
+        import importlib
+
+        blocks = importlib.import_module(".blocks", __name__)
+        if name == "blocks":
+            return blocks
+        if name in blocks.__all__:
+            value = globals()[name] = getattr(blocks, name)
+            return value
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

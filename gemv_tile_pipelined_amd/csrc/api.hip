@@ -10,6 +10,7 @@
 #include <atomic>
 
 #include "../../include/gemvtile.h"
+#include "groups.hpp"
 #include "kernels.hpp"
 #include "tile_order.hpp"
 
@@ -343,6 +344,11 @@ int64_t gemvtile_xcd_logical_id(int64_t w, int64_t grid) {
   return gt::xcd_logical_id(w, grid);
 }
 
+int64_t gemvtile_xcd_block_id(int64_t w, int64_t grid) {
+  if (grid <= 0 || w < 0 || w >= grid) return -1;
+  return gt::xcd_block_id(w, grid);
+}
+
 void gemvtile_gemm_config(int *bm, int *bn, int *bk, int *stages, int *threads, int *group_m) {
   if (bm) *bm = gt::kGemmBM;
   if (bn) *bn = gt::kGemmBN;
@@ -406,6 +412,188 @@ int gemvtile_gemm_tile(int64_t M, int64_t N, int64_t num_cus, int *bm, int *bn, 
   if (bn) *bn = t.bn;
   if (stages) *stages = t.stages;
   return GEMVTILE_OK;
+}
+
+}  // extern "C"
+
+// ---- block-scaled 8-bit operands and products by expert --------------------
+namespace {
+constexpr int64_t kMaxFp8Rows = int64_t{1} << 25;  // a grid's threads are counted in 32 bits
+constexpr int64_t kMaxFp8K = 4194288;
+constexpr int64_t kMaxGroupedCols = int64_t{1} << 20;
+constexpr int64_t kMax32 = (int64_t{1} << 31) - 1;
+
+int64_t blocks_of(int64_t n) { return (n + 127) / 128; }
+
+int run_quantize(const void *x, void *q, float *scale, int64_t E, int64_t N, int64_t K, bool tiles, void *stream,
+                 int dtype) {
+  if (E < 0 || N < 0 || K < 0) return GEMVTILE_ERR_INVALID_ARG;
+  if (E == 0 || N == 0 || K == 0) return GEMVTILE_OK;
+  if (x == nullptr || q == nullptr || scale == nullptr) return GEMVTILE_ERR_INVALID_ARG;
+  if (K % 16 != 0 || E > kMax32 || N > kMax32 || K > kMax32) return GEMVTILE_ERR_UNSUPPORTED;
+  const int64_t rows = tiles ? blocks_of(N) : N;
+  const int64_t most = tiles ? (int64_t{1} << 24) - 1 : (int64_t{1} << 29) - 1;
+  if (rows > most / blocks_of(K) || E > most / (rows * blocks_of(K))) return GEMVTILE_ERR_UNSUPPORTED;
+  if (misaligned(x, 16) || misaligned(q, 16) || misaligned(scale, 4)) return GEMVTILE_ERR_UNSUPPORTED;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return to_status(tiles ? gt::launch_quantize_tiles(dtype, x, q, scale, static_cast<int>(E), static_cast<int>(N),
+                                                     static_cast<int>(K), s)
+                         : gt::launch_quantize_rows(dtype, x, q, scale, N, static_cast<int>(K), s));
+}
+
+int run_gemm_fp8(const void *A, const float *sa, const void *B, const float *sb, void *D, int64_t M, int64_t N, int64_t K,
+                 int64_t sb_rows, void *stream, int out) {
+  if (M < 0 || N < 0 || K < 0 || (sb_rows != 1 && sb_rows != 128)) return GEMVTILE_ERR_INVALID_ARG;
+  if (M == 0 || N == 0) return GEMVTILE_OK;
+  if (D == nullptr) return GEMVTILE_ERR_INVALID_ARG;
+  if (K > 0 && (A == nullptr || B == nullptr || sa == nullptr || sb == nullptr)) return GEMVTILE_ERR_INVALID_ARG;
+  if (M > kMaxFp8Rows || N > kMaxFp8Rows || K > kMaxFp8K || K % 16 != 0) return GEMVTILE_ERR_UNSUPPORTED;
+  if (misaligned(D, 2)) return GEMVTILE_ERR_UNSUPPORTED;
+  if (K > 0 && (misaligned(A, 16) || misaligned(B, 16) || misaligned(sa, 4) || misaligned(sb, 4)))
+    return GEMVTILE_ERR_UNSUPPORTED;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int m = static_cast<int>(M), n = static_cast<int>(N), k = static_cast<int>(K), r = static_cast<int>(sb_rows);
+  if (M <= gt::kFp8StreamRows) return to_status(gt::launch_stream_fp8(out, A, sa, B, sb, r, D, m, n, k, s));
+  int cus = 0;
+  const int st = current_cu_count(&cus);
+  if (st != GEMVTILE_OK) return st;
+  return to_status(gt::launch_gemm_fp8(out, A, sa, B, sb, r, D, m, n, k, cus, s));
+}
+
+enum GroupedOp { kOpForward = 0, kOpDgrad = 1, kOpWgrad = 2, kOpFp8 = 3 };
+
+// A and B as the kernels take them (X, W; dY, W; dY, X).  The limits shared by
+// the launch and the plan.
+int check_grouped_sizes(int op, int64_t T, int64_t N, int64_t K, int64_t E) {
+  if (T < 0 || N < 0 || K < 0 || E < 0) return GEMVTILE_ERR_INVALID_ARG;
+  if (T > kMaxRows || N > kMaxGroupedCols || K > kMaxGroupedCols || E > gt::kMaxGroups) return GEMVTILE_ERR_UNSUPPORTED;
+  if (K % (op == kOpFp8 ? 16 : 8) != 0) return GEMVTILE_ERR_UNSUPPORTED;
+  if ((op == kOpDgrad || op == kOpWgrad) && N % 8 != 0) return GEMVTILE_ERR_UNSUPPORTED;
+  if (op == kOpWgrad && E * blocks_of(N) * blocks_of(K) >= (int64_t{1} << 24)) return GEMVTILE_ERR_UNSUPPORTED;
+  return GEMVTILE_OK;
+}
+
+int run_grouped(int op, const void *A, const float *sa, const void *B, const float *sb, const int32_t *offsets, void *D,
+                int64_t T, int64_t N, int64_t K, int64_t E, void *stream, int dtype) {
+  if (T < 0 || N < 0 || K < 0 || E < 0) return GEMVTILE_ERR_INVALID_ARG;
+  // Elements of the output, and of the sum of each.
+  if (E == 0 || (op == kOpWgrad ? N == 0 || K == 0 : T == 0 || (op == kOpDgrad ? K : N) == 0)) return GEMVTILE_OK;
+  const int64_t summed = op == kOpDgrad ? N : op == kOpWgrad ? T : K;
+  if (D == nullptr || offsets == nullptr) return GEMVTILE_ERR_INVALID_ARG;
+  if (summed > 0 && (A == nullptr || B == nullptr || (op == kOpFp8 && (sa == nullptr || sb == nullptr))))
+    return GEMVTILE_ERR_INVALID_ARG;
+  int st = check_grouped_sizes(op, T, N, K, E);
+  if (st != GEMVTILE_OK) return st;
+  if (misaligned(D, 2) || misaligned(offsets, 4)) return GEMVTILE_ERR_UNSUPPORTED;
+  if (summed > 0 && (misaligned(A, 16) || misaligned(B, 16) || misaligned(sa, 4) || misaligned(sb, 4)))
+    return GEMVTILE_ERR_UNSUPPORTED;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int t = static_cast<int>(T), n = static_cast<int>(N), k = static_cast<int>(K), e = static_cast<int>(E);
+  const int rows = op == kOpForward || op == kOpFp8 ? gt::grouped_stream_rows(T, N, E) : 0;
+  if (rows != 0)
+    return to_status(op == kOpFp8 ? gt::launch_stream_grouped_fp8(dtype, A, sa, B, sb, offsets, D, t, n, k, e, rows, s)
+                                  : gt::launch_stream_grouped(dtype, A, B, offsets, D, t, n, k, e, rows, s));
+  int cus = 0;
+  st = current_cu_count(&cus);
+  if (st != GEMVTILE_OK) return st;
+  switch (op) {
+    case kOpDgrad: return to_status(gt::launch_grouped_dgrad(dtype, A, B, offsets, D, t, n, k, e, cus, s));
+    case kOpWgrad: return to_status(gt::launch_grouped_wgrad(dtype, A, B, offsets, D, t, n, k, e, cus, s));
+    case kOpFp8: return to_status(gt::launch_grouped_fp8(dtype, A, sa, B, sb, offsets, D, t, n, k, e, cus, s));
+    default: return to_status(gt::launch_grouped_forward(dtype, A, B, offsets, D, t, n, k, e, cus, s));
+  }
+}
+}  // namespace
+
+extern "C" {
+
+int quantize_fp8_rows_f16(const void *x, void *q, float *scale, int64_t M, int64_t K, void *stream) {
+  return run_quantize(x, q, scale, 1, M, K, false, stream, gt::kF16);
+}
+int quantize_fp8_rows_bf16(const void *x, void *q, float *scale, int64_t M, int64_t K, void *stream) {
+  return run_quantize(x, q, scale, 1, M, K, false, stream, gt::kBF16);
+}
+int quantize_fp8_tiles_f16(const void *x, void *q, float *scale, int64_t E, int64_t N, int64_t K, void *stream) {
+  return run_quantize(x, q, scale, E, N, K, true, stream, gt::kF16);
+}
+int quantize_fp8_tiles_bf16(const void *x, void *q, float *scale, int64_t E, int64_t N, int64_t K, void *stream) {
+  return run_quantize(x, q, scale, E, N, K, true, stream, gt::kBF16);
+}
+
+int gemm_fp8_f16(const void *A, const float *scale_A, const void *B, const float *scale_B, void *D, int64_t M, int64_t N,
+                 int64_t K, int64_t scale_B_rows, void *stream) {
+  return run_gemm_fp8(A, scale_A, B, scale_B, D, M, N, K, scale_B_rows, stream, gt::kF16);
+}
+int gemm_fp8_bf16(const void *A, const float *scale_A, const void *B, const float *scale_B, void *D, int64_t M,
+                  int64_t N, int64_t K, int64_t scale_B_rows, void *stream) {
+  return run_gemm_fp8(A, scale_A, B, scale_B, D, M, N, K, scale_B_rows, stream, gt::kBF16);
+}
+
+int gemm_grouped_f16(const void *X, const void *W, const int32_t *offsets, void *D, int64_t T, int64_t N, int64_t K,
+                     int64_t E, void *stream) {
+  return run_grouped(kOpForward, X, nullptr, W, nullptr, offsets, D, T, N, K, E, stream, gt::kF16);
+}
+int gemm_grouped_bf16(const void *X, const void *W, const int32_t *offsets, void *D, int64_t T, int64_t N, int64_t K,
+                      int64_t E, void *stream) {
+  return run_grouped(kOpForward, X, nullptr, W, nullptr, offsets, D, T, N, K, E, stream, gt::kBF16);
+}
+int gemm_grouped_dgrad_f16(const void *dY, const void *W, const int32_t *offsets, void *dX, int64_t T, int64_t N,
+                           int64_t K, int64_t E, void *stream) {
+  return run_grouped(kOpDgrad, dY, nullptr, W, nullptr, offsets, dX, T, N, K, E, stream, gt::kF16);
+}
+int gemm_grouped_dgrad_bf16(const void *dY, const void *W, const int32_t *offsets, void *dX, int64_t T, int64_t N,
+                            int64_t K, int64_t E, void *stream) {
+  return run_grouped(kOpDgrad, dY, nullptr, W, nullptr, offsets, dX, T, N, K, E, stream, gt::kBF16);
+}
+int gemm_grouped_wgrad_f16(const void *dY, const void *X, const int32_t *offsets, void *dW, int64_t T, int64_t N,
+                           int64_t K, int64_t E, void *stream) {
+  return run_grouped(kOpWgrad, dY, nullptr, X, nullptr, offsets, dW, T, N, K, E, stream, gt::kF16);
+}
+int gemm_grouped_wgrad_bf16(const void *dY, const void *X, const int32_t *offsets, void *dW, int64_t T, int64_t N,
+                            int64_t K, int64_t E, void *stream) {
+  return run_grouped(kOpWgrad, dY, nullptr, X, nullptr, offsets, dW, T, N, K, E, stream, gt::kBF16);
+}
+int gemm_grouped_fp8_f16(const void *X, const float *scale_X, const void *W, const float *scale_W,
+                         const int32_t *offsets, void *D, int64_t T, int64_t N, int64_t K, int64_t E, void *stream) {
+  return run_grouped(kOpFp8, X, scale_X, W, scale_W, offsets, D, T, N, K, E, stream, gt::kF16);
+}
+int gemm_grouped_fp8_bf16(const void *X, const float *scale_X, const void *W, const float *scale_W,
+                          const int32_t *offsets, void *D, int64_t T, int64_t N, int64_t K, int64_t E, void *stream) {
+  return run_grouped(kOpFp8, X, scale_X, W, scale_W, offsets, D, T, N, K, E, stream, gt::kBF16);
+}
+
+int gemvtile_grouped_plan(int op, int64_t T, int64_t N, int64_t K, int64_t E, int64_t num_cus, int *rows, int *cols) {
+  if (op < kOpForward || op > kOpFp8 || T <= 0 || N <= 0 || K <= 0 || E <= 0 || num_cus <= 0 ||
+      num_cus > (int64_t{1} << 20) || rows == nullptr || cols == nullptr)
+    return -1;
+  if (check_grouped_sizes(op, T, N, K, E) != GEMVTILE_OK) return -1;
+  const int stream_rows = op == kOpForward || op == kOpFp8 ? gt::grouped_stream_rows(T, N, E) : 0;
+  if (stream_rows != 0) {
+    *rows = stream_rows;
+    *cols = 16;
+    return 1;
+  }
+  gt::grouped_tile(op, T, N, K, E, static_cast<int>(num_cus), rows, cols);
+  return 0;
+}
+
+int64_t gemvtile_group_unit(const int32_t *offsets, int64_t E, int64_t T, int64_t rows, int64_t unit, int64_t *group,
+                            int64_t *first, int64_t *past) {
+  if (offsets == nullptr || E <= 0 || E > gt::kMaxGroups || T < 0 || T > kMaxRows || rows <= 0 || rows > 4096 || unit < 0 ||
+      group == nullptr || first == nullptr || past == nullptr)
+    return -2;
+  for (int64_t e = 0; e < E; ++e) {
+    const gt::GroupRows g = gt::group_rows(offsets[e], offsets[e + 1], static_cast<int>(T));
+    const int64_t n = (g.end - g.begin + rows - 1) / rows;
+    if (unit < n) {
+      *group = e;
+      *first = g.begin + unit * rows;
+      *past = *first + rows < g.end ? *first + rows : g.end;
+      return gt::unit_bound(T, E, rows);
+    }
+    unit -= n;
+  }
+  return -1;
 }
 
 }  // extern "C"

@@ -1,0 +1,304 @@
+// fp8_gemm.hip -- tiled products of block-scaled e4m3 operands, dense and
+// grouped:
+//
+//   D[m, n] = sum_b sa[m, b] sb[n / r, b] sum_{k in block b} A[m, k] B[n, k]
+//
+// A K tile is one scale block of 128 columns, i.e. 128-byte LDS rows and one
+// 16x16x128 MFMA per 16x16 outputs, whose sum is scaled and added to an FP32
+// accumulator by four FMAs: the scales change from block to block, so the
+// matrix cores cannot accumulate across blocks themselves.  The FMAs need the
+// accumulators in ordinary VGPRs (not AGPRs), 256 of which a wave has beside
+// nothing else if two waves share a SIMD; hence 8 waves with 64x128 outputs
+// each (128 accumulators) on a 256x256 tile, two to a SIMD, so that one wave's
+// FMAs and LDS reads run beside the other's MFMAs.
+//
+// The ring holds STAGES K tiles: the operands' rows (direct-to-LDS loads,
+// swizzled as in gemm_kernel.hpp) and the scale of every row of A and of B for
+// this block (one 4-byte direct-to-LDS load per wave; with r = 128 rows of B
+// that share a scale load it again).  Operand order and epilogue are the
+// GEMM's: B first, so that a lane holds 4 consecutive columns of one row, its
+// row's scale is one number per 16 rows, and rows leave through LDS as whole
+// lines.
+#include "fp8_common.hpp"
+#include "groups.hpp"
+#include "kernels.hpp"
+
+#include <type_traits>
+
+namespace gt {
+
+namespace {
+
+struct Fp8Args {
+  const uint8_t *A, *B;
+  const float *sa, *sb;
+  const int *offsets;
+  uint16_t *D;
+  int M, N, K, E;  // M: rows of A (all groups)
+  int tiles_n;
+  int vec16;
+};
+
+template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int STAGES_>
+struct Fp8Shape {
+  static constexpr int BM = BM_, BN = BN_, WAVES_M = WAVES_M_, WAVES_N = WAVES_N_, STAGES = STAGES_;
+  static constexpr int kWaves = WAVES_M * WAVES_N;
+  static constexpr int kThreads = 64 * kWaves;
+  static constexpr int kWaveM = BM / WAVES_M, kWaveN = BN / WAVES_N;
+  static constexpr int kFragM = kWaveM / 16, kFragN = kWaveN / 16;
+  static constexpr int kRowBytes = kScaleBlock;
+  static constexpr int kRowsPerDma = 1024 / kRowBytes;
+  static constexpr int kDmaA = BM / kRowsPerDma / kWaves, kDmaB = BN / kRowsPerDma / kWaves;
+  static constexpr int kStageA = BM * kRowBytes;
+  static constexpr int kStageScales = (BM + BN) * kRowBytes;  // then BM + BN scales
+  static constexpr int kStageBytes = kStageScales + (BM + BN) * 4;
+  static constexpr int kPerStage = kDmaA + kDmaB + 1;
+  static constexpr int kStagePitch = kWaveN * 2 + 16;
+  static constexpr int kStagingBytes = kWaves * kWaveM * kStagePitch;
+  static constexpr int kRingBytes = STAGES * kStageBytes;
+  static constexpr int kLdsBytes = kRingBytes > kStagingBytes ? kRingBytes : kStagingBytes;
+  static_assert((BM + BN) / 64 == kWaves, "one scale load per wave and stage");
+  static_assert(kRowsPerDma * kWaves % 16 == 0 && BM % (kRowsPerDma * kWaves) == 0 && BN % (kRowsPerDma * kWaves) == 0,
+                "operand loads");
+  static_assert(kScaleBlock % kWaveN == 0, "a wave's columns share a scale of B when r = 128");
+  static_assert((STAGES - 1) * kPerStage <= 63, "vmcnt range");
+  // As GemmShape::swz for 128-byte rows.
+  __host__ __device__ static constexpr int swz(int row) { return (row & 7) ^ ((row >> 3) & 1); }
+};
+
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+// As lds_dma_b128, 4 bytes per lane: lane i's dword goes to lds_base + 4 i.
+__device__ inline void lds_dma_b32(int4_t rsrc, uint32_t voffset, uint32_t lds_base) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dword %0, %2, 0 offen lds"
+               : : "v"(voffset), "s"(lds_base), "s"(rsrc) : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+template <class S, int OUT, bool GROUPED, int SB>
+__global__ void __launch_bounds__(S::kThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
+fp8_gemm_kernel(Fp8Args a) {
+  // The table lies behind the ring in one allocation, so that the ring starts
+  // at LDS address 0 and its offsets fit the instructions.
+  __shared__ __attribute__((aligned(1024))) char smem[S::kLdsBytes + (GROUPED ? sizeof(GroupTable) : 0)];
+  GroupTable &table = *reinterpret_cast<GroupTable *>(smem + S::kLdsBytes);
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / S::WAVES_N;
+  const int wn = wave % S::WAVES_N;
+  const uint32_t lds0 = lds_addr(smem);
+  const int KT = (a.K + kScaleBlock - 1) / kScaleBlock;
+
+  const int ld_row = wave * S::kRowsPerDma + lane / 8;
+  const int ld_k = ((lane % 8) ^ S::swz(ld_row)) * 16;
+  constexpr int kRowStep = S::kRowsPerDma * S::kWaves;
+  const uint32_t ld_off = static_cast<uint32_t>(ld_row) * static_cast<uint32_t>(a.K) + static_cast<uint32_t>(ld_k);
+  const uint32_t ld_step = static_cast<uint32_t>(kRowStep) * static_cast<uint32_t>(a.K);
+  // Scales: wave w loads those of rows 64 w .. 64 w + 63 of A's rows followed
+  // by B's.
+  const bool scale_a = wave < S::BM / 64;
+  const int scale_row = (scale_a ? wave : wave - S::BM / 64) * 64 + lane;
+  const uint32_t scale_off =
+      static_cast<uint32_t>(scale_a || SB == 1 ? scale_row : scale_row / kScaleBlock) * static_cast<uint32_t>(KT) * 4u;
+
+  const int frag_row = lane % 16;
+  const int frag_kgrp = lane / 16;
+  const int frag_piece = ((frag_kgrp & 1) << 1) | (frag_kgrp >> 1);  // and frag_piece + 4
+  const uint32_t piece0 = static_cast<uint32_t>((frag_piece ^ S::swz(frag_row)) * 16);
+  const uint32_t piece1 = static_cast<uint32_t>(((frag_piece + 4) ^ S::swz(frag_row)) * 16);
+  const uint32_t a_base = static_cast<uint32_t>(wm * S::kWaveM + frag_row) * S::kRowBytes;
+  const uint32_t b_base = static_cast<uint32_t>(wn * S::kWaveN + frag_row) * S::kRowBytes + S::kStageA;
+  const uint32_t sa_base = S::kStageScales + static_cast<uint32_t>(wm * S::kWaveM + frag_row) * 4u;
+  const uint32_t sb_base =
+      S::kStageScales + static_cast<uint32_t>(S::BM + wn * S::kWaveN + (SB == 1 ? 4 * frag_kgrp : 0)) * 4u;
+
+  int units = (a.M + S::BM - 1) / S::BM;
+  if constexpr (GROUPED) {
+    build_group_table(&table, a.offsets, a.E, a.M, S::BM);
+    __syncthreads();
+    units = __builtin_amdgcn_readfirstlane(table.upto[a.E - 1]);
+  }
+  const int64_t num_tiles = static_cast<int64_t>(units) * a.tiles_n;
+  for (int64_t u = xcd_logical_id(blockIdx.x, gridDim.x); u < num_tiles; u += gridDim.x) {
+    const TileCoord tc = tile_of(u, units, a.tiles_n, kGemmGroupM);
+    GroupUnit g{0, static_cast<int>(tc.tm) * S::BM, a.M};
+    if constexpr (GROUPED) g = table_unit(&table, a.E, S::BM, static_cast<int>(tc.tm));
+    const int n0 = static_cast<int>(tc.tn) * S::BN;
+    const int rows = min(S::BM, g.end - g.row);
+    const int cols = min(S::BN, a.N - n0);
+    const int64_t b_row = static_cast<int64_t>(g.group) * a.N + n0;
+    const int4_t rsrc_a =
+        make_buffer_rsrc(a.A + static_cast<int64_t>(g.row) * a.K, static_cast<uint32_t>(rows) * a.K);
+    const int4_t rsrc_b = make_buffer_rsrc(a.B + b_row * a.K, static_cast<uint32_t>(cols) * a.K);
+    // This wave's rows of scales.
+    const int64_t sb_row =
+        SB == 1 ? b_row
+                : static_cast<int64_t>(g.group) * ((a.N + kScaleBlock - 1) / kScaleBlock) + n0 / kScaleBlock;
+    const int sb_rows = SB == 1 ? cols : (cols + kScaleBlock - 1) / kScaleBlock;
+    const int4_t rsrc_s = make_buffer_rsrc((scale_a ? a.sa + static_cast<int64_t>(g.row) * KT : a.sb + sb_row * KT),
+                                           static_cast<uint32_t>(scale_a ? rows : sb_rows) * KT * 4u);
+    uint32_t tile_off = ld_off;
+    int tile_k = ld_k;
+    asm volatile("" : "+v"(tile_off), "+v"(tile_k));
+
+    auto issue = [&](int kt) {
+      const uint32_t stage = lds0 + static_cast<uint32_t>((kt % S::STAGES) * S::kStageBytes);
+      const uint32_t dst = stage + static_cast<uint32_t>(wave) * 1024u;
+      const int k0 = kt * kScaleBlock;
+      const uint32_t off = k0 + tile_k < a.K ? tile_off + static_cast<uint32_t>(k0) : kOobOffset;
+#pragma unroll
+      for (int d = 0; d < S::kDmaA; ++d)
+        lds_dma_b128(rsrc_a, off + d * ld_step, __builtin_amdgcn_readfirstlane(dst + d * S::kWaves * 1024));
+#pragma unroll
+      for (int d = 0; d < S::kDmaB; ++d)
+        lds_dma_b128(rsrc_b, off + d * ld_step,
+                     __builtin_amdgcn_readfirstlane(dst + S::kStageA + d * S::kWaves * 1024));
+      lds_dma_b32(rsrc_s, scale_off + static_cast<uint32_t>(kt) * 4u,
+                  __builtin_amdgcn_readfirstlane(stage + S::kStageScales + static_cast<uint32_t>(wave) * 256u));
+    };
+
+    float4_t acc[S::kFragM][S::kFragN];
+    // Every wave is done with the previous tile's LDS.
+    __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
+    workgroup_barrier();
+#pragma unroll
+    for (int s = 0; s < S::STAGES - 1; ++s)
+      if (s < KT) issue(s);
+#pragma unroll
+    for (int i = 0; i < S::kFragM; ++i)
+#pragma unroll
+      for (int j = 0; j < S::kFragN; ++j) acc[i][j] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+
+    for (int kt = 0; kt < KT; ++kt) {
+      // K tile kt has landed (for every wave, past the barrier), and every
+      // wave has read all of K tile kt - 1, whose stage is filled next.
+      wait_younger<S::kPerStage, S::STAGES - 2>(min(KT - 1 - kt, S::STAGES - 2));
+      __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
+      workgroup_barrier();
+      if (kt + S::STAGES - 1 < KT) issue(kt + S::STAGES - 1);
+      const char *stage = smem + (kt % S::STAGES) * S::kStageBytes;
+      int8_v fa[S::kFragM];
+      float sa[S::kFragM];
+      const float sb0 = *reinterpret_cast<const float *>(stage + sb_base);
+#pragma unroll
+      for (int i = 0; i < S::kFragM; ++i) {
+        const char *row = stage + a_base + i * 16 * S::kRowBytes;
+        fa[i] = join(*reinterpret_cast<const int4_t *>(row + piece0), *reinterpret_cast<const int4_t *>(row + piece1));
+        sa[i] = *reinterpret_cast<const float *>(stage + sa_base + i * 64);
+        if constexpr (SB != 1) sa[i] *= sb0;
+      }
+#pragma unroll
+      for (int j = 0; j < S::kFragN; ++j) {
+        const char *row = stage + b_base + j * 16 * S::kRowBytes;
+        const int8_v fb =
+            join(*reinterpret_cast<const int4_t *>(row + piece0), *reinterpret_cast<const int4_t *>(row + piece1));
+        float4_t sb{1.0f, 1.0f, 1.0f, 1.0f};
+        if constexpr (SB == 1) sb = *reinterpret_cast<const float4_t *>(stage + sb_base + j * 64);
+#pragma unroll
+        for (int i = 0; i < S::kFragM; ++i) {
+          const float4_t p = mfma_fp8(fb, fa[i], float4_t{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            acc[i][j][e] = __builtin_fmaf(p[e], SB == 1 ? sa[i] * sb[e] : sa[i], acc[i][j][e]);
+        }
+      }
+    }
+
+    // ---- epilogue ------------------------------------------------------------
+    __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
+    workgroup_barrier();  // every wave is done reading the ring
+    const uint32_t stage_base = static_cast<uint32_t>(wave * S::kWaveM * S::kStagePitch);
+#pragma unroll
+    for (int i = 0; i < S::kFragM; ++i) {
+#pragma unroll
+      for (int j = 0; j < S::kFragN; ++j) {
+        half4_t h;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[e] = round_out<OUT>(acc[i][j][e]);
+        *reinterpret_cast<half4_t *>(smem + stage_base + (i * 16 + frag_row) * S::kStagePitch +
+                                     (j * 16 + frag_kgrp * 4) * 2) = h;
+      }
+    }
+    constexpr int kRowChunks = S::kWaveN / 8;
+    constexpr int kRowsPerPass = 64 / kRowChunks;
+    static_assert(64 % kRowChunks == 0, "lanes per staged row");
+    const int chunk = lane % kRowChunks;
+    const int n = n0 + wn * S::kWaveN + chunk * 8;
+#pragma unroll 4
+    for (int r0 = 0; r0 < S::kWaveM; r0 += kRowsPerPass) {
+      const int r = r0 + lane / kRowChunks;
+      const half8_t v = *reinterpret_cast<const half8_t *>(smem + stage_base + r * S::kStagePitch + chunk * 16);
+      const int m = wm * S::kWaveM + r;
+      if (m < rows) {
+        _Float16 *dst = reinterpret_cast<_Float16 *>(a.D) + (static_cast<int64_t>(g.row) + m) * a.N + n;
+        if (a.vec16 && n + 8 <= a.N) {
+          __builtin_nontemporal_store(v, reinterpret_cast<half8_t *>(dst));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (n + e < a.N) dst[e] = v[e];
+        }
+      }
+    }
+  }
+}
+
+using Fp8Tile256 = Fp8Shape<256, 256, 4, 2, 2>;
+using Fp8Tile128 = Fp8Shape<128, 128, 2, 2, 2>;
+
+template <class S, int OUT, bool GROUPED, int SB>
+hipError_t launch_shape(Fp8Args a, int num_cus, hipStream_t stream) {
+  a.tiles_n = (a.N + S::BN - 1) / S::BN;
+  a.vec16 = a.N % 8 == 0 && reinterpret_cast<uintptr_t>(a.D) % 16 == 0;
+  const int64_t units = GROUPED ? unit_bound(a.M, a.E, S::BM) : (a.M + S::BM - 1) / S::BM;
+  const int64_t tiles = units * a.tiles_n;
+  // Workgroups that fit the CUs at once: by LDS, and two waves to a SIMD.
+  constexpr int kLds = S::kLdsBytes + (GROUPED ? static_cast<int>(sizeof(GroupTable)) : 0);
+  constexpr int kByLds = 160 * 1024 / kLds, kByWaves = 8 / S::kWaves;
+  constexpr int kPerCu = kByLds < kByWaves ? kByLds : kByWaves;
+  static_assert(kPerCu >= 1, "a workgroup fits a CU");
+  const int64_t fit = static_cast<int64_t>(num_cus) * kPerCu;
+  const dim3 grid(static_cast<unsigned>(tiles < fit ? tiles : fit));
+  hipLaunchKernelGGL((fp8_gemm_kernel<S, OUT, GROUPED, SB>), grid, dim3(S::kThreads), 0, stream, a);
+  return hipGetLastError();
+}
+
+// 256x256 tiles when they give most CUs one (groups: when they are expected to).
+bool use_tile256(bool grouped, int64_t M, int64_t N, int64_t E, int num_cus) {
+  const int64_t some = E < M ? E : M;
+  const int64_t units = grouped ? M / 256 + (some + 1) / 2 : (M + 255) / 256;
+  return units * ((N + 255) / 256) >= num_cus * 3 / 4;
+}
+
+template <int OUT, bool GROUPED, int SB>
+hipError_t launch_tile(const Fp8Args &a, int num_cus, hipStream_t stream) {
+  if (use_tile256(GROUPED, a.M, a.N, a.E, num_cus)) return launch_shape<Fp8Tile256, OUT, GROUPED, SB>(a, num_cus, stream);
+  return launch_shape<Fp8Tile128, OUT, GROUPED, SB>(a, num_cus, stream);
+}
+
+}  // namespace
+
+hipError_t launch_gemm_fp8(int out, const void *A, const float *sa, const void *B, const float *sb, int sb_rows, void *D,
+                           int M, int N, int K, int num_cus, hipStream_t stream) {
+  const Fp8Args a{static_cast<const uint8_t *>(A), static_cast<const uint8_t *>(B), sa, sb, nullptr,
+                  static_cast<uint16_t *>(D), M, N, K, 1, 0, 0};
+  if (sb_rows == 1)
+    return out == kBF16 ? launch_tile<kBF16, false, 1>(a, num_cus, stream) : launch_tile<kF16, false, 1>(a, num_cus, stream);
+  return out == kBF16 ? launch_tile<kBF16, false, kScaleBlock>(a, num_cus, stream)
+                      : launch_tile<kF16, false, kScaleBlock>(a, num_cus, stream);
+}
+
+hipError_t launch_grouped_fp8(int out, const void *X, const float *sx, const void *W, const float *sw, const int *offsets,
+                              void *D, int T, int N, int K, int E, int num_cus, hipStream_t stream) {
+  const Fp8Args a{static_cast<const uint8_t *>(X), static_cast<const uint8_t *>(W), sx, sw, offsets,
+                  static_cast<uint16_t *>(D), T, N, K, E, 0, 0};
+  return out == kBF16 ? launch_tile<kBF16, true, kScaleBlock>(a, num_cus, stream)
+                      : launch_tile<kF16, true, kScaleBlock>(a, num_cus, stream);
+}
+
+void fp8_tile(bool grouped, int64_t M, int64_t N, int64_t E, int num_cus, int *rows, int *cols) {
+  *rows = *cols = use_tile256(grouped, M, N, E, num_cus) ? 256 : 128;
+}
+
+}  // namespace gt

@@ -1,0 +1,164 @@
+// groups.hpp -- which rows of which group a workgroup of a grouped product
+// computes.
+//
+// A grouped product has T rows sorted by group and an array offsets[E + 1] in
+// device memory: group e owns rows offsets[e] .. offsets[e + 1] - 1.  A
+// kernel cuts every group's rows into blocks of `rows` ("units"), counted
+// group by group; the number of units is known on the device only, so the
+// host launches unit_bound() of them and those past the last return at once.
+//
+// The offsets are not read by the host (that would need a synchronisation),
+// so they are made safe where they are read: a group's rows are
+// [begin, end) with begin = offsets[e] clamped to [0, T] and end =
+// offsets[e + 1] clamped to [begin, T].  No value of offsets lets a kernel
+// read or write outside the T rows.  (With offsets that are not
+// non-decreasing the units may outnumber the bound, and then the last ones
+// are not computed.)
+#pragma once
+
+#include <stdint.h>
+
+#include "tile_order.hpp"  // GT_HD
+
+namespace gt {
+
+// Most groups of a grouped product: the tiled kernels keep a table of the
+// groups in LDS.
+constexpr int kMaxGroups = 1024;
+
+struct GroupRows {
+  int begin;
+  int end;
+};
+
+GT_HD inline GroupRows group_rows(int first, int next, int T) {
+  GroupRows g;
+  g.begin = first < 0 ? 0 : (first > T ? T : first);
+  g.end = next < g.begin ? g.begin : (next > T ? T : next);
+  return g;
+}
+
+// No more units than this for T rows in E groups: every group's last unit may
+// be short, and no more groups than rows have any.
+GT_HD inline int64_t unit_bound(int64_t T, int64_t E, int64_t rows) {
+  const int64_t some = E < T ? E : T;
+  return (T - some) / rows + some;
+}
+
+// Rows of a unit when the groups are streamed (stream.hip), by the mean rows
+// of a group, or 0 for the tiled kernels.
+inline int grouped_stream_rows(int64_t T, int64_t N, int64_t E) {
+  const int64_t mean = (T + E - 1) / E;
+  const int rows = mean <= 8 ? 16 : mean <= 16 ? 32 : mean <= 32 ? 64 : 0;
+  // A grid's threads are counted in 32 bits.
+  if (rows != 0 && unit_bound(T, E, rows) * ((N + 15) / 16) >= (int64_t{1} << 22)) return 0;
+  return rows;
+}
+
+}  // namespace gt
+
+#if defined(__HIPCC__)
+namespace gt {
+
+struct GroupUnit {
+  int group;
+  int row;  // first row of the unit
+  int end;  // end of its group's rows
+};
+
+// Inclusive sum over the lanes of a wave.
+__device__ inline int wave_scan(int v) {
+  const int lane = static_cast<int>(threadIdx.x & 63);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int up = __shfl_up(v, d);
+    if (lane >= d) v += up;
+  }
+  return v;
+}
+
+// Unit `u` of the groups cut into `rows` rows each; false past the last unit.
+// Every wave of a workgroup works it out for itself (one read of the offsets
+// from the caches for every 256 groups, and a scan): cheaper for a short
+// kernel than a launch of its own or a barrier.  u is wave-uniform, and all
+// 64 lanes must be active.
+__device__ inline bool find_unit(const int *__restrict__ offsets, int E, int T, int rows, int u, GroupUnit *out) {
+  constexpr int kAhead = 4;
+  const int lane = static_cast<int>(threadIdx.x & 63);
+  int before = 0;
+  for (int e0 = 0; e0 < E; e0 += 64 * kAhead) {
+    int first[kAhead], next[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int e = e0 + 64 * j + lane;
+      first[j] = e < E ? offsets[e] : T;  // groups past the last are empty
+      next[j] = e < E ? offsets[e + 1] : T;
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const GroupRows g = group_rows(first[j], next[j], T);
+      const int n = (g.end - g.begin + rows - 1) / rows;
+      const int upto = before + wave_scan(n);
+      const uint64_t past = __ballot(upto > u);
+      if (past != 0) {
+        const int l = __builtin_ctzll(past);
+        const int at = u - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(n, l));
+        out->group = e0 + 64 * j + l;
+        out->row = __builtin_amdgcn_readlane(g.begin, l) + at * rows;
+        out->end = __builtin_amdgcn_readlane(g.end, l);
+        return true;
+      }
+      before = __builtin_amdgcn_readlane(upto, 63);
+    }
+  }
+  return false;
+}
+
+// The groups' units as a table in LDS, for persistent kernels that look up
+// one unit after another.
+struct GroupTable {
+  int upto[kMaxGroups];   // units of groups 0 .. e
+  int begin[kMaxGroups];  // rows of group e
+  int end[kMaxGroups];
+};
+
+// Fills the table (the first wave of the workgroup; the caller places a
+// barrier before the first use).
+__device__ inline void build_group_table(GroupTable *table, const int *__restrict__ offsets, int E, int T, int rows) {
+  if (threadIdx.x >= 64) return;
+  const int lane = static_cast<int>(threadIdx.x);
+  int before = 0;
+  for (int e0 = 0; e0 < E; e0 += 64) {
+    const int e = e0 + lane;
+    const GroupRows g = group_rows(e < E ? offsets[e] : T, e < E ? offsets[e + 1] : T, T);
+    const int upto = before + wave_scan((g.end - g.begin + rows - 1) / rows);
+    if (e < E) {
+      table->upto[e] = upto;
+      table->begin[e] = g.begin;
+      table->end[e] = g.end;
+    }
+    before = __builtin_amdgcn_readlane(upto, 63);
+  }
+}
+
+// Unit `u` of the table's units (u is wave-uniform and below upto[E - 1]).
+__device__ inline GroupUnit table_unit(const GroupTable *table, int E, int rows, int u) {
+  const int lane = static_cast<int>(threadIdx.x & 63);
+  int e = 0;
+  for (int e0 = 0; e0 < E; e0 += 64) {
+    const uint64_t past = __ballot(e0 + lane < E && table->upto[e0 + lane < E ? e0 + lane : 0] > u);
+    if (past != 0) {
+      e = e0 + __builtin_ctzll(past);
+      break;
+    }
+  }
+  const int before = e > 0 ? table->upto[e - 1] : 0;
+  GroupUnit g;
+  g.group = __builtin_amdgcn_readfirstlane(e);
+  g.row = __builtin_amdgcn_readfirstlane(table->begin[e] + (u - before) * rows);
+  g.end = __builtin_amdgcn_readfirstlane(table->end[e]);
+  return g;
+}
+
+}  // namespace gt
+#endif

@@ -322,4 +322,39 @@ hipError_t launch_gemm_skinny_bf16(const void *A, const void *B, void *D, int M,
                                    hipStream_t stream);
 hipError_t launch_gemv_bf16(const void *x, const void *W, void *y, int N, int K, int num_cus, hipStream_t stream);
 
+// ---- block-scaled 8-bit operands and products by expert --------------------
+// quantize.hip: scale and e4m3 numbers of 1 x 128 and 128 x 128 blocks of x
+// (dtype kF16 or kBF16).
+hipError_t launch_quantize_rows(int dtype, const void *x, void *q, float *scale, int64_t M, int K, hipStream_t stream);
+hipError_t launch_quantize_tiles(int dtype, const void *x, void *q, float *scale, int E, int N, int K,
+                                 hipStream_t stream);
+// stream.hip: few rows against weights read once; `out` and dtype kF16 or
+// kBF16, `rows` the rows of a unit (16, 32 or 64).
+hipError_t launch_stream_fp8(int out, const void *x, const float *sx, const void *w, const float *sw, int w_scale_rows,
+                             void *d, int M, int N, int K, hipStream_t stream);
+hipError_t launch_stream_grouped(int dtype, const void *x, const void *w, const int *offsets, void *d, int T, int N,
+                                 int K, int E, int rows, hipStream_t stream);
+hipError_t launch_stream_grouped_fp8(int out, const void *x, const float *sx, const void *w, const float *sw,
+                                     const int *offsets, void *d, int T, int N, int K, int E, int rows,
+                                     hipStream_t stream);
+// gemm_fp8_* streams B for at most this many rows of A.
+constexpr int64_t kFp8StreamRows = 64;
+// fp8_gemm.hip: tiled products of e4m3 operands (K > 0).
+hipError_t launch_gemm_fp8(int out, const void *A, const float *sa, const void *B, const float *sb, int sb_rows, void *D,
+                           int M, int N, int K, int num_cus, hipStream_t stream);
+hipError_t launch_grouped_fp8(int out, const void *X, const float *sx, const void *W, const float *sw, const int *offsets,
+                              void *D, int T, int N, int K, int E, int num_cus, hipStream_t stream);
+// grouped_*.hip: tiled products by expert in 16 bits: A, B and D are X, W and
+// D; dY, W and dX; dY, X and dW.
+hipError_t launch_grouped_forward(int dtype, const void *A, const void *B, const int *offsets, void *D, int T, int N, int K,
+                                  int E, int num_cus, hipStream_t stream);
+hipError_t launch_grouped_dgrad(int dtype, const void *A, const void *B, const int *offsets, void *D, int T, int N, int K,
+                                int E, int num_cus, hipStream_t stream);
+hipError_t launch_grouped_wgrad(int dtype, const void *A, const void *B, const int *offsets, void *D, int T, int N, int K,
+                                int E, int num_cus, hipStream_t stream);
+// The output tile of the tiled grouped kernels: op 0 forward, 1 dgrad, 2
+// wgrad, 3 e4m3 forward.
+void grouped_tile(int op, int64_t T, int64_t N, int64_t K, int64_t E, int num_cus, int *rows, int *cols);
+void fp8_tile(bool grouped, int64_t M, int64_t N, int64_t E, int num_cus, int *rows, int *cols);
+
 }  // namespace gt
