@@ -14,8 +14,10 @@ input (quantisers) or of the output.
 from __future__ import annotations
 
 import torch
+from torch import Tensor
+from torch._C import _cuda_getCurrentRawStream as _raw_stream
 
-from . import _check, _require, _stream_handle, load_library
+from . import _check, _require, load_library
 
 __all__ = [f"{name}_{fmt}" for name in ("quantize_fp8_rows", "quantize_fp8_tiles", "gemm_fp8", "gemm_grouped",
                                         "gemm_grouped_dgrad", "gemm_grouped_wgrad", "gemm_grouped_fp8")
@@ -29,44 +31,64 @@ def _blocks(n: int) -> int:
     return (n + BLOCK - 1) // BLOCK
 
 
-def _shaped(t, name, dtype, shape, device):
-    """t is a contiguous tensor of this type and shape on `device`."""
+# A call's checks cost as much time as its launch if they are made one by one
+# through several functions; each tensor is tested in one expression, and the
+# reason is looked for only when that fails.
+def _shaped(t, name, dtype, shape, dev):
+    """t is a contiguous tensor of this type and shape on device number `dev`."""
+    if (isinstance(t, Tensor) and t.dtype is dtype and t.get_device() == dev and t.shape == shape
+            and t.is_contiguous() and dev >= 0):
+        return
     _require(t, name, len(shape), dtype)
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    raise ValueError(f"{name} must be on device {dev}, got {t.device}")
 
 
-def _output(t, name, dtype, shape, device):
+def _first(t, name, dtype, ndim):
+    """The device number of a call's first tensor."""
+    if not (isinstance(t, Tensor) and t.dtype is dtype and t.dim() == ndim and t.is_contiguous() and t.is_cuda):
+        _require(t, name, ndim, dtype)
+    return t.get_device()
+
+
+def _output(t, name, dtype, shape, dev):
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _shaped(t, name, dtype, shape, device)
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+    _shaped(t, name, dtype, shape, dev)
     return t
 
 
-def _offsets(offsets, device):
-    _require(offsets, "offsets", 1, torch.int32)
-    if offsets.device != device:
-        raise ValueError(f"offsets must be on {device}, got {offsets.device}")
-    if offsets.shape[0] < 1:
+def _offsets(offsets, dev):
+    if _first(offsets, "offsets", torch.int32, 1) != dev:
+        raise ValueError(f"offsets must be on device {dev}, got {offsets.device}")
+    groups = offsets.shape[0] - 1
+    if groups < 0:
         raise ValueError("offsets must have one element more than there are groups")
-    return offsets.shape[0] - 1
+    return groups
 
 
-def _run(like, stream, call, *args):
-    s = _stream_handle(like, stream)
-    with torch.cuda.device(like.device):
-        _check(call(*args, s))
+def _run(dev, stream, call, *args):
+    if stream is None:
+        s = _raw_stream(dev)
+    else:
+        s = stream if isinstance(stream, int) else stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        status = call(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            status = call(*args, s)
+    if status != 0:
+        _check(status)
 
 
 # ---- quantisers ----------------------------------------------------------------
 def _quantize_rows(x, q, scale, stream, dtype, call):
-    _require(x, "x", 2, dtype)
+    dev = _first(x, "x", dtype, 2)
     M, K = x.shape
-    q = _output(q, "q", FP8, (M, K), x.device)
-    scale = _output(scale, "scale", torch.float32, (M, _blocks(K)), x.device)
-    _run(x, stream, call, x.data_ptr(), q.data_ptr(), scale.data_ptr(), M, K)
+    q = _output(q, "q", FP8, (M, K), dev)
+    scale = _output(scale, "scale", torch.float32, (M, _blocks(K)), dev)
+    _run(dev, stream, call, x.data_ptr(), q.data_ptr(), scale.data_ptr(), M, K)
     return q, scale
 
 
@@ -84,12 +106,11 @@ def quantize_fp8_rows_bf16(x, q=None, scale=None, stream=None):
 
 def _quantize_tiles(x, q, scale, stream, dtype, call):
     many = isinstance(x, torch.Tensor) and x.dim() == 3
-    _require(x, "x", 3 if many else 2, dtype)
-    lead = tuple(x.shape[:-2])
-    N, K = x.shape[-2:]
-    q = _output(q, "q", FP8, tuple(x.shape), x.device)
-    scale = _output(scale, "scale", torch.float32, (*lead, _blocks(N), _blocks(K)), x.device)
-    _run(x, stream, call, x.data_ptr(), q.data_ptr(), scale.data_ptr(), lead[0] if many else 1, N, K)
+    dev = _first(x, "x", dtype, 3 if many else 2)
+    *lead, N, K = x.shape
+    q = _output(q, "q", FP8, (*lead, N, K), dev)
+    scale = _output(scale, "scale", torch.float32, (*lead, _blocks(N), _blocks(K)), dev)
+    _run(dev, stream, call, x.data_ptr(), q.data_ptr(), scale.data_ptr(), lead[0] if many else 1, N, K)
     return q, scale
 
 
@@ -106,20 +127,17 @@ def quantize_fp8_tiles_bf16(x, q=None, scale=None, stream=None):
 
 # ---- products --------------------------------------------------------------------
 def _gemm_fp8(A, scale_A, B, scale_B, D, stream, dtype, call):
-    _require(A, "A", 2, FP8)
-    dev = A.device
-    _require(B, "B", 2, FP8)
+    dev = _first(A, "A", FP8, 2)
+    if _first(B, "B", FP8, 2) != dev:
+        raise ValueError("A and B must be on the same device")
     M, K = A.shape
     N, K2 = B.shape
     if K != K2:
         raise ValueError(f"K mismatch: A is {tuple(A.shape)}, B is {tuple(B.shape)}")
-    if B.device != dev:
-        raise ValueError("A and B must be on the same device")
     kb = _blocks(K)
     _shaped(scale_A, "scale_A", torch.float32, (M, kb), dev)
-    _require(scale_B, "scale_B", 2, torch.float32)
-    if scale_B.device != dev:
-        raise ValueError(f"scale_B must be on {dev}, got {scale_B.device}")
+    if _first(scale_B, "scale_B", torch.float32, 2) != dev:
+        raise ValueError(f"scale_B must be on device {dev}, got {scale_B.device}")
     if scale_B.shape == (_blocks(N), kb):
         rows = BLOCK
     elif scale_B.shape == (N, kb):
@@ -128,7 +146,8 @@ def _gemm_fp8(A, scale_A, B, scale_B, D, stream, dtype, call):
         raise ValueError(f"scale_B must be {[_blocks(N), kb]} (128 x 128 blocks) or {[N, kb]} (1 x 128), "
                          f"got {tuple(scale_B.shape)}")
     D = _output(D, "D", dtype, (M, N), dev)
-    _run(A, stream, call, A.data_ptr(), scale_A.data_ptr(), B.data_ptr(), scale_B.data_ptr(), D.data_ptr(), M, N, K, rows)
+    _run(dev, stream, call, A.data_ptr(), scale_A.data_ptr(), B.data_ptr(), scale_B.data_ptr(), D.data_ptr(), M, N, K,
+         rows)
     return D
 
 
@@ -148,21 +167,25 @@ def gemm_fp8_bf16(A, scale_A, B, scale_B, D=None, stream=None):
     return _gemm_fp8(A, scale_A, B, scale_B, D, stream, torch.bfloat16, load_library().gemm_fp8_bf16)
 
 
-def _groups_of(W, name, E):
-    if W.shape[0] != E:
-        raise ValueError(f"{name} has {W.shape[0]} groups, offsets {E}")
+def _weights(W, dtype, E, dev):
+    """The [N, K] of one group's weights."""
+    if _first(W, "W", dtype, 3) != dev:
+        raise ValueError(f"W must be on device {dev}, got {W.device}")
+    groups, N, K = W.shape
+    if groups != E:
+        raise ValueError(f"W has {groups} groups, offsets {E}")
+    return N, K
 
 
 def _grouped(X, W, offsets, D, stream, dtype, call):
-    _require(X, "X", 2, dtype)
-    _require(W, "W", 3, dtype)
-    E = _offsets(offsets, X.device)
+    dev = _first(X, "X", dtype, 2)
+    E = _offsets(offsets, dev)
     T, K = X.shape
-    _groups_of(W, "W", E)
-    N = W.shape[1]
-    _shaped(W, "W", dtype, (E, N, K), X.device)
-    D = _output(D, "D", dtype, (T, N), X.device)
-    _run(X, stream, call, X.data_ptr(), W.data_ptr(), offsets.data_ptr(), D.data_ptr(), T, N, K, E)
+    N, K2 = _weights(W, dtype, E, dev)
+    if K != K2:
+        raise ValueError(f"K mismatch: X is {tuple(X.shape)}, W is {tuple(W.shape)}")
+    D = _output(D, "D", dtype, (T, N), dev)
+    _run(dev, stream, call, X.data_ptr(), W.data_ptr(), offsets.data_ptr(), D.data_ptr(), T, N, K, E)
     return D
 
 
@@ -181,15 +204,14 @@ def gemm_grouped_bf16(X, W, offsets, D=None, stream=None):
 
 
 def _grouped_dgrad(dY, W, offsets, dX, stream, dtype, call):
-    _require(dY, "dY", 2, dtype)
-    _require(W, "W", 3, dtype)
-    E = _offsets(offsets, dY.device)
+    dev = _first(dY, "dY", dtype, 2)
+    E = _offsets(offsets, dev)
     T, N = dY.shape
-    _groups_of(W, "W", E)
-    K = W.shape[2]
-    _shaped(W, "W", dtype, (E, N, K), dY.device)
-    dX = _output(dX, "dX", dtype, (T, K), dY.device)
-    _run(dY, stream, call, dY.data_ptr(), W.data_ptr(), offsets.data_ptr(), dX.data_ptr(), T, N, K, E)
+    N2, K = _weights(W, dtype, E, dev)
+    if N != N2:
+        raise ValueError(f"N mismatch: dY is {tuple(dY.shape)}, W is {tuple(W.shape)}")
+    dX = _output(dX, "dX", dtype, (T, K), dev)
+    _run(dev, stream, call, dY.data_ptr(), W.data_ptr(), offsets.data_ptr(), dX.data_ptr(), T, N, K, E)
     return dX
 
 
@@ -205,14 +227,16 @@ def gemm_grouped_dgrad_bf16(dY, W, offsets, dX=None, stream=None):
 
 
 def _grouped_wgrad(dY, X, offsets, dW, stream, dtype, call):
-    _require(dY, "dY", 2, dtype)
-    E = _offsets(offsets, dY.device)
+    dev = _first(dY, "dY", dtype, 2)
+    E = _offsets(offsets, dev)
     T, N = dY.shape
-    _require(X, "X", 2, dtype)
-    K = X.shape[1]
-    _shaped(X, "X", dtype, (T, K), dY.device)
-    dW = _output(dW, "dW", dtype, (E, N, K), dY.device)
-    _run(dY, stream, call, dY.data_ptr(), X.data_ptr(), offsets.data_ptr(), dW.data_ptr(), T, N, K, E)
+    if _first(X, "X", dtype, 2) != dev:
+        raise ValueError(f"X must be on device {dev}, got {X.device}")
+    T2, K = X.shape
+    if T != T2:
+        raise ValueError(f"T mismatch: dY is {tuple(dY.shape)}, X is {tuple(X.shape)}")
+    dW = _output(dW, "dW", dtype, (E, N, K), dev)
+    _run(dev, stream, call, dY.data_ptr(), X.data_ptr(), offsets.data_ptr(), dW.data_ptr(), T, N, K, E)
     return dW
 
 
@@ -228,17 +252,17 @@ def gemm_grouped_wgrad_bf16(dY, X, offsets, dW=None, stream=None):
 
 
 def _grouped_fp8(X, scale_X, W, scale_W, offsets, D, stream, dtype, call):
-    _require(X, "X", 2, FP8)
-    _require(W, "W", 3, FP8)
-    E = _offsets(offsets, X.device)
+    dev = _first(X, "X", FP8, 2)
+    E = _offsets(offsets, dev)
     T, K = X.shape
-    _groups_of(W, "W", E)
-    N = W.shape[1]
-    _shaped(W, "W", FP8, (E, N, K), X.device)
-    _shaped(scale_X, "scale_X", torch.float32, (T, _blocks(K)), X.device)
-    _shaped(scale_W, "scale_W", torch.float32, (E, _blocks(N), _blocks(K)), X.device)
-    D = _output(D, "D", dtype, (T, N), X.device)
-    _run(X, stream, call, X.data_ptr(), scale_X.data_ptr(), W.data_ptr(), scale_W.data_ptr(), offsets.data_ptr(),
+    N, K2 = _weights(W, FP8, E, dev)
+    if K != K2:
+        raise ValueError(f"K mismatch: X is {tuple(X.shape)}, W is {tuple(W.shape)}")
+    kb = _blocks(K)
+    _shaped(scale_X, "scale_X", torch.float32, (T, kb), dev)
+    _shaped(scale_W, "scale_W", torch.float32, (E, _blocks(N), kb), dev)
+    D = _output(D, "D", dtype, (T, N), dev)
+    _run(dev, stream, call, X.data_ptr(), scale_X.data_ptr(), W.data_ptr(), scale_W.data_ptr(), offsets.data_ptr(),
          D.data_ptr(), T, N, K, E)
     return D
 
