@@ -453,10 +453,10 @@ int run_gemm_fp8(const void *A, const float *sa, const void *B, const float *sb,
     return GEMVTILE_ERR_UNSUPPORTED;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int m = static_cast<int>(M), n = static_cast<int>(N), k = static_cast<int>(K), r = static_cast<int>(sb_rows);
-  if (M <= gt::kFp8StreamRows) return to_status(gt::launch_stream_fp8(out, A, sa, B, sb, r, D, m, n, k, s));
   int cus = 0;
   const int st = current_cu_count(&cus);
   if (st != GEMVTILE_OK) return st;
+  if (M <= gt::kFp8StreamRows) return to_status(gt::launch_stream_fp8(out, A, sa, B, sb, r, D, m, n, k, cus, s));
   return to_status(gt::launch_gemm_fp8(out, A, sa, B, sb, r, D, m, n, k, cus, s));
 }
 
@@ -489,13 +489,13 @@ int run_grouped(int op, const void *A, const float *sa, const void *B, const flo
     return GEMVTILE_ERR_UNSUPPORTED;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int t = static_cast<int>(T), n = static_cast<int>(N), k = static_cast<int>(K), e = static_cast<int>(E);
-  const int rows = op == kOpForward || op == kOpFp8 ? gt::grouped_stream_rows(T, N, E) : 0;
-  if (rows != 0)
-    return to_status(op == kOpFp8 ? gt::launch_stream_grouped_fp8(dtype, A, sa, B, sb, offsets, D, t, n, k, e, rows, s)
-                                  : gt::launch_stream_grouped(dtype, A, B, offsets, D, t, n, k, e, rows, s));
   int cus = 0;
   st = current_cu_count(&cus);
   if (st != GEMVTILE_OK) return st;
+  const int rows = op == kOpForward || op == kOpFp8 ? gt::grouped_stream_rows(T, N, E) : 0;
+  if (rows != 0)
+    return to_status(op == kOpFp8 ? gt::launch_stream_grouped_fp8(dtype, A, sa, B, sb, offsets, D, t, n, k, e, rows, cus, s)
+                                  : gt::launch_stream_grouped(dtype, A, B, offsets, D, t, n, k, e, rows, cus, s));
   switch (op) {
     case kOpDgrad: return to_status(gt::launch_grouped_dgrad(dtype, A, B, offsets, D, t, n, k, e, cus, s));
     case kOpWgrad: return to_status(gt::launch_grouped_wgrad(dtype, A, B, offsets, D, t, n, k, e, cus, s));

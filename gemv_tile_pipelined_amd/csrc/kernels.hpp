@@ -331,12 +331,12 @@ hipError_t launch_quantize_tiles(int dtype, const void *x, void *q, float *scale
 // stream.hip: few rows against weights read once; `out` and dtype kF16 or
 // kBF16, `rows` the rows of a unit (16, 32 or 64).
 hipError_t launch_stream_fp8(int out, const void *x, const float *sx, const void *w, const float *sw, int w_scale_rows,
-                             void *d, int M, int N, int K, hipStream_t stream);
+                             void *d, int M, int N, int K, int num_cus, hipStream_t stream);
 hipError_t launch_stream_grouped(int dtype, const void *x, const void *w, const int *offsets, void *d, int T, int N,
-                                 int K, int E, int rows, hipStream_t stream);
+                                 int K, int E, int rows, int num_cus, hipStream_t stream);
 hipError_t launch_stream_grouped_fp8(int out, const void *x, const float *sx, const void *w, const float *sw,
                                      const int *offsets, void *d, int T, int N, int K, int E, int rows,
-                                     hipStream_t stream);
+                                     int num_cus, hipStream_t stream);
 // gemm_fp8_* streams B for at most this many rows of A.
 constexpr int64_t kFp8StreamRows = 64;
 // fp8_gemm.hip: tiled products of e4m3 operands (K > 0).

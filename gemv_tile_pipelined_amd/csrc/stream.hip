@@ -5,8 +5,8 @@
 //   D[t, n] = sum_k x[t, k] W[n, k]                                   16-bit
 //   D[t, n] = sum_b sx[t, b] sw[n / r, b] sum_{k in b} x[t, k] W[n, k]  8-bit
 //
-// Bound by reading W: a workgroup owns 16 rows of W and all of a unit's rows
-// of x (up to 16 QB of them), so each byte of W is read once per unit.  Its
+// Bound by reading W: a workgroup owns 16 or 32 rows of W and all of a unit's
+// rows of x (up to 16 QB of them), so each byte of W is read once per unit.  Its
 // waves split K in steps of 128 bytes of a row, which for 8-bit operands is
 // one scale block: a step is one 16x16x128 MFMA per 16 rows of x (two
 // 16x16x32 of 16-bit numbers), W rows first, so that lane l holds outputs
@@ -30,8 +30,6 @@ namespace gt {
 namespace {
 
 constexpr int kStepBytes = 128;  // bytes of a row per step
-constexpr int kStreamRows = 16;  // rows of W per workgroup
-constexpr int kUnroll = 4;
 
 struct StreamArgs {
   const uint8_t *x, *w;
@@ -40,18 +38,20 @@ struct StreamArgs {
   uint16_t *d;
   int T, N, E;
   int row_bytes;  // of x and W
-  int blocks_n;   // 16-row blocks of W
+  int blocks_n;   // workgroups along W's rows
 };
 
-// IN: kF16, kBF16 (16-bit operands) or kE4m3.  SW: rows of W per scale (128 or 1).
+// IN: kF16, kBF16 (16-bit operands) or kE4m3.  SW: rows of W per scale (128 or
+// 1).  PB, QB: 16-row blocks of W and of x per workgroup.
 constexpr int kE4m3 = 2;
-template <int IN, int OUT, int QB, int WAVES, bool GROUPED, int SW>
+template <int IN, int OUT, int PB, int QB, int WAVES, int UNROLL, bool GROUPED, int SW>
 __global__ void __launch_bounds__(WAVES * 64) stream_kernel(StreamArgs a) {
   constexpr bool kScaled = IN == kE4m3;
-  __shared__ float partial[WAVES][16 * QB][kStreamRows + 1];
+  constexpr int kRows = 16 * PB;
+  __shared__ float partial[WAVES][16 * QB][kRows + 1];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n0 = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.blocks_n)) * kStreamRows;
+  const int n0 = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.blocks_n)) * kRows;
   const int unit = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.blocks_n));
   GroupUnit g{0, unit * 16 * QB, a.T};
   if constexpr (GROUPED) {
@@ -61,75 +61,96 @@ __global__ void __launch_bounds__(WAVES * 64) stream_kernel(StreamArgs a) {
   const uint32_t rb = static_cast<uint32_t>(a.row_bytes);
   const int steps = (a.row_bytes + kStepBytes - 1) / kStepBytes;
 
+  // Byte ranges, so that what lies outside reads as zeros.
+  auto range = [](const void *p, int64_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, static_cast<int>(bytes), 0x00020000);
+  };
+  auto load16 = [](__amdgpu_buffer_rsrc_t r, uint32_t off) {
+    return __builtin_bit_cast(int4_t, __builtin_amdgcn_raw_buffer_load_b128(r, static_cast<int>(off), 0, 0));
+  };
+  const int w_rows = min(kRows, a.N - n0);
   const int64_t w_row = static_cast<int64_t>(g.group) * a.N + n0;
-  const auto rsrc_w = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<uint8_t *>(a.w + w_row * a.row_bytes), 0, static_cast<int>(min(kStreamRows, a.N - n0) * rb), 0x00020000);
-  const auto rsrc_x = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<uint8_t *>(a.x + static_cast<int64_t>(g.row) * a.row_bytes), 0, static_cast<int>(rows * rb), 0x00020000);
+  const auto rsrc_w = range(a.w + w_row * a.row_bytes, static_cast<int64_t>(w_rows) * rb);
+  const auto rsrc_x = range(a.x + static_cast<int64_t>(g.row) * a.row_bytes, static_cast<int64_t>(rows) * rb);
   const int frow = lane & 15;
-  const uint32_t piece = static_cast<uint32_t>(lane >> 4) * 16;
+  const int fgrp = lane >> 4;
+  const uint32_t piece = static_cast<uint32_t>(fgrp) * 16;
   const uint32_t lane_off = static_cast<uint32_t>(frow) * rb + piece;
 
-  // Scales of this lane's rows: rows past the last repeat the last one's (their
-  // sums are zeros, or are not stored).
-  const float *sx[QB];
-  const float *sw[4];
+  // Scales of this lane's rows of x, and of the rows of W of its outputs: 4
+  // steps' at a time, from one 16-byte load (4-byte aligned is enough).
+  __amdgpu_buffer_rsrc_t rsrc_sx, rsrc_sw;
   if constexpr (kScaled) {
-#pragma unroll
-    for (int q = 0; q < QB; ++q) sx[q] = a.sx + static_cast<int64_t>(g.row + min(16 * q + frow, rows - 1)) * steps;
-    if constexpr (SW == 1) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sw[e] = a.sw + static_cast<int64_t>(min(n0 + 4 * (lane >> 4) + e, a.N - 1)) * steps;
-    } else {
-      sw[0] = a.sw + (static_cast<int64_t>(g.group) * ((a.N + kScaleBlock - 1) / kScaleBlock) + n0 / kScaleBlock) * steps;
-    }
+    rsrc_sx = range(a.sx + static_cast<int64_t>(g.row) * steps, static_cast<int64_t>(rows) * steps * 4);
+    const int64_t sw_row = SW == 1 ? w_row
+                                   : static_cast<int64_t>(g.group) * ((a.N + kScaleBlock - 1) / kScaleBlock) + n0 / kScaleBlock;
+    rsrc_sw = range(a.sw + sw_row * steps, static_cast<int64_t>(SW == 1 ? w_rows : 1) * steps * 4);
   }
+  static_assert(UNROLL <= 4, "the scales of one 16-byte load");
 
-  float4_t acc[QB];
+  float4_t acc[PB][QB];
 #pragma unroll
-  for (int q = 0; q < QB; ++q) acc[q] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int s0 = wave * kUnroll; s0 < steps; s0 += WAVES * kUnroll) {
-    int4_t wv[kUnroll][2], xv[kUnroll][QB][2];
-    float sxv[kUnroll][QB], swv[kUnroll][SW == 1 ? 4 : 1];
+  for (int p = 0; p < PB; ++p)
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int q = 0; q < QB; ++q) acc[p][q] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  // Workgroups that run side by side on an XCD (every eighth) start their
+  // waves at different places of K, so that they do not all ask for the same
+  // lines of x at once.
+  const int first = static_cast<int>((static_cast<unsigned>(wave) + (blockIdx.x >> 3)) % WAVES);
+  for (int s0 = first * UNROLL; s0 < steps; s0 += WAVES * UNROLL) {
+    int4_t wv[UNROLL][PB][2], xv[UNROLL][QB][2];
+    float4_t sxv[QB], swv[SW == 1 ? 4 * PB : 1];
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint32_t at = static_cast<uint32_t>(s0 + u) * kStepBytes + 64u * h;
         const uint32_t off = at + piece < rb ? lane_off + at : kOobOffset;
-        wv[u][h] = __builtin_bit_cast(int4_t, __builtin_amdgcn_raw_buffer_load_b128(rsrc_w, off, 0, 0));
 #pragma unroll
-        for (int q = 0; q < QB; ++q)
-          xv[u][q][h] = __builtin_bit_cast(int4_t, __builtin_amdgcn_raw_buffer_load_b128(
-                                                       rsrc_x, at + piece < rb ? off + 16u * q * rb : kOobOffset, 0, 0));
-      }
-      if constexpr (kScaled) {
-        const int b = min(s0 + u, steps - 1);
+        for (int p = 0; p < PB; ++p) wv[u][p][h] = load16(rsrc_w, off + 16u * p * rb);
 #pragma unroll
-        for (int q = 0; q < QB; ++q) sxv[u][q] = sx[q][b];
-#pragma unroll
-        for (int e = 0; e < (SW == 1 ? 4 : 1); ++e) swv[u][e] = sw[e][b];
+        for (int q = 0; q < QB; ++q) xv[u][q][h] = load16(rsrc_x, off + 16u * q * rb);
       }
     }
+    if constexpr (kScaled) {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      if (s0 + u >= steps) break;  // uniform; a step past the end would add zeros
+      for (int q = 0; q < QB; ++q)
+        sxv[q] = __builtin_bit_cast(float4_t, load16(rsrc_sx, static_cast<uint32_t>((16 * q + frow) * steps + s0) * 4u));
+#pragma unroll
+      for (int r = 0; r < (SW == 1 ? 4 * PB : 1); ++r) {
+        const int row = SW == 1 ? 16 * (r / 4) + 4 * fgrp + r % 4 : 0;
+        swv[r] = __builtin_bit_cast(float4_t, load16(rsrc_sw, static_cast<uint32_t>(row * steps + s0) * 4u));
+      }
+    }
+    // Every load of the steps is issued before the first is waited for.
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+      // A step past the end multiplies zeros; its scales, which belong to the
+      // next row, may be anything and count as zero.
+      const bool past = s0 + u >= steps;
 #pragma unroll
       for (int q = 0; q < QB; ++q) {
-        if constexpr (kScaled) {
-          const float4_t p =
-              mfma_fp8(join(wv[u][0], wv[u][1]), join(xv[u][q][0], xv[u][q][1]), float4_t{0.0f, 0.0f, 0.0f, 0.0f});
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[q][e] = __builtin_fmaf(p[e], sxv[u][q] * swv[u][SW == 1 ? e : 0], acc[q][e]);
-        } else {
+        for (int p = 0; p < PB; ++p) {
+          if constexpr (kScaled) {
+            const float4_t v =
+                mfma_fp8(join(wv[u][p][0], wv[u][p][1]), join(xv[u][q][0], xv[u][q][1]), float4_t{0.0f, 0.0f, 0.0f, 0.0f});
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if constexpr (IN == kF16)
-              acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, wv[u][h]),
-                                                              __builtin_bit_cast(half8_t, xv[u][q][h]), acc[q], 0, 0, 0);
-            else
-              acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, wv[u][h]),
-                                                               __builtin_bit_cast(bf16x8_t, xv[u][q][h]), acc[q], 0, 0, 0);
+            for (int e = 0; e < 4; ++e) {
+              const float scale = sxv[q][u] * swv[SW == 1 ? 4 * p + e : 0][u];
+              acc[p][q][e] = __builtin_fmaf(v[e], past ? 0.0f : scale, acc[p][q][e]);
+            }
+          } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if constexpr (IN == kF16)
+                acc[p][q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, wv[u][p][h]),
+                                                                   __builtin_bit_cast(half8_t, xv[u][q][h]), acc[p][q], 0, 0, 0);
+              else
+                acc[p][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, wv[u][p][h]),
+                                                                    __builtin_bit_cast(bf16x8_t, xv[u][q][h]), acc[p][q], 0, 0, 0);
+            }
           }
         }
       }
@@ -137,13 +158,15 @@ __global__ void __launch_bounds__(WAVES * 64) stream_kernel(StreamArgs a) {
   }
 
 #pragma unroll
-  for (int q = 0; q < QB; ++q)
+  for (int p = 0; p < PB; ++p)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) partial[wave][16 * q + frow][4 * (lane >> 4) + e] = acc[q][e];
+    for (int q = 0; q < QB; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) partial[wave][16 * q + frow][16 * p + 4 * fgrp + e] = acc[p][q][e];
   __syncthreads();
-  for (int i = threadIdx.x; i < 16 * QB * kStreamRows; i += WAVES * 64) {
-    const int t = i / kStreamRows, n = i % kStreamRows;
-    if (t >= rows || n0 + n >= a.N) continue;
+  for (int i = threadIdx.x; i < 16 * QB * kRows; i += WAVES * 64) {
+    const int t = i / kRows, n = i % kRows;
+    if (t >= rows || n >= w_rows) continue;
     float sum = 0.0f;
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) sum += partial[w][t][n];
@@ -151,62 +174,78 @@ __global__ void __launch_bounds__(WAVES * 64) stream_kernel(StreamArgs a) {
   }
 }
 
-template <int IN, int OUT, int QB, int WAVES, bool GROUPED, int SW>
-hipError_t launch_one(const StreamArgs &a, int64_t units, hipStream_t stream) {
+template <int IN, int OUT, int PB, int QB, int WAVES, int UNROLL, bool GROUPED, int SW>
+hipError_t launch_one(StreamArgs a, int64_t units, hipStream_t stream) {
+  a.blocks_n = (a.N + 16 * PB - 1) / (16 * PB);
   const dim3 grid(static_cast<unsigned>(units * a.blocks_n));
-  hipLaunchKernelGGL((stream_kernel<IN, OUT, QB, WAVES, GROUPED, SW>), grid, dim3(WAVES * 64), 0, stream, a);
+  hipLaunchKernelGGL((stream_kernel<IN, OUT, PB, QB, WAVES, UNROLL, GROUPED, SW>), grid, dim3(WAVES * 64), 0, stream, a);
   return hipGetLastError();
 }
 
-// 4 steps or more for a wave, as far as 4 to 16 waves allow; 16 waves of 64
-// rows would not leave two workgroups their LDS.
+// The launch shape.  Measured (MI355X, 8 bits unless said; PB x WAVES x
+// UNROLL):
+//  * x is read once per workgroup, so 32 rows of W pay when x has more than a
+//    few rows and every CU still gets a workgroup (27x8192x4096: 1x8x4 12.7 us,
+//    2x8x4 9.8; 1x32768x4096 24.1 and 25.4; 32x2048x8192 14.0 and 18.2).
+//  * Many groups make many workgroups of little work: small ones with few
+//    loads in flight each, so that more of them share a CU (64 rows in 64
+//    groups x 2048 x 4096: 1x8x4 84 us, 2x8x4 67, 2x4x2 65; 16-bit 32 rows x
+//    2048 x 2048 40.9, 41.8 and 38.7).
+//  * 2 steps in flight instead of 4 where that leaves the slowest wave fewer
+//    steps (1x4096x14336, 112 steps: 12.1 -> 10.7 us).
 template <int IN, int OUT, int QB, bool GROUPED, int SW>
-hipError_t launch_waves(const StreamArgs &a, int64_t units, hipStream_t stream) {
+hipError_t launch_waves(const StreamArgs &a, int64_t units, int num_cus, hipStream_t stream) {
   const int steps = (a.row_bytes + kStepBytes - 1) / kStepBytes;
-  if (steps >= 16 * kUnroll && QB < 4) return launch_one<IN, OUT, QB, 16, GROUPED, SW>(a, units, stream);
-  if (steps >= 8 * kUnroll) return launch_one<IN, OUT, QB, 8, GROUPED, SW>(a, units, stream);
-  return launch_one<IN, OUT, QB, 4, GROUPED, SW>(a, units, stream);
+  const bool two = (steps + 15) / 16 * 2 < (steps + 31) / 32 * 4;
+  const int64_t wide = units * ((a.N + 31) / 32);  // workgroups of 32 rows of W
+  if (GROUPED ? wide >= 2 * num_cus : a.T > 4 && steps < 32 && wide >= num_cus)
+    return launch_one<IN, OUT, 2, QB, 4, 2, GROUPED, SW>(a, units, stream);
+  if (!GROUPED && a.T > 4 && wide >= num_cus)
+    return two ? launch_one<IN, OUT, 2, QB, 8, 2, GROUPED, SW>(a, units, stream)
+               : launch_one<IN, OUT, 2, QB, 8, 4, GROUPED, SW>(a, units, stream);
+  return two ? launch_one<IN, OUT, 1, QB, 8, 2, GROUPED, SW>(a, units, stream)
+             : launch_one<IN, OUT, 1, QB, 8, 4, GROUPED, SW>(a, units, stream);
 }
 
 template <int IN, int OUT, bool GROUPED, int SW>
-hipError_t launch_rows(const StreamArgs &a, int rows, int64_t units, hipStream_t stream) {
-  if (rows <= 16) return launch_waves<IN, OUT, 1, GROUPED, SW>(a, units, stream);
-  if (rows <= 32) return launch_waves<IN, OUT, 2, GROUPED, SW>(a, units, stream);
-  return launch_waves<IN, OUT, 4, GROUPED, SW>(a, units, stream);
+hipError_t launch_rows(const StreamArgs &a, int rows, int64_t units, int num_cus, hipStream_t stream) {
+  if (rows <= 16) return launch_waves<IN, OUT, 1, GROUPED, SW>(a, units, num_cus, stream);
+  if (rows <= 32) return launch_waves<IN, OUT, 2, GROUPED, SW>(a, units, num_cus, stream);
+  return launch_waves<IN, OUT, 4, GROUPED, SW>(a, units, num_cus, stream);
 }
 
 }  // namespace
 
 hipError_t launch_stream_fp8(int out, const void *x, const float *sx, const void *w, const float *sw, int w_scale_rows,
-                             void *d, int M, int N, int K, hipStream_t stream) {
+                             void *d, int M, int N, int K, int num_cus, hipStream_t stream) {
   const StreamArgs a{static_cast<const uint8_t *>(x), static_cast<const uint8_t *>(w), sx, sw, nullptr,
-                     static_cast<uint16_t *>(d), M, N, 1, K, (N + kStreamRows - 1) / kStreamRows};
+                     static_cast<uint16_t *>(d), M, N, 1, K, 0};
   const int rows = M <= 16 ? 16 : M <= 32 ? 32 : 64;
   const int64_t units = (M + rows - 1) / rows;
   if (w_scale_rows == 1)
-    return out == kBF16 ? launch_rows<kE4m3, kBF16, false, 1>(a, rows, units, stream)
-                        : launch_rows<kE4m3, kF16, false, 1>(a, rows, units, stream);
-  return out == kBF16 ? launch_rows<kE4m3, kBF16, false, kScaleBlock>(a, rows, units, stream)
-                      : launch_rows<kE4m3, kF16, false, kScaleBlock>(a, rows, units, stream);
+    return out == kBF16 ? launch_rows<kE4m3, kBF16, false, 1>(a, rows, units, num_cus, stream)
+                        : launch_rows<kE4m3, kF16, false, 1>(a, rows, units, num_cus, stream);
+  return out == kBF16 ? launch_rows<kE4m3, kBF16, false, kScaleBlock>(a, rows, units, num_cus, stream)
+                      : launch_rows<kE4m3, kF16, false, kScaleBlock>(a, rows, units, num_cus, stream);
 }
 
 hipError_t launch_stream_grouped(int dtype, const void *x, const void *w, const int *offsets, void *d, int T, int N,
-                                 int K, int E, int rows, hipStream_t stream) {
+                                 int K, int E, int rows, int num_cus, hipStream_t stream) {
   const StreamArgs a{static_cast<const uint8_t *>(x), static_cast<const uint8_t *>(w), nullptr, nullptr, offsets,
-                     static_cast<uint16_t *>(d), T, N, E, 2 * K, (N + kStreamRows - 1) / kStreamRows};
+                     static_cast<uint16_t *>(d), T, N, E, 2 * K, 0};
   const int64_t units = unit_bound(T, E, rows);
-  return dtype == kBF16 ? launch_rows<kBF16, kBF16, true, kScaleBlock>(a, rows, units, stream)
-                        : launch_rows<kF16, kF16, true, kScaleBlock>(a, rows, units, stream);
+  return dtype == kBF16 ? launch_rows<kBF16, kBF16, true, kScaleBlock>(a, rows, units, num_cus, stream)
+                        : launch_rows<kF16, kF16, true, kScaleBlock>(a, rows, units, num_cus, stream);
 }
 
 hipError_t launch_stream_grouped_fp8(int out, const void *x, const float *sx, const void *w, const float *sw,
                                      const int *offsets, void *d, int T, int N, int K, int E, int rows,
-                                     hipStream_t stream) {
+                                     int num_cus, hipStream_t stream) {
   const StreamArgs a{static_cast<const uint8_t *>(x), static_cast<const uint8_t *>(w), sx, sw, offsets,
-                     static_cast<uint16_t *>(d), T, N, E, K, (N + kStreamRows - 1) / kStreamRows};
+                     static_cast<uint16_t *>(d), T, N, E, K, 0};
   const int64_t units = unit_bound(T, E, rows);
-  return out == kBF16 ? launch_rows<kE4m3, kBF16, true, kScaleBlock>(a, rows, units, stream)
-                      : launch_rows<kE4m3, kF16, true, kScaleBlock>(a, rows, units, stream);
+  return out == kBF16 ? launch_rows<kE4m3, kBF16, true, kScaleBlock>(a, rows, units, num_cus, stream)
+                      : launch_rows<kE4m3, kF16, true, kScaleBlock>(a, rows, units, num_cus, stream);
 }
 
 }  // namespace gt
