@@ -142,72 +142,144 @@ fp8_gemm_kernel(Fp8Args a) {
     int tile_k = ld_k;
     asm volatile("" : "+v"(tile_off), "+v"(tile_k));
 
-    auto issue = [&](int kt) {
+    // Load d of this wave for K tile kt (A's rows, B's rows, then the scales).
+    auto issue_one = [&](int kt, int d) {
       const uint32_t stage = lds0 + static_cast<uint32_t>((kt % S::STAGES) * S::kStageBytes);
-      const uint32_t dst = stage + static_cast<uint32_t>(wave) * 1024u;
       const int k0 = kt * kScaleBlock;
-      const uint32_t off = k0 + tile_k < a.K ? tile_off + static_cast<uint32_t>(k0) : kOobOffset;
-#pragma unroll
-      for (int d = 0; d < S::kDmaA; ++d)
-        lds_dma_b128(rsrc_a, off + d * ld_step, __builtin_amdgcn_readfirstlane(dst + d * S::kWaves * 1024));
-#pragma unroll
-      for (int d = 0; d < S::kDmaB; ++d)
-        lds_dma_b128(rsrc_b, off + d * ld_step,
-                     __builtin_amdgcn_readfirstlane(dst + S::kStageA + d * S::kWaves * 1024));
-      lds_dma_b32(rsrc_s, scale_off + static_cast<uint32_t>(kt) * 4u,
-                  __builtin_amdgcn_readfirstlane(stage + S::kStageScales + static_cast<uint32_t>(wave) * 256u));
+      if (d < S::kDmaA + S::kDmaB) {
+        const bool is_a = d < S::kDmaA;
+        const int i = is_a ? d : d - S::kDmaA;
+        const uint32_t off = k0 + tile_k < a.K ? tile_off + static_cast<uint32_t>(k0) : kOobOffset;
+        lds_dma_b128(is_a ? rsrc_a : rsrc_b, off + i * ld_step,
+                     __builtin_amdgcn_readfirstlane(stage + (is_a ? 0 : S::kStageA) + (i * S::kWaves + wave) * 1024));
+      } else {
+        lds_dma_b32(rsrc_s, scale_off + static_cast<uint32_t>(kt) * 4u,
+                    __builtin_amdgcn_readfirstlane(stage + S::kStageScales + static_cast<uint32_t>(wave) * 256u));
+      }
     };
 
-    float4_t acc[S::kFragM][S::kFragN];
+    // Operands in registers: all 16-row blocks of A for a K tile, and the
+    // current and next block of B; scales of A's rows (times the one of B's
+    // columns if they share it) of this K tile and the one before.
+    float4_t acc[S::kFragM][S::kFragN], part[S::kFragM], sbv[2];
+    int8_v fa[S::kFragM], fb[2];
+    float sa[2][S::kFragM];
+    auto read_a = [&](const char *stage, int i) {
+      const char *row = stage + a_base + i * 16 * S::kRowBytes;
+      fa[i] = join(*reinterpret_cast<const int4_t *>(row + piece0), *reinterpret_cast<const int4_t *>(row + piece1));
+    };
+    auto read_b = [&](const char *stage, int j) {
+      const char *row = stage + b_base + j * 16 * S::kRowBytes;
+      fb[j & 1] = join(*reinterpret_cast<const int4_t *>(row + piece0), *reinterpret_cast<const int4_t *>(row + piece1));
+    };
+    auto read_scales = [&](const char *stage, int buf) {
+      const float sb = SB == 1 ? 1.0f : *reinterpret_cast<const float *>(stage + sb_base);
+#pragma unroll
+      for (int i = 0; i < S::kFragM; ++i) {
+        sa[buf][i] = *reinterpret_cast<const float *>(stage + sa_base + i * 64);
+        if constexpr (SB != 1) sa[buf][i] *= sb;
+      }
+    };
+    // Add the scaled sum of MFMA slot m of a K tile whose scales are in sa[buf].
+    auto accumulate = [&](int m, int buf) {
+      const int i = m % S::kFragM, j = m / S::kFragM;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        acc[i][j][e] = __builtin_fmaf(part[i][e], SB == 1 ? sa[buf][i] * sbv[j & 1][e] : sa[buf][i], acc[i][j][e]);
+      asm volatile("" : "+v"(acc[i][j]));  // here, and not where the sums are used next
+    };
+    // One K tile, fixed in order: per MFMA slot the MFMA, the four FMAs of the
+    // slot three before it (whose MFMA has long finished), and what has to be
+    // read or loaded meanwhile.  B's blocks are read one block ahead.  Before
+    // the last block's MFMAs the wave has read all of this stage: it waits for
+    // its loads of the next K tile, meets the other waves, and from then on the
+    // next K tile may be read (each block of A as soon as this tile's last
+    // MFMA on it is issued) and this stage refilled.
+    constexpr int kSlots = S::kFragM * S::kFragN;
+    constexpr int kBehind = 3;
+    static_assert(S::STAGES == 2 && S::kFragM == 4 && S::kFragN % 2 == 0, "the slots' register reuse");
+    auto k_tile = [&](auto parity, int kt) {
+      constexpr int P = decltype(parity)::value;
+      const char *stage = smem + P * S::kStageBytes;
+      const char *other = smem + (1 - P) * S::kStageBytes;
+#pragma unroll
+      for (int n = 0; n < kSlots; ++n) {
+        const int i = n % S::kFragM, j = n / S::kFragM;
+        if (n == kSlots - S::kFragM) {
+          __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
+          wait_vmcnt<0>();
+          workgroup_barrier();
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        part[i] = mfma_fp8(fb[j & 1], fa[i], float4_t{0.0f, 0.0f, 0.0f, 0.0f});
+        __builtin_amdgcn_sched_barrier(0);
+        if (n < kBehind)
+          accumulate(kSlots - kBehind + n, 1 - P);
+        else
+          accumulate(n - kBehind, P);
+        __builtin_amdgcn_sched_barrier(0);
+        if (j + 1 < S::kFragN) {
+          if (i == 0) read_b(stage, j + 1);
+        } else {
+          // No branches here, so that the slots stay in this order: past the
+          // last K tile the reads fetch stale numbers that nothing uses, and
+          // the loads write zeros to a stage that nothing reads.
+          read_a(other, i);
+          if (i == 0) read_b(other, 0);
+          if (i == S::kFragM - 1) read_scales(other, 1 - P);
+#pragma unroll
+          for (int d = 0; d < S::kPerStage; ++d)
+            if (d % S::kFragM == i) issue_one(kt + 2, d);
+        }
+        if constexpr (SB == 1) {
+          // B's scales of a block, once the slots of the block two before are done.
+          if (i == kBehind - 1) sbv[(j + 1) & 1] = *reinterpret_cast<const float4_t *>(
+              (j + 1 < S::kFragN ? stage : other) + sb_base + (j + 1) % S::kFragN * 64);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+
     // Every wave is done with the previous tile's LDS.
     __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
     workgroup_barrier();
 #pragma unroll
-    for (int s = 0; s < S::STAGES - 1; ++s)
-      if (s < KT) issue(s);
+    for (int s = 0; s < 2; ++s)
 #pragma unroll
-    for (int i = 0; i < S::kFragM; ++i)
+      for (int d = 0; d < S::kPerStage; ++d) issue_one(s, d);
+#pragma unroll
+    for (int i = 0; i < S::kFragM; ++i) {
+      part[i] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      sa[1][i] = 0.0f;  // "before" the first K tile
 #pragma unroll
       for (int j = 0; j < S::kFragN; ++j) acc[i][j] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-
-    for (int kt = 0; kt < KT; ++kt) {
-      // K tile kt has landed (for every wave, past the barrier), and every
-      // wave has read all of K tile kt - 1, whose stage is filled next.
-      wait_younger<S::kPerStage, S::STAGES - 2>(min(KT - 1 - kt, S::STAGES - 2));
-      __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
-      workgroup_barrier();
-      if (kt + S::STAGES - 1 < KT) issue(kt + S::STAGES - 1);
-      const char *stage = smem + (kt % S::STAGES) * S::kStageBytes;
-      int8_v fa[S::kFragM];
-      float sa[S::kFragM];
-      const float sb0 = *reinterpret_cast<const float *>(stage + sb_base);
+    }
+    sbv[1] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    wait_vmcnt<S::kPerStage>();
+    workgroup_barrier();
 #pragma unroll
-      for (int i = 0; i < S::kFragM; ++i) {
-        const char *row = stage + a_base + i * 16 * S::kRowBytes;
-        fa[i] = join(*reinterpret_cast<const int4_t *>(row + piece0), *reinterpret_cast<const int4_t *>(row + piece1));
-        sa[i] = *reinterpret_cast<const float *>(stage + sa_base + i * 64);
-        if constexpr (SB != 1) sa[i] *= sb0;
-      }
+    for (int i = 0; i < S::kFragM; ++i) read_a(smem, i);
+    read_b(smem, 0);
+    read_scales(smem, 0);
+    if constexpr (SB == 1) sbv[0] = *reinterpret_cast<const float4_t *>(smem + sb_base);
+    int kt = 0;
+    for (; kt + 1 < KT; kt += 2) {
+      k_tile(std::integral_constant<int, 0>{}, kt);
+      k_tile(std::integral_constant<int, 1>{}, kt + 1);
+    }
+    if (kt < KT) {
+      k_tile(std::integral_constant<int, 0>{}, kt);
 #pragma unroll
-      for (int j = 0; j < S::kFragN; ++j) {
-        const char *row = stage + b_base + j * 16 * S::kRowBytes;
-        const int8_v fb =
-            join(*reinterpret_cast<const int4_t *>(row + piece0), *reinterpret_cast<const int4_t *>(row + piece1));
-        float4_t sb{1.0f, 1.0f, 1.0f, 1.0f};
-        if constexpr (SB == 1) sb = *reinterpret_cast<const float4_t *>(stage + sb_base + j * 64);
+      for (int m = kSlots - kBehind; m < kSlots; ++m) accumulate(m, 0);
+    } else {
 #pragma unroll
-        for (int i = 0; i < S::kFragM; ++i) {
-          const float4_t p = mfma_fp8(fb, fa[i], float4_t{0.0f, 0.0f, 0.0f, 0.0f});
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            acc[i][j][e] = __builtin_fmaf(p[e], SB == 1 ? sa[i] * sb[e] : sa[i], acc[i][j][e]);
-        }
-      }
+      for (int m = kSlots - kBehind; m < kSlots; ++m) accumulate(m, 1);
     }
 
     // ---- epilogue ------------------------------------------------------------
     __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
-    workgroup_barrier();  // every wave is done reading the ring
+    wait_vmcnt<0>();      // the loads past the last K tile have written their zeros
+    workgroup_barrier();  // and every wave is done with the ring
     const uint32_t stage_base = static_cast<uint32_t>(wave * S::kWaveM * S::kStagePitch);
 #pragma unroll
     for (int i = 0; i < S::kFragM; ++i) {
