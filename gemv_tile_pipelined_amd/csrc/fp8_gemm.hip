@@ -188,16 +188,36 @@ fp8_gemm_kernel(Fp8Args a) {
         acc[i][j][e] = __builtin_fmaf(part[i][e], SB == 1 ? sa[buf][i] * sbv[j & 1][e] : sa[buf][i], acc[i][j][e]);
       asm volatile("" : "+v"(acc[i][j]));  // here, and not where the sums are used next
     };
+    // Loads are issued in two parts.  The first half of each wave column's
+    // blocks of B lies in the even loads of B's rows, the second in the odd.
+    constexpr int kEarly = S::kDmaA + S::kDmaB / 2;  // A and B's first half
+    constexpr int kLate = S::kPerStage - kEarly;     // the scales, then B's second half
+    auto issue_early = [&](int kt, int k) {
+      issue_one(kt, k < S::kDmaA ? k : S::kDmaA + 2 * (k - S::kDmaA));
+    };
+    auto issue_late = [&](int kt, int k) {
+      issue_one(kt, k == 0 ? S::kDmaA + S::kDmaB : S::kDmaA + 2 * (k - 1) + 1);
+    };
+    static_assert(S::kDmaB % 2 == 0 && kRowStep * 2 == S::kWaveN, "a half of a wave column's rows per load of B");
     // One K tile, fixed in order: per MFMA slot the MFMA, the four FMAs of the
     // slot three before it (whose MFMA has long finished), and what has to be
-    // read or loaded meanwhile.  B's blocks are read one block ahead.  Before
-    // the last block's MFMAs the wave has read all of this stage: it waits for
-    // its loads of the next K tile, meets the other waves, and from then on the
-    // next K tile may be read (each block of A as soon as this tile's last
-    // MFMA on it is issued) and this stage refilled.
+    // read or loaded meanwhile.  B's blocks are read one block ahead.  Two
+    // barriers let every load fly for about 1.5 K tiles, two stages
+    // notwithstanding:
+    //  * the first, before the last block of B's first half: all of A (read
+    //    during the K tile before) and of B's first half is in registers, so
+    //    that part of the stage is refilled; and B's second half has landed;
+    //  * the second, before the last block: the rest is in registers and is
+    //    refilled, and the next K tile's A, first half of B and scales have
+    //    landed, the blocks of A being read into the registers of this one's as
+    //    its last MFMA on each is issued.
+    // Loads complete in order: what may still be in flight at a barrier is
+    // what was issued after what it needs.
     constexpr int kSlots = S::kFragM * S::kFragN;
     constexpr int kBehind = 3;
+    constexpr int kFirst = (S::kFragN / 2 - 1) * S::kFragM, kSecond = kSlots - S::kFragM;
     static_assert(S::STAGES == 2 && S::kFragM == 4 && S::kFragN % 2 == 0, "the slots' register reuse");
+    static_assert(kFirst + kEarly <= kSecond && kLate <= S::kFragM, "a load per slot");
     auto k_tile = [&](auto parity, int kt) {
       constexpr int P = decltype(parity)::value;
       const char *stage = smem + P * S::kStageBytes;
@@ -205,9 +225,12 @@ fp8_gemm_kernel(Fp8Args a) {
 #pragma unroll
       for (int n = 0; n < kSlots; ++n) {
         const int i = n % S::kFragM, j = n / S::kFragM;
-        if (n == kSlots - S::kFragM) {
+        if (n == kFirst || n == kSecond) {
           __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
-          wait_vmcnt<0>();
+          if (n == kFirst)
+            wait_vmcnt<kEarly + kLate>();  // all of K tile kt + 1
+          else
+            wait_vmcnt<kLate - 1 + kEarly>();  // B's second half of kt + 1, the early part of kt + 2
           workgroup_barrier();
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -218,18 +241,17 @@ fp8_gemm_kernel(Fp8Args a) {
         else
           accumulate(n - kBehind, P);
         __builtin_amdgcn_sched_barrier(0);
+        // No branches, so that the slots stay in this order: past the last K
+        // tile the reads fetch numbers that nothing uses, and the loads, out
+        // of range, write zeros that nothing reads.
         if (j + 1 < S::kFragN) {
           if (i == 0) read_b(stage, j + 1);
+          if (n >= kFirst && n < kFirst + kEarly) issue_early(kt + 2, n - kFirst);
         } else {
-          // No branches here, so that the slots stay in this order: past the
-          // last K tile the reads fetch stale numbers that nothing uses, and
-          // the loads write zeros to a stage that nothing reads.
           read_a(other, i);
           if (i == 0) read_b(other, 0);
           if (i == S::kFragM - 1) read_scales(other, 1 - P);
-#pragma unroll
-          for (int d = 0; d < S::kPerStage; ++d)
-            if (d % S::kFragM == i) issue_one(kt + 2, d);
+          if (i < kLate) issue_late(kt + 2, i);
         }
         if constexpr (SB == 1) {
           // B's scales of a block, once the slots of the block two before are done.
@@ -244,9 +266,12 @@ fp8_gemm_kernel(Fp8Args a) {
     __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
     workgroup_barrier();
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int s = 0; s < 2; ++s) {
 #pragma unroll
-      for (int d = 0; d < S::kPerStage; ++d) issue_one(s, d);
+      for (int k = 0; k < kEarly; ++k) issue_early(s, k);
+#pragma unroll
+      for (int k = 0; k < kLate; ++k) issue_late(s, k);
+    }
 #pragma unroll
     for (int i = 0; i < S::kFragM; ++i) {
       part[i] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
@@ -255,7 +280,7 @@ fp8_gemm_kernel(Fp8Args a) {
       for (int j = 0; j < S::kFragN; ++j) acc[i][j] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
     }
     sbv[1] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    wait_vmcnt<S::kPerStage>();
+    wait_vmcnt<kLate - 1 + S::kPerStage>();  // K tile 0 but for B's second half
     workgroup_barrier();
 #pragma unroll
     for (int i = 0; i < S::kFragM; ++i) read_a(smem, i);
