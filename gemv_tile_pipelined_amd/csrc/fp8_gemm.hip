@@ -22,6 +22,7 @@
 #include "fp8_common.hpp"
 #include "groups.hpp"
 #include "kernels.hpp"
+#include "tile_store.hpp"
 
 #include <type_traits>
 
@@ -36,7 +37,7 @@ struct Fp8Args {
   uint16_t *D;
   int M, N, K, E;  // M: rows of A (all groups)
   int tiles_n;
-  int vec16;
+  int alignment;  // of D's rows
 };
 
 template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int STAGES_>
@@ -305,39 +306,28 @@ fp8_gemm_kernel(Fp8Args a) {
     __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
     wait_vmcnt<0>();      // the loads past the last K tile have written their zeros
     workgroup_barrier();  // and every wave is done with the ring
-    const uint32_t stage_base = static_cast<uint32_t>(wave * S::kWaveM * S::kStagePitch);
+    // The lane, made new for every tile (grouped_kernel.hpp).
+    int ep_lane = lane;
+    asm volatile("" : "+v"(ep_lane));
+    const int ep_row = ep_lane % 16;
+    const int ep_kgrp = ep_lane / 16;
+    char *const tile = smem + wave * S::kWaveM * S::kStagePitch;
+    const int n = n0 + wn * S::kWaveN;
+    _Float16 *const dst =
+        reinterpret_cast<_Float16 *>(a.D) + (static_cast<int64_t>(g.row) + wm * S::kWaveM) * a.N + n;
 #pragma unroll
     for (int i = 0; i < S::kFragM; ++i) {
+      const int r = i * 16 + ep_row;
 #pragma unroll
       for (int j = 0; j < S::kFragN; ++j) {
         half4_t h;
 #pragma unroll
         for (int e = 0; e < 4; ++e) h[e] = round_out<OUT>(acc[i][j][e]);
-        *reinterpret_cast<half4_t *>(smem + stage_base + (i * 16 + frag_row) * S::kStagePitch +
-                                     (j * 16 + frag_kgrp * 4) * 2) = h;
+        *reinterpret_cast<half4_t *>(tile + r * S::kStagePitch + (j * 16 + ep_kgrp * 4) * 2) = h;
       }
     }
-    constexpr int kRowChunks = S::kWaveN / 8;
-    constexpr int kRowsPerPass = 64 / kRowChunks;
-    static_assert(64 % kRowChunks == 0, "lanes per staged row");
-    const int chunk = lane % kRowChunks;
-    const int n = n0 + wn * S::kWaveN + chunk * 8;
-#pragma unroll 4
-    for (int r0 = 0; r0 < S::kWaveM; r0 += kRowsPerPass) {
-      const int r = r0 + lane / kRowChunks;
-      const half8_t v = *reinterpret_cast<const half8_t *>(smem + stage_base + r * S::kStagePitch + chunk * 16);
-      const int m = wm * S::kWaveM + r;
-      if (m < rows) {
-        _Float16 *dst = reinterpret_cast<_Float16 *>(a.D) + (static_cast<int64_t>(g.row) + m) * a.N + n;
-        if (a.vec16 && n + 8 <= a.N) {
-          __builtin_nontemporal_store(v, reinterpret_cast<half8_t *>(dst));
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (n + e < a.N) dst[e] = v[e];
-        }
-      }
-    }
+    store_wave_tile<S::kWaveM, S::kWaveN, S::kStagePitch>(tile, dst, a.N, rows - wm * S::kWaveM, a.N - n, a.alignment,
+                                                          ep_lane);
   }
 }
 
@@ -347,7 +337,7 @@ using Fp8Tile128 = Fp8Shape<128, 128, 2, 2, 2>;
 template <class S, int OUT, bool GROUPED, int SB>
 hipError_t launch_shape(Fp8Args a, int num_cus, hipStream_t stream) {
   a.tiles_n = (a.N + S::BN - 1) / S::BN;
-  a.vec16 = a.N % 8 == 0 && reinterpret_cast<uintptr_t>(a.D) % 16 == 0;
+  a.alignment = row_alignment(a.D, a.N);
   const int64_t units = GROUPED ? unit_bound(a.M, a.E, S::BM) : (a.M + S::BM - 1) / S::BM;
   const int64_t tiles = units * a.tiles_n;
   // Workgroups that fit the CUs at once: by LDS, and two waves to a SIMD.

@@ -31,6 +31,7 @@
 
 #include "gemm_kernel.hpp"
 #include "groups.hpp"
+#include "tile_store.hpp"
 
 namespace gt {
 
@@ -42,7 +43,7 @@ struct GroupedArgs {
   const int *offsets;
   int T, N, K, E;
   int tiles_m, tiles_n;  // column tiles; row tiles of a group's output (wgrad)
-  int vec16;             // rows of D are 16-byte aligned
+  int alignment;         // of D's rows
 };
 
 template <int BX>
@@ -357,41 +358,23 @@ grouped_gemm_kernel(GroupedArgs a) {
     asm volatile("" : "+v"(ep_lane));
     const int ep_row = ep_lane % 16;
     const int ep_kgrp = ep_lane / 16;
-    const uint32_t stage_base = static_cast<uint32_t>(wave * S::kWaveM * S::kStagePitch);
+    char *const tile = smem + wave * S::kWaveM * S::kStagePitch;
+    const int n = n0 + wn * S::kWaveN;
+    _Float16 *const dst = reinterpret_cast<_Float16 *>(pd) + static_cast<int64_t>(wm * S::kWaveM) * cols + n;
 #pragma unroll
     for (int i = 0; i < S::kFragM; ++i) {
+      const int r = i * 16 + ep_row;
 #pragma unroll
       for (int j = 0; j < S::kFragN; ++j) {
         half4_t h;
 #pragma unroll
         for (int e = 0; e < 4; ++e) h[e] = round_out<S::DTYPE>(acc[i][j][e]);
-        const uint32_t off = stage_base + static_cast<uint32_t>((i * 16 + ep_row) * S::kStagePitch) +
-                             static_cast<uint32_t>(j * 16 + ep_kgrp * 4) * 2u;
-        *reinterpret_cast<half4_t *>(smem + off) = h;
+        *reinterpret_cast<half4_t *>(tile + r * S::kStagePitch + (j * 16 + ep_kgrp * 4) * 2) = h;
       }
       __builtin_amdgcn_sched_barrier(0);  // a block row at a time, for the registers
     }
-    constexpr int kRowChunks = S::kWaveN / 8;
-    constexpr int kRowsPerPass = 64 / kRowChunks;
-    static_assert(64 % kRowChunks == 0, "lanes per staged row");
-    const int chunk = ep_lane % kRowChunks;
-    const int n = n0 + wn * S::kWaveN + chunk * 8;
-#pragma unroll 2
-    for (int r0 = 0; r0 < S::kWaveM; r0 += kRowsPerPass) {
-      const int r = r0 + ep_lane / kRowChunks;
-      const half8_t v = *reinterpret_cast<const half8_t *>(smem + stage_base + r * S::kStagePitch + chunk * 16);
-      const int m = wm * S::kWaveM + r;
-      if (m < rows) {
-        _Float16 *dst = reinterpret_cast<_Float16 *>(pd) + static_cast<int64_t>(m) * cols + n;
-        if (a.vec16 && n + 8 <= cols) {
-          __builtin_nontemporal_store(v, reinterpret_cast<half8_t *>(dst));
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (n + e < cols) dst[e] = v[e];
-        }
-      }
-    }
+    store_wave_tile<S::kWaveM, S::kWaveN, S::kStagePitch>(tile, dst, cols, rows - wm * S::kWaveM, cols - n, a.alignment,
+                                                          ep_lane);
   }
 }
 
@@ -429,7 +412,7 @@ static hipError_t launch_grouped_shape(GroupedArgs a, int num_cus, hipStream_t s
   const int cols = OP == kGroupForward ? a.N : a.K;
   a.tiles_n = (cols + S::BN - 1) / S::BN;
   a.tiles_m = (a.N + S::BM - 1) / S::BM;
-  a.vec16 = cols % 8 == 0 && reinterpret_cast<uintptr_t>(a.D) % 16 == 0;
+  a.alignment = row_alignment(a.D, cols);
   int64_t grid;
   if constexpr (OP == kGroupWgrad) {
     grid = static_cast<int64_t>(a.E) * a.tiles_m * a.tiles_n;
