@@ -484,7 +484,7 @@ int run_grouped(int op, const void *A, const float *sa, const void *B, const flo
     return GEMVTILE_ERR_INVALID_ARG;
   int st = check_grouped_sizes(op, T, N, K, E);
   if (st != GEMVTILE_OK) return st;
-  if (misaligned(D, 2) || misaligned(offsets, 4)) return GEMVTILE_ERR_UNSUPPORTED;
+  if (misaligned(D, op == kOpDgrad || op == kOpWgrad ? 16 : 2) || misaligned(offsets, 4)) return GEMVTILE_ERR_UNSUPPORTED;
   if (summed > 0 && (misaligned(A, 16) || misaligned(B, 16) || misaligned(sa, 4) || misaligned(sb, 4)))
     return GEMVTILE_ERR_UNSUPPORTED;
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -573,7 +573,10 @@ int gemvtile_grouped_plan(int op, int64_t T, int64_t N, int64_t K, int64_t E, in
     *cols = 16;
     return 1;
   }
-  gt::grouped_tile(op, T, N, K, E, static_cast<int>(num_cus), rows, cols);
+  if (op == kOpFp8)
+    gt::fp8_tile(true, T, N, E, static_cast<int>(num_cus), rows, cols);
+  else
+    gt::grouped_plan_tile(op, T, N, K, E, static_cast<int>(num_cus), rows, cols);
   return 0;
 }
 

@@ -81,8 +81,8 @@ __global__ void __launch_bounds__(S::kThreads) __attribute__((amdgpu_waves_per_e
 fp8_gemm_kernel(Fp8Args a) {
   // The table lies behind the ring in one allocation, so that the ring starts
   // at LDS address 0 and its offsets fit the instructions.
-  __shared__ __attribute__((aligned(1024))) char smem[S::kLdsBytes + (GROUPED ? sizeof(GroupTable) : 0)];
-  GroupTable &table = *reinterpret_cast<GroupTable *>(smem + S::kLdsBytes);
+  __shared__ __attribute__((aligned(1024))) char smem[S::kLdsBytes + (GROUPED ? sizeof(GroupTable<kMaxGroups>) : 0)];
+  auto &table = *reinterpret_cast<GroupTable<kMaxGroups> *>(smem + S::kLdsBytes);
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -118,7 +118,7 @@ fp8_gemm_kernel(Fp8Args a) {
   if constexpr (GROUPED) {
     build_group_table(&table, a.offsets, a.E, a.M, S::BM);
     __syncthreads();
-    units = __builtin_amdgcn_readfirstlane(table.upto[a.E - 1]);
+    units = table_units(&table, a.E);
   }
   const int64_t num_tiles = static_cast<int64_t>(units) * a.tiles_n;
   for (int64_t u = xcd_logical_id(blockIdx.x, gridDim.x); u < num_tiles; u += gridDim.x) {
@@ -341,7 +341,7 @@ hipError_t launch_shape(Fp8Args a, int num_cus, hipStream_t stream) {
   const int64_t units = GROUPED ? unit_bound(a.M, a.E, S::BM) : (a.M + S::BM - 1) / S::BM;
   const int64_t tiles = units * a.tiles_n;
   // Workgroups that fit the CUs at once: by LDS, and two waves to a SIMD.
-  constexpr int kLds = S::kLdsBytes + (GROUPED ? static_cast<int>(sizeof(GroupTable)) : 0);
+  constexpr int kLds = S::kLdsBytes + (GROUPED ? static_cast<int>(sizeof(GroupTable<kMaxGroups>)) : 0);
   constexpr int kByLds = 160 * 1024 / kLds, kByWaves = 8 / S::kWaves;
   constexpr int kPerCu = kByLds < kByWaves ? kByLds : kByWaves;
   static_assert(kPerCu >= 1, "a workgroup fits a CU");

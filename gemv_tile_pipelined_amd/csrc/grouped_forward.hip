@@ -10,8 +10,7 @@ hipError_t launch_grouped_forward(int dtype, const void *A, const void *B, const
                         : launch_grouped_op<kF16, kGroupForward>(A, B, offsets, D, T, N, K, E, num_cus, stream);
 }
 
-void grouped_tile(int op, int64_t T, int64_t N, int64_t K, int64_t E, int num_cus, int *rows, int *cols) {
-  if (op == 3) return fp8_tile(true, T, N, E, num_cus, rows, cols);
+void grouped_plan_tile(int op, int64_t T, int64_t N, int64_t K, int64_t E, int num_cus, int *rows, int *cols) {
   const GemmTileShape &s = kGemmTileShapes[grouped_default_tile(op, T, N, K, E, num_cus)];
   *rows = s.bm;
   *cols = s.bn;

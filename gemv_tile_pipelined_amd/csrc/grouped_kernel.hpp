@@ -24,9 +24,19 @@
 // Which tiles there are.  Forward and dgrad cut every group's rows into units
 // of BM rows; a persistent workgroup keeps a table of the groups in LDS and
 // walks (unit, column tile) pairs in the GEMM's grouped order, so that units
-// of one group share the group's weights in L2.  In wgrad the groups'
-// outputs are all alike and the contraction differs: workgroups are not
-// persistent there, so that whichever finishes takes the next tile.
+// of one group share the group's weights in L2.  In wgrad the groups' outputs
+// are all alike and the contraction differs: the groups' tiles come in order of
+// falling length and the workgroups take them forwards and backwards in turn,
+// so that each gets about the same sum of lengths.
+//
+// Between two tiles.  Contractions are short here (a group's rows in wgrad, a
+// projection's width), so a tile's start and end count.  The first loads of the
+// next tile go out as soon as every wave has read its last operands, before
+// this tile's results are rounded and stored; these leave straight from the
+// registers (16 bytes a lane once v_permlane16_swap has joined the halves of
+// two blocks) by buffer stores, always the same number of them, so that the
+// next tile's waits can count them.  Outputs whose rows are not 16-byte
+// aligned go through LDS instead (tile_store.hpp), before the next tile's loads.
 #pragma once
 
 #include "gemm_kernel.hpp"
@@ -35,6 +45,9 @@
 
 namespace gt {
 
+typedef uint32_t uint4_v __attribute__((ext_vector_type(4)));
+constexpr int kStreamed = 2;  // cache policy of a store: nt
+
 enum : int { kGroupForward = 0, kGroupDgrad = 1, kGroupWgrad = 2 };
 
 struct GroupedArgs {
@@ -42,8 +55,7 @@ struct GroupedArgs {
   uint16_t *D;
   const int *offsets;
   int T, N, K, E;
-  int tiles_m, tiles_n;  // column tiles; row tiles of a group's output (wgrad)
-  int alignment;         // of D's rows
+  int alignment;  // of D's rows
 };
 
 template <int BX>
@@ -62,17 +74,172 @@ __device__ inline half4_t lds_read_transposed(uint32_t addr) {
       half4_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<GT_LDS short4_v *>(static_cast<uintptr_t>(addr))));
 }
 
-template <class S, int OP>
-__global__ void __launch_bounds__(S::kThreads) __attribute__((amdgpu_waves_per_eu(S::kWaves / 4, S::kWaves / 4)))
-grouped_gemm_kernel(GroupedArgs a) {
+// The groups in the order wgrad takes them.
+template <int CAP>
+struct WgradTable {
+  int group[CAP];
+  int begin[CAP];
+  int end[CAP];
+};
+// Groups are sorted by length if there are no more than this; among many the
+// sums even out by themselves.
+constexpr int kMaxSorted = 256;
+
+template <int CAP>
+__device__ inline void build_wgrad_table(WgradTable<CAP> *table, const int *__restrict__ offsets, int E, int T, int threads) {
+  const int tid = static_cast<int>(threadIdx.x);
+  for (int e = tid; e < E; e += threads) {
+    const GroupRows g = group_rows(offsets[e], offsets[e + 1], T);
+    table->group[e] = e;
+    table->begin[e] = g.begin;
+    table->end[e] = g.end;
+  }
+  __syncthreads();
+  if (E > kMaxSorted) return;
+  const bool mine = tid < E;
+  const int begin = mine ? table->begin[tid] : 0, end = mine ? table->end[tid] : 0;
+  int rank = 0;
+  for (int e = 0; e < E; ++e) {
+    const int len = table->end[e] - table->begin[e];
+    rank += len > end - begin || (len == end - begin && e < tid);
+  }
+  __syncthreads();
+  if (mine) {
+    table->group[rank] = tid;
+    table->begin[rank] = begin;
+    table->end[rank] = end;
+  }
+}
+
+// The ring walker's operations (gemm_kernel.hpp), with waits that let `STORES`
+// younger stores of the tile before stay in flight while `stores` is set.
+template <class S, int STORES, class Base>
+struct GroupedRingOps : Base {
+  bool stores;
+  static constexpr int loop_count() {
+    if constexpr (S::EARLY_FREE)
+      return RingEarly<S>::kSteadyVmcnt;
+    else
+      return (S::STAGES - 2) * S::kDmaPerStage;
+  }
+  __device__ __attribute__((always_inline)) void wait_tile(int n) {
+    if (stores)
+      wait_counted<STORES>(n);
+    else
+      wait_counted<0>(n);
+    stores = false;
+  }
+  // n is one of the two counts of grouped_k_loop's waits.
+  template <int MORE>
+  __device__ __attribute__((always_inline)) void wait_counted(int n) {
+    constexpr int kLoop = loop_count();
+    if (n == kLoop)
+      wait_vmcnt<kLoop + MORE>();
+    else
+      wait_vmcnt<(S::STAGES - 1) * S::kDmaPerStage + MORE>();
+  }
+};
+
+// K tiles whose loads are issued ahead of a K loop.
+template <class S>
+constexpr int grouped_ahead() {
+  return S::EARLY_FREE ? S::STAGES : S::STAGES - 1;
+}
+
+// ring.hpp's K loops from the point where the loads of the first tiles are
+// issued, with every K tile in the steady state: loads past the last K tile are
+// out of range and write zeros to stages that nothing reads any more, and the
+// operands read past it are not used.  One loop body instead of one for each
+// phase of the ring: through several, the accumulators did not keep their
+// registers.
+template <class S, class Ops>
+__device__ __attribute__((always_inline)) inline void grouped_k_loop(Ops &ops, int ktu, bool stores) {
+  constexpr int kEndless = 1 << 24;  // K tiles, for the walker's counts
+  ops.init_acc();
+  ops.fence();
+  ops.stores = stores;
+  ops.wait_tile((grouped_ahead<S>() - 1) * S::kDmaPerStage);
+  ops.stores = stores;  // tile 1 is older than the stores as well
+  ops.barrier();
+#pragma unroll
+  for (int r = 0; r < S::kReads; ++r) ops.read(0, 0, 0, r);
+  int kt = 0;
+  if constexpr (S::EARLY_FREE) {
+    for (; kt + 1 < ktu; kt += 2) {
+      ring_ktile_ef<S, true, true>(ops, kt, kEndless);
+      ring_ktile_ef<S, true, true>(ops, kt + 1, kEndless);
+    }
+    if (kt < ktu) ring_ktile_ef<S, true, true>(ops, kt, kEndless);
+  } else {
+#pragma unroll
+    for (int pos = 0; pos < RingSlots<S>::kAfter; ++pos) {
+      const int d = ring_slot_load<S>(pos);
+      if (d >= 0) ops.load(S::STAGES - 1, d);
+    }
+    for (; kt < ktu; ++kt) ring_ktile<S, true, true, true>(ops, kt, kEndless);
+  }
+}
+
+// Where a tile lies in its group's output (or unit): the operands' rows that
+// it is made of, its sizes and its place in the output.
+struct GroupedTile {
+  const uint16_t *pa, *pb;
+  uint16_t *pd;
+  int rows, C, KT, n0, m0;
+  int4_t rsrc_a, rsrc_b;  // of operands that are contiguous along the contraction
+};
+
+// The output's rows of a big tile: a unit's, or BM rows of a group's dW.
+struct GroupedRows {
+  int group, begin, end;  // the group's rows of the operands
+  int row;                // the first row of the output (of the group's dW in wgrad)
+  int rows;               // and how many there are from there on
+};
+
+template <int OP>
+__device__ inline GroupedTile grouped_tile(const GroupedArgs &a, const GroupedRows &g, int n0, int BM, int BN, int BK) {
+  constexpr bool kTransA = OP == kGroupWgrad;
+  constexpr bool kTransB = OP != kGroupForward;
+  const int lda = OP == kGroupForward ? a.K : a.N;
+  const int cols = OP == kGroupForward ? a.N : a.K;
+  GroupedTile t{};
+  t.n0 = n0;
+  t.rows = min(BM, g.rows);
+  if constexpr (OP != kGroupWgrad) {
+    t.C = OP == kGroupForward ? a.K : a.N;
+    t.pa = a.A + static_cast<int64_t>(g.row) * lda;
+    t.pb = a.B + static_cast<int64_t>(g.group) * a.N * a.K;
+    if constexpr (OP == kGroupForward) t.pb += static_cast<int64_t>(n0) * a.K;
+    t.pd = a.D + static_cast<int64_t>(g.row) * cols;
+  } else {
+    t.m0 = g.row;
+    t.C = g.end - g.begin;
+    t.pa = a.A + static_cast<int64_t>(g.begin) * lda;
+    t.pb = a.B + static_cast<int64_t>(g.begin) * a.K;
+    t.pd = a.D + (static_cast<int64_t>(g.group) * a.N + g.row) * cols;
+  }
+  // A sum over nothing still walks one K tile, all of it out of range: zeros.
+  t.KT = max(1, (t.C + BK - 1) / BK);
+  if constexpr (!kTransA) t.rsrc_a = make_buffer_rsrc(t.pa, static_cast<uint32_t>(t.rows) * lda * 2u);
+  if constexpr (!kTransB) t.rsrc_b = make_buffer_rsrc(t.pb, static_cast<uint32_t>(min(BN, cols - n0)) * a.K * 2u);
+  return t;
+}
+
+// LDS of a phase: the ring, and behind it a block row of staging per wave, or
+// (outputs whose rows are not aligned) the whole staged tile over the ring.
+template <class S, bool ALIGNED>
+constexpr int grouped_lds() {
+  return ALIGNED ? S::kRingBytes + S::kWaves * 16 * S::kStagePitch : S::kLdsBytes;
+}
+
+// Computes the tiles that `next` gives, one after another: next(&tile) returns
+// false when there are no more (both wave-uniform).  No other wave may still
+// use the LDS, nor this one have loads to it in flight.
+template <class S, int OP, bool ALIGNED, class Next>
+__device__ __attribute__((always_inline)) inline void grouped_phase(const GroupedArgs &a, char *smem, Next next) {
   static_assert(S::MI == 16 && S::BK == 64 && S::STAGES >= 2 && S::SWIZZLE, "the pipelined 16x16x32 loop");
   constexpr bool kTransA = OP == kGroupWgrad;
   constexpr bool kTransB = OP != kGroupForward;
-  constexpr bool kTable = OP != kGroupWgrad;
-  // The table lies behind the ring in one allocation, so that the ring starts
-  // at LDS address 0 and its offsets fit the instructions.
-  __shared__ __attribute__((aligned(1024))) char smem[S::kLdsBytes + (kTable ? sizeof(GroupTable) : 0)];
-  GroupTable &table = *reinterpret_cast<GroupTable *>(smem + S::kLdsBytes);
 
   const int tid = threadIdx.x;
   const int lane = tid & 63;
@@ -81,8 +248,7 @@ grouped_gemm_kernel(GroupedArgs a) {
   const int wn = wave % S::WAVES_N;
   const uint32_t lds0 = lds_addr(smem);
 
-  // Row strides (elements) of the operands and the output, columns of the
-  // output, and the contraction (per group in wgrad).
+  // Row strides (elements) of the operands, and the columns of the output.
   const int lda = OP == kGroupForward ? a.K : a.N;
   const int ldb = a.K;
   const int cols = OP == kGroupForward ? a.N : a.K;
@@ -133,137 +299,130 @@ grouped_gemm_kernel(GroupedArgs a) {
   const uint32_t tb_base = lds0 + S::kStageA + static_cast<uint32_t>(t_row * TileB::kRowBytes) +
                            ((static_cast<uint32_t>(wn * S::kWaveN * 2) + t_col) ^ t_swz);
 
-  // The first barrier of the next tile's K loop also ends this tile's use of
-  // the LDS.
-  const int64_t stride = gridDim.x;
-  int64_t num_tiles, u;
-  int units = 0;
-  if constexpr (kTable) {
-    build_group_table(&table, a.offsets, a.E, a.T, S::BM);
-    __syncthreads();
-    units = __builtin_amdgcn_readfirstlane(table.upto[a.E - 1]);
-    num_tiles = static_cast<int64_t>(units) * a.tiles_n;
-    u = xcd_logical_id(blockIdx.x, gridDim.x);
-  } else {
-    num_tiles = gridDim.x;
-    u = xcd_block_id(blockIdx.x, gridDim.x);
-  }
-  for (; u < num_tiles; u += stride) {
-    // This tile's operands, sizes and place in the output.
-    const uint16_t *pa, *pb;
-    uint16_t *pd;
-    int rows, C, n0, m0 = 0;
-    if constexpr (kTable) {
-      const TileCoord tc = tile_of(u, units, a.tiles_n, kGemmGroupM);
-      const GroupUnit g = table_unit(&table, a.E, S::BM, static_cast<int>(tc.tm));
-      n0 = static_cast<int>(tc.tn) * S::BN;
-      rows = min(S::BM, g.end - g.row);
-      C = OP == kGroupForward ? a.K : a.N;
-      pa = a.A + static_cast<int64_t>(g.row) * lda;
-      pb = a.B + static_cast<int64_t>(g.group) * a.N * a.K;
-      if constexpr (OP == kGroupForward) pb += static_cast<int64_t>(n0) * ldb;
-      pd = a.D + static_cast<int64_t>(g.row) * cols;
+  // The descriptor of K tile kt's rows of an operand that is not contiguous
+  // along the contraction, from column `col0` on: rows past the contraction's
+  // end read as zeros; columns past the operand's own only reach outputs that
+  // are not stored.
+  auto k_rows_rsrc = [&](const uint16_t *p, int ld, int col0, int C, int kt) {
+    const int k0 = kt * S::BK;
+    const int have = min(S::BK, C - k0);
+    return make_buffer_rsrc(p + static_cast<int64_t>(k0) * ld + col0,
+                            have > 0 ? static_cast<uint32_t>(have) * ld * 2u - static_cast<uint32_t>(col0) * 2u : 0u);
+  };
+
+  // This lane's byte offset in each operand, and the bytes from one load
+  // instruction's rows to the next's; of a transposed operand every load's
+  // offset (the flipped column is bit 6 of the element index).  Re-materialised
+  // inside the tile loop, as in gemm_kernel.
+  uint32_t off_a, step_a, trans_a[kTransA ? S::kDmaA : 1], trans_b[kTransB ? S::kDmaB : 1];
+  int kcol;
+  auto lane_offsets = [&]() {
+    if constexpr (!kTransA) {
+      off_a = static_cast<uint32_t>(ld_row) * lda * 2u + static_cast<uint32_t>(ld_kcol) * 2u;
+      step_a = static_cast<uint32_t>(kRowStep) * lda * 2u;
+      kcol = ld_kcol;
+      asm volatile("" : "+v"(off_a), "+v"(kcol), "+s"(step_a));
+    }
+    auto trans = [&](auto tile, uint32_t row, uint32_t col, int ld, uint32_t *off) {
+      using Tt = decltype(tile);
+#pragma unroll
+      for (int i = 0; i < S::BK / (Tt::kRowsPerDma * S::kWaves); ++i) {
+        off[i] = ((row + static_cast<uint32_t>(i * Tt::kRowsPerDma * S::kWaves)) * static_cast<uint32_t>(ld) +
+                  (flip(tile, i) ? col ^ 64u : col)) *
+                 2u;
+        asm volatile("" : "+v"(off[i]));
+      }
+    };
+    if constexpr (kTransA) trans(TileA{}, ta_row, ta_col, lda, trans_a);
+    if constexpr (kTransB) trans(TileB{}, tb_row, tb_col, ldb, trans_b);
+  };
+
+  struct DmaArgs {
+    int4_t rsrc;
+    uint32_t voffset;
+  };
+  // Load d of a K tile: descriptors ra and rb, and the K tile's first
+  // contraction index (its byte offset and the range test of operands that
+  // are contiguous along it).
+  auto dma_args = [&](int4_t ra, int4_t rb, int C, int k0, int d) -> DmaArgs {
+    const bool is_a = d < S::kDmaA;
+    const int i = is_a ? d : d - S::kDmaA;
+    if (is_a ? kTransA : kTransB) return DmaArgs{is_a ? ra : rb, is_a ? trans_a[i] : trans_b[i]};
+    // Both operands' rows are equally long where neither is transposed.
+    const uint32_t off = k0 + kcol < C ? off_a + static_cast<uint32_t>(k0) * 2u : kOobOffset;
+    return DmaArgs{is_a ? ra : rb, off + static_cast<uint32_t>(i) * step_a};
+  };
+  auto lds_of = [&](int kt, int d) {
+    const uint32_t at = lds0 + static_cast<uint32_t>((kt % S::STAGES) * S::kStageBytes) +
+                        static_cast<uint32_t>(wave) * 1024u +
+                        (d < S::kDmaA ? d * kLdsStep : S::kStageA + (d - S::kDmaA) * kLdsStep);
+    return static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(at));
+  };
+  auto load_of = [&](const GroupedTile &t, int kt, int d) {
+    int4_t ra = t.rsrc_a, rb = t.rsrc_b;
+    if (d < S::kDmaA) {
+      if constexpr (kTransA) ra = k_rows_rsrc(t.pa, lda, t.m0, t.C, kt);
     } else {
-      const int per = a.tiles_m * a.tiles_n;
-      const int e = static_cast<int>(u / per);
-      const TileCoord tc = tile_of(u - static_cast<int64_t>(e) * per, a.tiles_m, a.tiles_n, kGemmGroupM);
-      const GroupRows g = group_rows(__builtin_amdgcn_readfirstlane(a.offsets[e]),
-                                     __builtin_amdgcn_readfirstlane(a.offsets[e + 1]), a.T);
-      m0 = static_cast<int>(tc.tm) * S::BM;
-      n0 = static_cast<int>(tc.tn) * S::BN;
-      rows = min(S::BM, a.N - m0);
-      C = g.end - g.begin;
-      pa = a.A + static_cast<int64_t>(g.begin) * lda;
-      pb = a.B + static_cast<int64_t>(g.begin) * ldb;
-      pd = a.D + (static_cast<int64_t>(e) * a.N + m0) * cols;
+      if constexpr (kTransB) rb = k_rows_rsrc(t.pb, ldb, t.n0, t.C, kt);
     }
-    // A sum over nothing still walks one K tile, all of it out of range: zeros.
-    const int KT = max(1, (C + S::BK - 1) / S::BK);
+    const DmaArgs g = dma_args(ra, rb, t.C, kt * S::BK, d);
+    lds_dma_b128(g.rsrc, g.voffset, lds_of(kt, d));
+  };
+  auto load_ahead = [&](const GroupedTile &t) {
+#pragma unroll
+    for (int s = 0; s < grouped_ahead<S>(); ++s)
+#pragma unroll
+      for (int d = 0; d < S::kDmaPerStage; ++d) load_of(t, s, d);
+  };
 
-    // Buffer descriptors: of a whole panel where the contraction is
-    // contiguous; of K tile kt's rows of it, from column `col0` on, where it
-    // is not (rows past the contraction's end read as zeros; columns past the
-    // operand's own only reach outputs that are not stored).
-    int4_t rsrc_a{}, rsrc_b{};
-    if constexpr (!kTransA) rsrc_a = make_buffer_rsrc(pa, static_cast<uint32_t>(rows) * lda * 2u);
-    if constexpr (!kTransB) rsrc_b = make_buffer_rsrc(pb, static_cast<uint32_t>(min(S::BN, cols - n0)) * ldb * 2u);
-    auto k_rows_rsrc = [&](const uint16_t *p, int ld, int col0, int kt) {
-      const int k0 = kt * S::BK;
-      const int have = min(S::BK, C - k0);
-      return make_buffer_rsrc(p + static_cast<int64_t>(k0) * ld + col0,
-                              have > 0 ? static_cast<uint32_t>(have) * ld * 2u - static_cast<uint32_t>(col0) * 2u : 0u);
-    };
-
-    // Re-materialised inside the tile loop, as in gemm_kernel: this lane's
-    // byte offset in each operand, and the bytes from one load instruction's
-    // rows to the next's.
-    uint32_t off_a = kTransA ? (ta_row * lda + ta_col) * 2u
-                             : static_cast<uint32_t>(ld_row) * lda * 2u + static_cast<uint32_t>(ld_kcol) * 2u;
-    uint32_t step_a = static_cast<uint32_t>(kTransA ? TileA::kRowsPerDma * S::kWaves : kRowStep) * lda * 2u;
-    int kcol = ld_kcol;
-    asm volatile("" : "+v"(off_a), "+v"(kcol), "+s"(step_a));
-    uint32_t off_b = off_a, step_b = step_a;  // alike where the operands are
-    if constexpr (OP != kGroupForward) {
-      off_b = (tb_row * ldb + tb_col) * 2u;
-      step_b = static_cast<uint32_t>(TileB::kRowsPerDma * S::kWaves) * ldb * 2u;
-      asm volatile("" : "+v"(off_b), "+s"(step_b));
+  GroupedTile cur;
+  if (!next(&cur)) return;
+  lane_offsets();
+  load_ahead(cur);
+  constexpr int kStores = S::kWaveM * S::kWaveN / 512;  // per wave and tile, 16 bytes a lane
+  bool stores = false;
+  for (;;) {
+    lane_offsets();
+    auto load_one = [&](int kt, int d) { load_of(cur, kt, d); };
+    // Operand addresses, made new for every tile: what follows from them would
+    // otherwise be worked out ahead of the tile loop and spilled across the
+    // epilogue, and a spill's reload waits for every load in flight.  Of a
+    // transposed operand all of them, in both stages of the early-free ring
+    // (the second lies past the instruction's offset): worked out beside the
+    // MFMAs they took issue slots (8192 rows x 4096 x 4096 wgrad 195 us).
+    constexpr int kBases = S::EARLY_FREE ? 2 : 1;
+    static_assert(!S::EARLY_FREE || S::STAGES == 2, "a base for each stage");
+    uint32_t rd_a = a_row_base, rd_b = b_row_base, rd_swz = static_cast<uint32_t>(frag_kchunk ^ frag_swz) * 16;
+    uint32_t rt_a[kBases][kTransA ? S::kFragM : 1], rt_b[kBases][kTransB ? S::kFragN : 1];
+    if constexpr (!kTransA || !kTransB) asm volatile("" : "+v"(rd_a), "+v"(rd_b), "+v"(rd_swz));
+#pragma unroll
+    for (int st = 0; st < kBases; ++st) {
+#pragma unroll
+      for (int i = 0; i < (kTransA ? S::kFragM : 0); ++i) {
+        rt_a[st][i] = (ta_base ^ (static_cast<uint32_t>(i) << 5)) + static_cast<uint32_t>(st * S::kStageBytes);
+        asm volatile("" : "+v"(rt_a[st][i]));
+      }
+#pragma unroll
+      for (int j = 0; j < (kTransB ? S::kFragN : 0); ++j) {
+        rt_b[st][j] = (tb_base ^ (static_cast<uint32_t>(j) << 5)) + static_cast<uint32_t>(st * S::kStageBytes);
+        asm volatile("" : "+v"(rt_b[st][j]));
+      }
     }
-
-    struct DmaArgs {
-      int4_t rsrc;
-      uint32_t voffset;
-    };
-    // Load d of a K tile: descriptors ra and rb, and the K tile's first
-    // contraction index (its byte offset and the range test of operands that
-    // are contiguous along it).
-    auto dma_args = [&](int4_t ra, int4_t rb, int k0, int d) -> DmaArgs {
-      const bool is_a = d < S::kDmaA;
-      const int i = is_a ? d : d - S::kDmaA;
-      const uint32_t step = static_cast<uint32_t>(i) * (is_a ? step_a : step_b);
-      if (is_a ? kTransA : kTransB) {
-        // The flipped column: bit 6 of the element index, i.e. bit 7 of the
-        // byte offset within the row.
-        uint32_t off = is_a ? off_a : off_b;
-        if (is_a ? flip(TileA{}, i) : flip(TileB{}, i)) {
-          const uint32_t col = is_a ? ta_col : tb_col;
-          off += ((col ^ 64u) - col) * 2u;
-        }
-        return DmaArgs{is_a ? ra : rb, off + step};
-      }
-      const uint32_t off = k0 + kcol < C ? (is_a ? off_a : off_b) + static_cast<uint32_t>(k0) * 2u : kOobOffset;
-      return DmaArgs{is_a ? ra : rb, off + step};
-    };
-    auto lds_of = [&](int kt, int d) {
-      const uint32_t at = lds0 + static_cast<uint32_t>((kt % S::STAGES) * S::kStageBytes) +
-                          static_cast<uint32_t>(wave) * 1024u +
-                          (d < S::kDmaA ? d * kLdsStep : S::kStageA + (d - S::kDmaA) * kLdsStep);
-      return static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(at));
-    };
-    auto load_one = [&](int kt, int d) {
-      int4_t ra = rsrc_a, rb = rsrc_b;
-      if (d < S::kDmaA) {
-        if constexpr (kTransA) ra = k_rows_rsrc(pa, lda, m0, kt);
-      } else {
-        if constexpr (kTransB) rb = k_rows_rsrc(pb, ldb, n0, kt);
-      }
-      const DmaArgs g = dma_args(ra, rb, kt * S::BK, d);
-      lds_dma_b128(g.rsrc, g.voffset, lds_of(kt, d));
-    };
-
     half8_t fa[2][S::kFragM], fb[2][S::kFragN];
     // Operand block `blk` of K step ks from the stage of K tile kt.
     auto read_block = [&](bool is_a, int blk, int kt, int ks) -> half8_t {
       const uint32_t stage = static_cast<uint32_t>((kt % S::STAGES) * S::kStageBytes);
       if (is_a ? kTransA : kTransB) {
         const uint32_t rb = is_a ? TileA::kRowBytes : TileB::kRowBytes;
-        const uint32_t at =
-            ((is_a ? ta_base : tb_base) ^ (static_cast<uint32_t>(blk) << 5)) + stage + static_cast<uint32_t>(ks) * 32u * rb;
+        const int st = S::EARLY_FREE ? kt & 1 : 0;
+        const uint32_t at = (is_a ? rt_a[st][blk] : rt_b[st][blk]) + (S::EARLY_FREE ? 0u : stage) +
+                            static_cast<uint32_t>(ks) * 32u * rb;
         const half4_t lo = lds_read_transposed(at), hi = lds_read_transposed(at + 4 * rb);
         return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
       }
-      const uint32_t chunk = static_cast<uint32_t>(((ks * 4 + frag_kchunk) ^ frag_swz) * 16);
-      return *reinterpret_cast<const half8_t *>(smem + stage + (is_a ? a_row_base : b_row_base) +
-                                                blk * 16 * S::kRowBytes + chunk);
+      // chunk (4 ks + frag_kchunk) ^ frag_swz of the row
+      return *reinterpret_cast<const half8_t *>(smem + stage + (is_a ? rd_a : rd_b) + blk * 16 * S::kRowBytes +
+                                                (rd_swz ^ static_cast<uint32_t>(ks * 64)));
     };
     auto read_frag = [&](int buf, int kt, int ks, int r) {
       if (r == 0)
@@ -276,10 +435,12 @@ grouped_gemm_kernel(GroupedArgs a) {
 
     float4_t acc[S::kFragM][S::kFragN];
     auto init_acc = [&]() {
+      float zero = 0.0f;
+      asm volatile("" : "+v"(zero));
 #pragma unroll
       for (int i = 0; i < S::kFragM; ++i)
 #pragma unroll
-        for (int j = 0; j < S::kFragN; ++j) acc[i][j] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int j = 0; j < S::kFragN; ++j) acc[i][j] = float4_t{zero, zero, zero, zero};
       // The zeros precede every hand-written MFMA by its wait states
       // (gemm_kernel's accumulator fence).
       static_assert(S::kFragN % 4 == 0, "accumulator fence covers 4 blocks per statement");
@@ -311,11 +472,11 @@ grouped_gemm_kernel(GroupedArgs a) {
         rf_lds = lds_of(tile, 0);
         asm volatile("" : "+s"(rf_lds));
       } else if (part == 2) {
-        rf_a = rsrc_a;
-        if constexpr (kTransA) rf_a = k_rows_rsrc(pa, lda, m0, tile);
+        rf_a = cur.rsrc_a;
+        if constexpr (kTransA) rf_a = k_rows_rsrc(cur.pa, lda, cur.m0, cur.C, tile);
       } else if (part == 3) {
-        rf_b = rsrc_b;
-        if constexpr (kTransB) rf_b = k_rows_rsrc(pb, ldb, n0, tile);
+        rf_b = cur.rsrc_b;
+        if constexpr (kTransB) rf_b = k_rows_rsrc(cur.pb, ldb, cur.n0, cur.C, tile);
       }
     };
 #pragma clang diagnostic push
@@ -324,7 +485,7 @@ grouped_gemm_kernel(GroupedArgs a) {
       const int i = S::mfma_i(idx);
       const int j = S::mfma_j(idx);
       (void)tile;
-      const DmaArgs g = dma_args(rf_a, rf_b, rf_k0, d);
+      const DmaArgs g = dma_args(rf_a, rf_b, cur.C, rf_k0, d);
       const uint32_t lds = rf_lds + (d < S::kDmaA ? d * kLdsStep : S::kStageA + (d - S::kDmaA) * kLdsStep);
       if constexpr (S::DTYPE == kF16)
         asm volatile(
@@ -340,45 +501,203 @@ grouped_gemm_kernel(GroupedArgs a) {
             : "memory", "m0");
     };
 #pragma clang diagnostic pop
-    KernelRingOps<S, decltype(mfma), decltype(read_frag), decltype(load_one), decltype(mfma_load), decltype(prep),
-                  decltype(init_acc)>
-        ops{mfma, read_frag, load_one, mfma_load, prep, init_acc};
-    if constexpr (S::EARLY_FREE)
-      ring_k_loop_ef<S>(ops, KT);
-    else
-      ring_k_loop<S>(ops, KT);
+    using Base = KernelRingOps<S, decltype(mfma), decltype(read_frag), decltype(load_one), decltype(mfma_load),
+                               decltype(prep), decltype(init_acc)>;
+    GroupedRingOps<S, kStores, Base> ops{{mfma, read_frag, load_one, mfma_load, prep, init_acc}, false};
+    // The loop's last barrier comes after every wave's last read of its
+    // operands: the ring is free.
+    grouped_k_loop<S>(ops, cur.KT, stores);
 
-    // ---- epilogue: as gemm_kernel's, in units' rows ------------------------
+    GroupedTile after{};
+    const bool more = next(&after);
+    if constexpr (ALIGNED) {
+      if (more) {
+        lane_offsets();
+        load_ahead(after);
+      }
+    }
+
+    // ---- epilogue ------------------------------------------------------------
     asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
-    workgroup_barrier();  // every wave is done reading the ring
     // The lane, made new for every tile: the epilogue's addresses would
     // otherwise be worked out ahead of the tile loop and spilled.
     int ep_lane = lane;
     asm volatile("" : "+v"(ep_lane));
     const int ep_row = ep_lane % 16;
     const int ep_kgrp = ep_lane / 16;
-    char *const tile = smem + wave * S::kWaveM * S::kStagePitch;
-    const int n = n0 + wn * S::kWaveN;
-    _Float16 *const dst = reinterpret_cast<_Float16 *>(pd) + static_cast<int64_t>(wm * S::kWaveM) * cols + n;
+    const int n = cur.n0 + wn * S::kWaveN;
+    if constexpr (ALIGNED) {
+      // A block row (16 rows) at a time through this wave's part of the
+      // staging area behind the ring, which the loads above do not touch:
+      // 8 bytes of a row per lane in, whole 16-byte pieces of consecutive
+      // columns out.
+      const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
+          cur.pd, 0, static_cast<int>(static_cast<uint32_t>(cur.rows) * cols * 2u), 0x00020000);
+      char *const tile = smem + S::kRingBytes + wave * 16 * S::kStagePitch;
+      constexpr int kPieces = S::kWaveN / 8;
+      constexpr int kPerPass = 64 / kPieces;
+      const int c = n + ep_lane % kPieces * 8;
+      const char *const from = tile + ep_lane / kPieces * S::kStagePitch + ep_lane % kPieces * 16;
+      const int row0 = wm * S::kWaveM + ep_lane / kPieces;
 #pragma unroll
-    for (int i = 0; i < S::kFragM; ++i) {
-      const int r = i * 16 + ep_row;
+      for (int i = 0; i < S::kFragM; ++i) {
+        // Still in AGPRs here: the compiler would read all of them into VGPRs
+        // ahead of the loads above.
 #pragma unroll
-      for (int j = 0; j < S::kFragN; ++j) {
-        half4_t h;
+        for (int j = 0; j < S::kFragN; ++j) asm volatile("" : "+a"(acc[i][j]));
 #pragma unroll
-        for (int e = 0; e < 4; ++e) h[e] = round_out<S::DTYPE>(acc[i][j][e]);
-        *reinterpret_cast<half4_t *>(tile + r * S::kStagePitch + (j * 16 + ep_kgrp * 4) * 2) = h;
+        for (int j = 0; j < S::kFragN; ++j) {
+          half4_t h;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) h[e] = round_out<S::DTYPE>(acc[i][j][e]);
+          *reinterpret_cast<half4_t *>(tile + ep_row * S::kStagePitch + (j * 16 + ep_kgrp * 4) * 2) = h;
+        }
+#pragma unroll
+        for (int r = 0; r < 16; r += kPerPass) {
+          const uint4_v v = *reinterpret_cast<const uint4_v *>(from + r * S::kStagePitch);
+          const uint32_t off = c < cols ? static_cast<uint32_t>(row0 + i * 16 + r) * static_cast<uint32_t>(cols) * 2u +
+                                              static_cast<uint32_t>(c) * 2u
+                                        : kOobOffset;
+          __builtin_amdgcn_raw_buffer_store_b128(v, rsrc, static_cast<int>(off), 0, kStreamed);
+        }
+        __builtin_amdgcn_sched_barrier(0);  // a block row at a time, for the registers
       }
-      __builtin_amdgcn_sched_barrier(0);  // a block row at a time, for the registers
+      stores = true;
+    } else {
+      wait_vmcnt<0>();  // the loads past the last K tile have written their zeros
+      workgroup_barrier();
+      char *const tile = smem + wave * S::kWaveM * S::kStagePitch;
+#pragma unroll
+      for (int i = 0; i < S::kFragM; ++i) {
+#pragma unroll
+        for (int j = 0; j < S::kFragN; ++j) asm volatile("" : "+a"(acc[i][j]));
+#pragma unroll
+        for (int j = 0; j < S::kFragN; ++j) {
+          half4_t h;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) h[e] = round_out<S::DTYPE>(acc[i][j][e]);
+          *reinterpret_cast<half4_t *>(tile + (i * 16 + ep_row) * S::kStagePitch + (j * 16 + ep_kgrp * 4) * 2) = h;
+        }
+        __builtin_amdgcn_sched_barrier(0);  // a block row at a time, for the registers
+      }
+      _Float16 *const dst = reinterpret_cast<_Float16 *>(cur.pd) + static_cast<int64_t>(wm * S::kWaveM) * cols + n;
+      store_wave_tile<S::kWaveM, S::kWaveN, S::kStagePitch>(tile, dst, cols, cur.rows - wm * S::kWaveM, cols - n,
+                                                            a.alignment, ep_lane);
+      __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
+      workgroup_barrier();  // every wave has read its staged tile
+      if (more) {
+        lane_offsets();
+        load_ahead(after);
+      }
     }
-    store_wave_tile<S::kWaveM, S::kWaveN, S::kStagePitch>(tile, dst, cols, rows - wm * S::kWaveM, cols - n, a.alignment,
-                                                          ep_lane);
+    if (!more) break;
+    cur = after;
   }
+  // Nothing of this phase writes to the LDS any more: the loads past the last K
+  // tile, which are older than the stores, have landed in every wave.
+  wait_vmcnt<ALIGNED ? kStores : 0>();
+  workgroup_barrier();
 }
 
-// Expected units of `rows` rows for T rows in E groups whose sizes are not
+// S tiles in whole rounds of all workgroups.  With Q (a quarter of S; S itself
+// for none), a last round that would leave half of the workgroups or more
+// without a tile is cut into quarters instead.
+template <class S, class Q, int OP, bool ALIGNED, int CAP>
+__global__ void __launch_bounds__(S::kThreads) __attribute__((amdgpu_waves_per_eu(S::kWaves / 4, S::kWaves / 4)))
+grouped_gemm_kernel(GroupedArgs a) {
+  constexpr bool kQuarters = !std::is_same_v<S, Q>;
+  static_assert(!kQuarters || (Q::BM * 2 == S::BM && Q::BN * 2 == S::BN && Q::kThreads == S::kThreads),
+                "quarters of a tile");
+  constexpr bool kUnits = OP != kGroupWgrad;
+  // The table lies behind the rings in one allocation, so that the rings start
+  // at LDS address 0 and their offsets fit the instructions.
+  using Table = std::conditional_t<kUnits, GroupTable<CAP>, WgradTable<CAP>>;
+  constexpr int kLds = ring_max(grouped_lds<S, ALIGNED>(), grouped_lds<Q, ALIGNED>());
+  static_assert(kLds + sizeof(Table) <= 160 * 1024, "gfx950 has 160 KiB of LDS per CU");
+  __shared__ __attribute__((aligned(1024))) char smem[kLds + sizeof(Table)];
+  Table &table = *reinterpret_cast<Table *>(smem + kLds);
+
+  const int cols = OP == kGroupForward ? a.N : a.K;
+  const int tiles_n = (cols + S::BN - 1) / S::BN;
+  const int tiles_m = (a.N + S::BM - 1) / S::BM;  // of a group's dW
+  const int grid = static_cast<int>(gridDim.x);
+  const int logical = static_cast<int>(xcd_logical_id(blockIdx.x, grid));
+  int units = 0;
+  int64_t num_tiles;
+  if constexpr (kUnits) {
+    build_group_table(&table, a.offsets, a.E, a.T, S::BM);
+    __syncthreads();
+    units = table_units(&table, a.E);
+    num_tiles = static_cast<int64_t>(units) * tiles_n;
+  } else {
+    build_wgrad_table(&table, a.offsets, a.E, a.T, S::kThreads);
+    __syncthreads();
+    num_tiles = static_cast<int64_t>(a.E) * tiles_m * tiles_n;
+  }
+  // The output rows and first column of big tile u.
+  auto big_tile = [&](int64_t u, int *n0) -> GroupedRows {
+    GroupedRows r;
+    if constexpr (kUnits) {
+      const TileCoord tc = tile_of(u, units, tiles_n, kGemmGroupM);
+      const GroupUnit g = table_unit(&table, a.E, S::BM, static_cast<int>(tc.tm));
+      *n0 = static_cast<int>(tc.tn) * S::BN;
+      r.group = g.group;
+      r.row = g.row;
+      r.rows = min(S::BM, g.end - g.row);
+    } else {
+      const int per = tiles_m * tiles_n;
+      const int at = static_cast<int>(u / per);
+      const TileCoord tc = tile_of(u - static_cast<int64_t>(at) * per, tiles_m, tiles_n, kGemmGroupM);
+      *n0 = static_cast<int>(tc.tn) * S::BN;
+      r.group = __builtin_amdgcn_readfirstlane(table.group[at]);
+      r.begin = __builtin_amdgcn_readfirstlane(table.begin[at]);
+      r.end = __builtin_amdgcn_readfirstlane(table.end[at]);
+      r.row = static_cast<int>(tc.tm) * S::BM;
+      r.rows = min(S::BM, a.N - r.row);
+    }
+    return r;
+  };
+
+  const int64_t whole = num_tiles / grid;
+  const int left = static_cast<int>(num_tiles - whole * grid);
+  const bool quarters = kQuarters && 2 * left <= grid;
+  const int64_t rounds = quarters ? whole : whole + 1;
+  int64_t round = 0;
+  grouped_phase<S, OP, ALIGNED>(a, smem, [&](GroupedTile *t) {
+    if (round == rounds) return false;
+    // Forwards; in wgrad backwards in every other round.
+    const int64_t u = round * grid + (!kUnits && (round & 1) ? grid - 1 - logical : logical);
+    ++round;
+    if (u >= num_tiles) return false;  // only the last round is not whole
+    int n0;
+    const GroupedRows r = big_tile(u, &n0);
+    *t = grouped_tile<OP>(a, r, n0, S::BM, S::BN, S::BK);
+    return true;
+  });
+  if constexpr (!kQuarters) return;
+  if (!quarters) return;
+  // Upper halves first, so that halves without rows come last.
+  int s = logical;
+  grouped_phase<Q, OP, ALIGNED>(a, smem, [&](GroupedTile *t) {
+    for (; s < 4 * left; s += grid) {
+      const int low = s >= 2 * left;
+      const int rest = s - low * 2 * left;
+      int n0;
+      GroupedRows r = big_tile(whole * grid + rest / 2, &n0);
+      r.row += low * Q::BM;
+      r.rows -= low * Q::BM;
+      n0 += rest % 2 * Q::BN;
+      if (r.rows <= 0 || n0 >= cols) continue;
+      *t = grouped_tile<OP>(a, r, n0, Q::BM, Q::BN, Q::BK);
+      s += grid;
+      return true;
+    }
+    return false;
+  });
+}
+
+// Units of `rows` rows to expect for T rows in E groups whose sizes are not
 // known on the host: T / rows whole ones, and half a unit more for each group
 // that can have rows.
 inline int64_t expected_units(int64_t T, int64_t E, int64_t rows) {
@@ -388,39 +707,40 @@ inline int64_t expected_units(int64_t T, int64_t E, int64_t rows) {
   return units < bound ? units : bound;
 }
 
-// The tile with the least estimated time (gemm_default_tile's estimate, with
-// the units expected instead of row tiles).
+// The tile (of kTile256x256, which stands for it with quarters, kTile256x128
+// and kTile128x128) with the least estimated time in rounds of all CUs.  The
+// smaller ones' rates of the 256x256 one are measured (8192x4096x2048 in one
+// group: 97.6 us, 127 and 137 us).
+constexpr int kGroupedCap = 512;  // groups the 256x128 tile's ring leaves room for
 inline GemmTile grouped_default_tile(int op, int64_t T, int64_t N, int64_t K, int64_t E, int num_cus) {
-  int best = kTile256x256;
-  int64_t best_cost = -1;
-  for (int t = 0; t <= kTile128x128; ++t) {
-    const GemmTileShape &s = kGemmTileShapes[t];
-    const int64_t cols = op == kGroupForward ? N : K;
-    const int64_t down = op == kGroupWgrad ? E * ((N + s.bm - 1) / s.bm) : expected_units(T, E, s.bm);
-    const int64_t tiles = down * ((cols + s.bn - 1) / s.bn);
-    const int64_t cost = (tiles + num_cus - 1) / num_cus * s.bm * s.bn * 100 / s.rate_pct;
-    if (best_cost < 0 || cost < best_cost) {
-      best = t;
-      best_cost = cost;
-    }
-  }
-  return static_cast<GemmTile>(best);
+  const int64_t cols = op == kGroupForward ? N : K;
+  auto tiles = [&](int64_t bm, int64_t bn) {
+    return (op == kGroupWgrad ? E * ((N + bm - 1) / bm) : expected_units(T, E, bm)) * ((cols + bn - 1) / bn);
+  };
+  auto rounds = [&](int64_t n) { return (n + num_cus - 1) / num_cus; };
+  // Times in percent of a round of 256x256 tiles.
+  const int64_t small = 100 * rounds(tiles(128, 128)) * 25 / 71;
+  const int64_t mid = 100 * rounds(tiles(256, 128)) * 50 / 77;
+  const int64_t n = tiles(256, 256), left = n % num_cus;
+  const int64_t big = 100 * (n / num_cus) + (left == 0 ? 0 : 2 * left > num_cus ? 100 : 100 * rounds(4 * left) * 25 / 71);
+  if (big < small && (big <= mid || E > kGroupedCap)) return kTile256x256;
+  return mid < small && E <= kGroupedCap ? kTile256x128 : kTile128x128;
 }
 
-template <class S, int OP>
-static hipError_t launch_grouped_shape(GroupedArgs a, int num_cus, hipStream_t stream) {
+template <class S, class Q, int OP, int CAP>
+static hipError_t launch_grouped_shape(const GroupedArgs &a, int num_cus, hipStream_t stream) {
   const int cols = OP == kGroupForward ? a.N : a.K;
-  a.tiles_n = (cols + S::BN - 1) / S::BN;
-  a.tiles_m = (a.N + S::BM - 1) / S::BM;
-  a.alignment = row_alignment(a.D, cols);
-  int64_t grid;
-  if constexpr (OP == kGroupWgrad) {
-    grid = static_cast<int64_t>(a.E) * a.tiles_m * a.tiles_n;
-  } else {
-    const int64_t tiles = unit_bound(a.T, a.E, S::BM) * a.tiles_n;
-    grid = tiles < num_cus ? tiles : num_cus;
-  }
-  hipLaunchKernelGGL((grouped_gemm_kernel<S, OP>), dim3(static_cast<unsigned>(grid)), dim3(S::kThreads), 0, stream, a);
+  // No more workgroups than there can be tiles, or quarters of tiles.
+  const int64_t down =
+      OP == kGroupWgrad ? static_cast<int64_t>(a.E) * ((a.N + S::BM - 1) / S::BM) : unit_bound(a.T, a.E, S::BM);
+  const int64_t tiles = (std::is_same_v<S, Q> ? 1 : 4) * down * ((cols + S::BN - 1) / S::BN);
+  const dim3 grid(static_cast<unsigned>(tiles < num_cus ? tiles : num_cus));
+  // The gradients' rows are a multiple of 8 elements long, and their outputs
+  // 16-byte aligned.
+  if (OP != kGroupForward || a.alignment == 16)
+    hipLaunchKernelGGL((grouped_gemm_kernel<S, Q, OP, true, CAP>), grid, dim3(S::kThreads), 0, stream, a);
+  else
+    hipLaunchKernelGGL((grouped_gemm_kernel<S, Q, OP, OP != kGroupForward, CAP>), grid, dim3(S::kThreads), 0, stream, a);
   return hipGetLastError();
 }
 
@@ -428,17 +748,14 @@ template <int DT, int OP>
 static hipError_t launch_grouped_op(const void *A, const void *B, const int *offsets, void *D, int T, int N, int K, int E,
                                     int num_cus, hipStream_t stream) {
   using Big = std::conditional_t<DT == kF16, GemmDefault, GemmBf16>;
+  using Mid = GemmTile256x128<DT, kGemmTileShapes[kTile256x128].stages>;
+  using Small = GemmTile128x128<DT, kGemmTileShapes[kTile128x128].stages>;
   const GroupedArgs a{static_cast<const uint16_t *>(A), static_cast<const uint16_t *>(B), static_cast<uint16_t *>(D),
-                      offsets, T, N, K, E, 0, 0, 0};
+                      offsets, T, N, K, E, row_alignment(D, OP == kGroupForward ? N : K)};
   switch (grouped_default_tile(OP, T, N, K, E, num_cus)) {
-    case kTile256x128:
-      return launch_grouped_shape<GemmTile256x128<DT, kGemmTileShapes[kTile256x128].stages>, OP>(a, num_cus, stream);
-    case kTile128x256:
-      return launch_grouped_shape<GemmTile128x256<DT, kGemmTileShapes[kTile128x256].stages>, OP>(a, num_cus, stream);
-    case kTile128x128:
-      return launch_grouped_shape<GemmTile128x128<DT, kGemmTileShapes[kTile128x128].stages>, OP>(a, num_cus, stream);
-    default:
-      return launch_grouped_shape<Big, OP>(a, num_cus, stream);
+    case kTile256x128: return launch_grouped_shape<Mid, Mid, OP, kGroupedCap>(a, num_cus, stream);
+    case kTile128x128: return launch_grouped_shape<Small, Small, OP, kMaxGroups>(a, num_cus, stream);
+    default: return launch_grouped_shape<Big, Small, OP, kMaxGroups>(a, num_cus, stream);
   }
 }
 

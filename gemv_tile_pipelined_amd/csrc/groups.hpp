@@ -115,16 +115,17 @@ __device__ inline bool find_unit(const int *__restrict__ offsets, int E, int T, 
 }
 
 // The groups' units as a table in LDS, for persistent kernels that look up
-// one unit after another.
+// one unit after another.  CAP: the most groups it holds.
+template <int CAP>
 struct GroupTable {
-  int upto[kMaxGroups];   // units of groups 0 .. e
-  int begin[kMaxGroups];  // rows of group e
-  int end[kMaxGroups];
+  int upto[CAP];       // units of groups 0 .. e
+  int begin[CAP + 1];  // rows of group e: begin[e] .. max(begin[e], begin[e + 1]) - 1
 };
 
 // Fills the table (the first wave of the workgroup; the caller places a
 // barrier before the first use).
-__device__ inline void build_group_table(GroupTable *table, const int *__restrict__ offsets, int E, int T, int rows) {
+template <int CAP>
+__device__ inline void build_group_table(GroupTable<CAP> *table, const int *__restrict__ offsets, int E, int T, int rows) {
   if (threadIdx.x >= 64) return;
   const int lane = static_cast<int>(threadIdx.x);
   int before = 0;
@@ -135,14 +136,20 @@ __device__ inline void build_group_table(GroupTable *table, const int *__restric
     if (e < E) {
       table->upto[e] = upto;
       table->begin[e] = g.begin;
-      table->end[e] = g.end;
     }
+    if (e == E - 1) table->begin[E] = g.end;
     before = __builtin_amdgcn_readlane(upto, 63);
   }
 }
 
-// Unit `u` of the table's units (u is wave-uniform and below upto[E - 1]).
-__device__ inline GroupUnit table_unit(const GroupTable *table, int E, int rows, int u) {
+template <int CAP>
+__device__ inline int table_units(const GroupTable<CAP> *table, int E) {
+  return __builtin_amdgcn_readfirstlane(table->upto[E - 1]);
+}
+
+// Unit `u` of the table's units (u is wave-uniform and below table_units()).
+template <int CAP>
+__device__ inline GroupUnit table_unit(const GroupTable<CAP> *table, int E, int rows, int u) {
   const int lane = static_cast<int>(threadIdx.x & 63);
   int e = 0;
   for (int e0 = 0; e0 < E; e0 += 64) {
@@ -153,10 +160,11 @@ __device__ inline GroupUnit table_unit(const GroupTable *table, int E, int rows,
     }
   }
   const int before = e > 0 ? table->upto[e - 1] : 0;
+  const int begin = table->begin[e], next = table->begin[e + 1];
   GroupUnit g;
   g.group = __builtin_amdgcn_readfirstlane(e);
-  g.row = __builtin_amdgcn_readfirstlane(table->begin[e] + (u - before) * rows);
-  g.end = __builtin_amdgcn_readfirstlane(table->end[e]);
+  g.row = __builtin_amdgcn_readfirstlane(begin + (u - before) * rows);
+  g.end = __builtin_amdgcn_readfirstlane(next < begin ? begin : next);
   return g;
 }
 

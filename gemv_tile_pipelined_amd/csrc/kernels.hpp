@@ -352,9 +352,9 @@ hipError_t launch_grouped_dgrad(int dtype, const void *A, const void *B, const i
                                 int E, int num_cus, hipStream_t stream);
 hipError_t launch_grouped_wgrad(int dtype, const void *A, const void *B, const int *offsets, void *D, int T, int N, int K,
                                 int E, int num_cus, hipStream_t stream);
-// The output tile of the tiled grouped kernels: op 0 forward, 1 dgrad, 2
-// wgrad, 3 e4m3 forward.
-void grouped_tile(int op, int64_t T, int64_t N, int64_t K, int64_t E, int num_cus, int *rows, int *cols);
+// The output tile of the tiled grouped kernels (op 0 forward, 1 dgrad, 2
+// wgrad), and of the 8-bit ones.
+void grouped_plan_tile(int op, int64_t T, int64_t N, int64_t K, int64_t E, int num_cus, int *rows, int *cols);
 void fp8_tile(bool grouped, int64_t M, int64_t N, int64_t E, int num_cus, int *rows, int *cols);
 
 }  // namespace gt

@@ -557,8 +557,8 @@ int gemm_fp8_bf16(const void *A, const float *scale_A, const void *B, const floa
  *
  * FP32 accumulation and one rounding (nearest, ties to even) of each output;
  * results are deterministic.  X and D [T,K] and [T,N], dY and dX [T,N] and
- * [T,K], W and dW [E,N,K], all row-major; inputs 16-byte aligned, outputs
- * 2-byte, offsets and scales 4-byte aligned.
+ * [T,K], W and dW [E,N,K], all row-major; inputs, dX and dW 16-byte aligned,
+ * D 2-byte, offsets and scales 4-byte aligned.
  *   T, N, K, E  sizes >= 0; T <= 2^31 - 512, N, K <= 2^20, E <= 1024;
  *               K % 8 == 0 (16 for 8-bit operands), for the two gradients
  *               N % 8 == 0 as well; dW of fewer than 2^24 blocks of 128 x 128;
@@ -589,18 +589,18 @@ int gemm_grouped_fp8_bf16(const void *X, const float *scale_X, const void *W, co
  * and _fp8_ (3) run on `num_cus` compute units: *rows is the number of a
  * group's rows that one workgroup takes at a time, *cols the columns of the
  * output, and the return value 1 for the kernel that streams W once (few rows
- * for each group), 0 for the tiled one.  Host-only; returns -1 for arguments
- * out of range.
+ * for each group), 0 for the tiled one (a last round of 256x256 16-bit tiles that
+ * would keep at most half of the compute units busy is cut into 128x128 ones).
+ * Host-only; returns -1 for arguments out of range.
  */
 int gemvtile_grouped_plan(int op, int64_t T, int64_t N, int64_t K, int64_t E, int64_t num_cus, int *rows, int *cols);
 
 /*
  * gemvtile_group_unit -- the rows that unit `unit` of a grouped product covers
  * when every group's rows are cut into units of `rows`, as the kernels work it
- * out from the offsets (here in host memory), and the most units that the
- * launch allows for.  Writes the group, its unit's first row and one past its
- * last; returns the number of units allowed for, -1 for a unit past the last
- * one, -2 for arguments out of range.
+ * out from the offsets (here in host memory).  Writes the group, its unit's
+ * first row and one past its last; returns the most units that a launch allows
+ * for, -1 for a unit past the last one, -2 for arguments out of range.
  */
 int64_t gemvtile_group_unit(const int32_t *offsets, int64_t E, int64_t T, int64_t rows, int64_t unit, int64_t *group,
                             int64_t *first, int64_t *past);

@@ -189,7 +189,7 @@ def test_grouped_plan(lib):
         kind, rows, cols = gt.grouped_plan(op, 16384, 4096, 4096, 32, 256)
         assert (kind, rows, cols) == ("tiled", 256, 256)
     # a streamed grid that would not fit is tiled instead
-    assert gt.grouped_plan("forward", 8000, 1 << 20, 64, 1000, 256)[0] == "tiled"
+    assert gt.grouped_plan("forward", 4000, 1 << 20, 64, 500, 256)[0] == "tiled"
     for bad in (("forward", 0, 16, 16, 1, 256), ("wgrad", 8, 12, 16, 1, 256), ("fp8", 8, 16, 24, 1, 256),
                 ("forward", 8, 16, 16, 1025, 256)):
         with pytest.raises(gt.GemvTileError):

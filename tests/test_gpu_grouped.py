@@ -125,25 +125,60 @@ def test_forward_odd_columns_in_tiles(env):
     _run(env, "forward", "f16", [300, 17], 261, 136)
 
 
-# Sizes at which each tile is chosen on 256 compute units.
-TILES = {
-    "forward": {(256, 256): ([900, 1100, 1000], 4000, 136), (256, 128): ([700, 1, 1300, 0], 3500, 200),
-                (128, 128): ([200, 90], 300, 264)},
-    "dgrad": {(256, 256): ([900, 1100, 1000], 136, 4000), (256, 128): ([800, 0, 1200], 200, 2000),
-              (128, 128): ([200, 90], 264, 304)},
-    "wgrad": {(256, 256): ([64, 0, 200], 2296, 2200), (256, 128): ([60, 100, 3, 1, 0, 70, 66], 1000, 1032),
-              (128, 128): ([200, 90], 264, 304)},
-    "fp8": {(256, 256): ([900, 1100, 1000], 4000, 272), (128, 128): ([700, 1, 300], 264, 400)},
+def _tiles(op, sizes, N, K):
+    """256 x 256 tiles of a product's output."""
+    down = len(sizes) * -(-N // 256) if op == "wgrad" else sum(-(-n // 256) for n in sizes)
+    return down * -(-(K if op in ("dgrad", "wgrad") else N) // 256)
+
+
+# 256 x 256 tiles on 256 workgroups: a last round that is not whole and not cut into quarters, alone and after a whole
+# one; whole rounds only; quarters after a whole round, and quarters alone.  Remainders of more and fewer than 128 rows.
+ROUNDS = {
+    "one": ([900, 1100, 1000], 4000, 136),
+    "whole": ([700, 1, 1024, 0, 1800], 4090, 72),
+    "whole and quarters": ([2560, 5, 0, 2000, 130], 4000, 72),
+    "two": ([2560, 1500, 0, 3000, 130], 3900, 72),
 }
 
 
-@pytest.mark.parametrize("op,tile", [(op, t) for op in TILES for t in TILES[op]])
-def test_every_tile(env, op, tile):
+@pytest.mark.parametrize("op", ["forward", "dgrad", "wgrad"])
+@pytest.mark.parametrize("kind", list(ROUNDS))
+def test_rounds_of_tiles(env, op, kind):
     torch, gt = env
-    sizes, N, K = TILES[op][tile]
+    sizes, N, K = ROUNDS[kind]
+    if op == "dgrad":
+        N, K = K, N - N % 8
+    if op == "wgrad":
+        sizes = [70, 0, 1, 130]
+        N, K = {"one": (2296, 1104), "whole": (2048, 2048), "whole and quarters": (2304, 2048), "two": (3584, 2048)}[kind]
+    whole, left = divmod(_tiles(op, sizes, N, K), torch.cuda.get_device_properties(0).multi_processor_count)
+    assert {"one": whole == 0 and left > 128, "whole": whole >= 1 and left == 0,
+            "whole and quarters": whole >= 1 and 0 < left <= 128, "two": whole >= 1 and left > 128}[kind], (whole, left)
+    assert gt.grouped_plan(op, sum(sizes), N, K, len(sizes), 256) == ("tiled", 256, 256)
+    _run(env, op, "f16", sizes, N, K)
+
+
+# The smaller tiles, and a plan that expected more rows in each group than there are.
+SMALL = [("forward", (256, 128), [700, 1, 1300, 0], 2001, 200), ("forward", (128, 128), [200, 90], 300, 264),
+         ("dgrad", (256, 128), [800, 0, 1200], 200, 2000), ("dgrad", (128, 128), [200, 90], 264, 304),
+         ("wgrad", (256, 128), [60, 100, 3, 1, 0, 70, 66], 1000, 1032), ("wgrad", (128, 128), [200, 90], 264, 304)]
+
+
+@pytest.mark.parametrize("op,tile,sizes,N,K", SMALL)
+def test_smaller_tiles(env, op, tile, sizes, N, K):
+    torch, gt = env
     cus = torch.cuda.get_device_properties(0).multi_processor_count
     assert gt.grouped_plan(op, sum(sizes), N, K, len(sizes), cus) == ("tiled", *tile)
     _run(env, op, "bf16", sizes, N, K)
+
+
+@pytest.mark.parametrize("tile,sizes,N,K", [(256, [900, 1100, 1000], 4000, 272), (256, [900, 5, 1100, 0, 2600], 4091, 144),
+                                            (128, [700, 1, 300], 264, 400)])
+def test_fp8_tiles(env, tile, sizes, N, K):
+    torch, gt = env
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    assert gt.grouped_plan("fp8", sum(sizes), N, K, len(sizes), cus) == ("tiled", tile, tile)
+    _run(env, "fp8", "bf16", sizes, N, K)
 
 
 @pytest.mark.parametrize("op", ["forward", "dgrad", "wgrad", "fp8"])
