@@ -30,6 +30,9 @@ namespace gt {
 
 namespace {
 
+typedef uint32_t uint4_v __attribute__((ext_vector_type(4)));
+constexpr int kStreamedStore = 2;  // cache policy: nt
+
 struct Fp8Args {
   const uint8_t *A, *B;
   const float *sa, *sb;
@@ -54,10 +57,18 @@ struct Fp8Shape {
   static constexpr int kStageScales = (BM + BN) * kRowBytes;  // then BM + BN scales
   static constexpr int kStageBytes = kStageScales + (BM + BN) * 4;
   static constexpr int kPerStage = kDmaA + kDmaB + 1;
-  static constexpr int kStagePitch = kWaveN * 2 + 16;
-  static constexpr int kStagingBytes = kWaves * kWaveM * kStagePitch;
   static constexpr int kRingBytes = STAGES * kStageBytes;
-  static constexpr int kLdsBytes = kRingBytes > kStagingBytes ? kRingBytes : kStagingBytes;
+  // Staging of the output: blocks of 16 rows x 64 columns per wave behind the
+  // ring, or (rows that are not 16-byte aligned) whole tiles over it.
+  static constexpr bool kLoadAhead = kWaves == 8;
+  static constexpr int kBlockPitch = 64 * 2 + 16;
+  static constexpr int kBlockBytes = kWaves * 16 * kBlockPitch;
+  static constexpr int kStores = kWaveM * kWaveN / 512;  // per wave and tile, 16 bytes a lane
+  static constexpr int kTilePitch = kWaveN * 2 + 16;
+  static constexpr int kTileBytes = kWaves * kWaveM * kTilePitch;
+  static constexpr int lds_bytes(bool aligned) {
+    return aligned ? kRingBytes + kBlockBytes : kRingBytes > kTileBytes ? kRingBytes : kTileBytes;
+  }
   static_assert((BM + BN) / 64 == kWaves, "one scale load per wave and stage");
   static_assert(kRowsPerDma * kWaves % 16 == 0 && BM % (kRowsPerDma * kWaves) == 0 && BN % (kRowsPerDma * kWaves) == 0,
                 "operand loads");
@@ -76,13 +87,13 @@ __device__ inline void lds_dma_b32(int4_t rsrc, uint32_t voffset, uint32_t lds_b
 }
 #pragma clang diagnostic pop
 
-template <class S, int OUT, bool GROUPED, int SB>
+template <class S, int OUT, bool GROUPED, int SB, bool ALIGNED>
 __global__ void __launch_bounds__(S::kThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
 fp8_gemm_kernel(Fp8Args a) {
   // The table lies behind the ring in one allocation, so that the ring starts
   // at LDS address 0 and its offsets fit the instructions.
-  __shared__ __attribute__((aligned(1024))) char smem[S::kLdsBytes + (GROUPED ? sizeof(GroupTable<kMaxGroups>) : 0)];
-  auto &table = *reinterpret_cast<GroupTable<kMaxGroups> *>(smem + S::kLdsBytes);
+  __shared__ __attribute__((aligned(1024))) char smem[S::lds_bytes(ALIGNED) + (GROUPED ? sizeof(GroupTable<kMaxGroups>) : 0)];
+  auto &table = *reinterpret_cast<GroupTable<kMaxGroups> *>(smem + S::lds_bytes(ALIGNED));
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -121,44 +132,98 @@ fp8_gemm_kernel(Fp8Args a) {
     units = table_units(&table, a.E);
   }
   const int64_t num_tiles = static_cast<int64_t>(units) * a.tiles_n;
-  for (int64_t u = xcd_logical_id(blockIdx.x, gridDim.x); u < num_tiles; u += gridDim.x) {
+  // A tile's descriptors, sizes and place in the output.
+  struct Tile {
+    int4_t rsrc_a, rsrc_b, rsrc_s;  // this wave's rows of scales
+    int row, rows, n0;
+  };
+  auto locate = [&](int64_t u) -> Tile {
     const TileCoord tc = tile_of(u, units, a.tiles_n, kGemmGroupM);
     GroupUnit g{0, static_cast<int>(tc.tm) * S::BM, a.M};
     if constexpr (GROUPED) g = table_unit(&table, a.E, S::BM, static_cast<int>(tc.tm));
-    const int n0 = static_cast<int>(tc.tn) * S::BN;
-    const int rows = min(S::BM, g.end - g.row);
-    const int cols = min(S::BN, a.N - n0);
-    const int64_t b_row = static_cast<int64_t>(g.group) * a.N + n0;
-    const int4_t rsrc_a =
-        make_buffer_rsrc(a.A + static_cast<int64_t>(g.row) * a.K, static_cast<uint32_t>(rows) * a.K);
-    const int4_t rsrc_b = make_buffer_rsrc(a.B + b_row * a.K, static_cast<uint32_t>(cols) * a.K);
-    // This wave's rows of scales.
+    Tile t;
+    t.n0 = static_cast<int>(tc.tn) * S::BN;
+    t.row = g.row;
+    t.rows = min(S::BM, g.end - g.row);
+    const int cols = min(S::BN, a.N - t.n0);
+    const int64_t b_row = static_cast<int64_t>(g.group) * a.N + t.n0;
+    t.rsrc_a = make_buffer_rsrc(a.A + static_cast<int64_t>(g.row) * a.K, static_cast<uint32_t>(t.rows) * a.K);
+    t.rsrc_b = make_buffer_rsrc(a.B + b_row * a.K, static_cast<uint32_t>(cols) * a.K);
     const int64_t sb_row =
         SB == 1 ? b_row
-                : static_cast<int64_t>(g.group) * ((a.N + kScaleBlock - 1) / kScaleBlock) + n0 / kScaleBlock;
+                : static_cast<int64_t>(g.group) * ((a.N + kScaleBlock - 1) / kScaleBlock) + t.n0 / kScaleBlock;
     const int sb_rows = SB == 1 ? cols : (cols + kScaleBlock - 1) / kScaleBlock;
-    const int4_t rsrc_s = make_buffer_rsrc((scale_a ? a.sa + static_cast<int64_t>(g.row) * KT : a.sb + sb_row * KT),
-                                           static_cast<uint32_t>(scale_a ? rows : sb_rows) * KT * 4u);
-    uint32_t tile_off = ld_off;
-    int tile_k = ld_k;
+    t.rsrc_s = make_buffer_rsrc((scale_a ? a.sa + static_cast<int64_t>(g.row) * KT : a.sb + sb_row * KT),
+                                static_cast<uint32_t>(scale_a ? t.rows : sb_rows) * KT * 4u);
+    return t;
+  };
+  uint32_t tile_off;
+  int tile_k;
+  auto lane_offsets = [&]() {
+    tile_off = ld_off;
+    tile_k = ld_k;
     asm volatile("" : "+v"(tile_off), "+v"(tile_k));
+  };
+  // Load d of this wave for K tile kt (A's rows, B's rows, then the scales).
+  auto issue_one = [&](const Tile &t, int kt, int d) {
+    const uint32_t stage = lds0 + static_cast<uint32_t>((kt % S::STAGES) * S::kStageBytes);
+    const int k0 = kt * kScaleBlock;
+    if (d < S::kDmaA + S::kDmaB) {
+      const bool is_a = d < S::kDmaA;
+      const int i = is_a ? d : d - S::kDmaA;
+      const uint32_t off = k0 + tile_k < a.K ? tile_off + static_cast<uint32_t>(k0) : kOobOffset;
+      lds_dma_b128(is_a ? t.rsrc_a : t.rsrc_b, off + i * ld_step,
+                   __builtin_amdgcn_readfirstlane(stage + (is_a ? 0 : S::kStageA) + (i * S::kWaves + wave) * 1024));
+    } else {
+      lds_dma_b32(t.rsrc_s, scale_off + static_cast<uint32_t>(kt) * 4u,
+                  __builtin_amdgcn_readfirstlane(stage + S::kStageScales + static_cast<uint32_t>(wave) * 256u));
+    }
+  };
 
-    // Load d of this wave for K tile kt (A's rows, B's rows, then the scales).
-    auto issue_one = [&](int kt, int d) {
-      const uint32_t stage = lds0 + static_cast<uint32_t>((kt % S::STAGES) * S::kStageBytes);
-      const int k0 = kt * kScaleBlock;
-      if (d < S::kDmaA + S::kDmaB) {
-        const bool is_a = d < S::kDmaA;
-        const int i = is_a ? d : d - S::kDmaA;
-        const uint32_t off = k0 + tile_k < a.K ? tile_off + static_cast<uint32_t>(k0) : kOobOffset;
-        lds_dma_b128(is_a ? rsrc_a : rsrc_b, off + i * ld_step,
-                     __builtin_amdgcn_readfirstlane(stage + (is_a ? 0 : S::kStageA) + (i * S::kWaves + wave) * 1024));
-      } else {
-        lds_dma_b32(rsrc_s, scale_off + static_cast<uint32_t>(kt) * 4u,
-                    __builtin_amdgcn_readfirstlane(stage + S::kStageScales + static_cast<uint32_t>(wave) * 256u));
-      }
-    };
+  // Loads are issued in two parts.  The first half of each wave column's
+  // blocks of B lies in the even loads of B's rows, the second in the odd.
+  constexpr int kEarly = S::kDmaA + S::kDmaB / 2;  // A and B's first half
+  constexpr int kLate = S::kPerStage - kEarly;     // the scales, then B's second half
+  auto issue_early = [&](const Tile &t, int kt, int k) {
+    issue_one(t, kt, k < S::kDmaA ? k : S::kDmaA + 2 * (k - S::kDmaA));
+  };
+  auto issue_late = [&](const Tile &t, int kt, int k) {
+    issue_one(t, kt, k == 0 ? S::kDmaA + S::kDmaB : S::kDmaA + 2 * (k - 1) + 1);
+  };
+  static_assert(S::kDmaB % 2 == 0 && kRowStep * 2 == S::kWaveN, "a half of a wave column's rows per load of B");
+  auto load_ahead = [&](const Tile &t) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+#pragma unroll
+      for (int k = 0; k < kEarly; ++k) issue_early(t, s, k);
+#pragma unroll
+      for (int k = 0; k < kLate; ++k) issue_late(t, s, k);
+    }
+  };
 
+  int64_t u = xcd_logical_id(blockIdx.x, gridDim.x);
+  if (u >= num_tiles) return;
+  Tile cur = locate(u);
+  lane_offsets();
+  load_ahead(cur);
+  bool stores = false;  // of the tile before, younger than the loads ahead
+  // Until all loads but the last `count` are complete, those stores aside.
+  auto wait_loads = [&](auto count, bool and_stores) {
+    constexpr int kCount = decltype(count)::value;
+    if (ALIGNED && and_stores)
+      wait_vmcnt<kCount + S::kStores>();
+    else
+      wait_vmcnt<kCount>();
+  };
+  using Ahead = std::integral_constant<int, kLate - 1 + S::kPerStage>;   // K tile 0 but for B's second half
+  using AtFirst = std::integral_constant<int, kEarly + kLate>;
+  using AtSecond = std::integral_constant<int, kLate - 1 + kEarly>;
+  for (;;) {
+    lane_offsets();
+    // A wave whose rows lie behind the last one loads its share, and leaves the
+    // matrix units to the wave that shares its SIMD (wave 4 above or below: 128
+    // rows away).
+    const bool idle = wm * S::kWaveM >= cur.rows;
     // Operands in registers: all 16-row blocks of A for a K tile, and the
     // current and next block of B; scales of A's rows (times the one of B's
     // columns if they share it) of this K tile and the one before.
@@ -189,17 +254,6 @@ fp8_gemm_kernel(Fp8Args a) {
         acc[i][j][e] = __builtin_fmaf(part[i][e], SB == 1 ? sa[buf][i] * sbv[j & 1][e] : sa[buf][i], acc[i][j][e]);
       asm volatile("" : "+v"(acc[i][j]));  // here, and not where the sums are used next
     };
-    // Loads are issued in two parts.  The first half of each wave column's
-    // blocks of B lies in the even loads of B's rows, the second in the odd.
-    constexpr int kEarly = S::kDmaA + S::kDmaB / 2;  // A and B's first half
-    constexpr int kLate = S::kPerStage - kEarly;     // the scales, then B's second half
-    auto issue_early = [&](int kt, int k) {
-      issue_one(kt, k < S::kDmaA ? k : S::kDmaA + 2 * (k - S::kDmaA));
-    };
-    auto issue_late = [&](int kt, int k) {
-      issue_one(kt, k == 0 ? S::kDmaA + S::kDmaB : S::kDmaA + 2 * (k - 1) + 1);
-    };
-    static_assert(S::kDmaB % 2 == 0 && kRowStep * 2 == S::kWaveN, "a half of a wave column's rows per load of B");
     // One K tile, fixed in order: per MFMA slot the MFMA, the four FMAs of the
     // slot three before it (whose MFMA has long finished), and what has to be
     // read or loaded meanwhile.  B's blocks are read one block ahead.  Two
@@ -219,8 +273,9 @@ fp8_gemm_kernel(Fp8Args a) {
     constexpr int kFirst = (S::kFragN / 2 - 1) * S::kFragM, kSecond = kSlots - S::kFragM;
     static_assert(S::STAGES == 2 && S::kFragM == 4 && S::kFragN % 2 == 0, "the slots' register reuse");
     static_assert(kFirst + kEarly <= kSecond && kLate <= S::kFragM, "a load per slot");
-    auto k_tile = [&](auto parity, int kt) {
+    auto k_tile = [&](auto parity, auto head, int kt) {
       constexpr int P = decltype(parity)::value;
+      constexpr bool kHead = decltype(head)::value;  // K tile 0 or 1
       const char *stage = smem + P * S::kStageBytes;
       const char *other = smem + (1 - P) * S::kStageBytes;
 #pragma unroll
@@ -228,10 +283,12 @@ fp8_gemm_kernel(Fp8Args a) {
         const int i = n % S::kFragM, j = n / S::kFragM;
         if (n == kFirst || n == kSecond) {
           __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
+          // All of K tile kt + 1; or B's second half of kt + 1 and the early
+          // part of kt + 2.
           if (n == kFirst)
-            wait_vmcnt<kEarly + kLate>();  // all of K tile kt + 1
+            wait_loads(AtFirst{}, kHead && stores);
           else
-            wait_vmcnt<kLate - 1 + kEarly>();  // B's second half of kt + 1, the early part of kt + 2
+            wait_loads(AtSecond{}, kHead && P == 0 && stores);
           workgroup_barrier();
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -247,12 +304,12 @@ fp8_gemm_kernel(Fp8Args a) {
         // of range, write zeros that nothing reads.
         if (j + 1 < S::kFragN) {
           if (i == 0) read_b(stage, j + 1);
-          if (n >= kFirst && n < kFirst + kEarly) issue_early(kt + 2, n - kFirst);
+          if (n >= kFirst && n < kFirst + kEarly) issue_early(cur, kt + 2, n - kFirst);
         } else {
           read_a(other, i);
           if (i == 0) read_b(other, 0);
           if (i == S::kFragM - 1) read_scales(other, 1 - P);
-          if (i < kLate) issue_late(kt + 2, i);
+          if (i < kLate) issue_late(cur, kt + 2, i);
         }
         if constexpr (SB == 1) {
           // B's scales of a block, once the slots of the block two before are done.
@@ -263,16 +320,6 @@ fp8_gemm_kernel(Fp8Args a) {
       }
     };
 
-    // Every wave is done with the previous tile's LDS.
-    __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
-    workgroup_barrier();
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-#pragma unroll
-      for (int k = 0; k < kEarly; ++k) issue_early(s, k);
-#pragma unroll
-      for (int k = 0; k < kLate; ++k) issue_late(s, k);
-    }
 #pragma unroll
     for (int i = 0; i < S::kFragM; ++i) {
       part[i] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
@@ -281,53 +328,120 @@ fp8_gemm_kernel(Fp8Args a) {
       for (int j = 0; j < S::kFragN; ++j) acc[i][j] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
     }
     sbv[1] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    wait_vmcnt<kLate - 1 + S::kPerStage>();  // K tile 0 but for B's second half
+    wait_loads(Ahead{}, stores);
     workgroup_barrier();
+    if (idle) {
+      for (int kt = 0; kt < KT; ++kt) {
+        wait_loads(AtFirst{}, stores && kt < 2);
+        workgroup_barrier();
+#pragma unroll
+        for (int k = 0; k < kEarly; ++k) issue_early(cur, kt + 2, k);
+        wait_loads(AtSecond{}, stores && kt < 1);
+        workgroup_barrier();
+#pragma unroll
+        for (int k = 0; k < kLate; ++k) issue_late(cur, kt + 2, k);
+      }
+    } else {
 #pragma unroll
     for (int i = 0; i < S::kFragM; ++i) read_a(smem, i);
     read_b(smem, 0);
     read_scales(smem, 0);
     if constexpr (SB == 1) sbv[0] = *reinterpret_cast<const float4_t *>(smem + sb_base);
+    using Even = std::integral_constant<int, 0>;
+    using Odd = std::integral_constant<int, 1>;
     int kt = 0;
+    if (ALIGNED && KT > 1) {
+      k_tile(Even{}, std::true_type{}, 0);
+      k_tile(Odd{}, std::true_type{}, 1);
+      kt = 2;
+    }
     for (; kt + 1 < KT; kt += 2) {
-      k_tile(std::integral_constant<int, 0>{}, kt);
-      k_tile(std::integral_constant<int, 1>{}, kt + 1);
+      k_tile(Even{}, std::false_type{}, kt);
+      k_tile(Odd{}, std::false_type{}, kt + 1);
     }
     if (kt < KT) {
-      k_tile(std::integral_constant<int, 0>{}, kt);
+      k_tile(Even{}, std::false_type{}, kt);
 #pragma unroll
       for (int m = kSlots - kBehind; m < kSlots; ++m) accumulate(m, 0);
     } else {
 #pragma unroll
       for (int m = kSlots - kBehind; m < kSlots; ++m) accumulate(m, 1);
     }
+    }
 
     // ---- epilogue ------------------------------------------------------------
-    __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
-    wait_vmcnt<0>();      // the loads past the last K tile have written their zeros
-    workgroup_barrier();  // and every wave is done with the ring
+    // Every wave has read its last operands before the loop's last barrier: the
+    // ring is free, and the next tile's first loads go out ahead of this one's
+    // stores (grouped_kernel.hpp).
+    const int64_t next_u = u + gridDim.x;
+    const bool more = next_u < num_tiles;
+    Tile after{};
+    if (more) after = locate(next_u);
+    if constexpr (ALIGNED) {
+      if (more) load_ahead(after);
+    }
     // The lane, made new for every tile (grouped_kernel.hpp).
     int ep_lane = lane;
     asm volatile("" : "+v"(ep_lane));
     const int ep_row = ep_lane % 16;
     const int ep_kgrp = ep_lane / 16;
-    char *const tile = smem + wave * S::kWaveM * S::kStagePitch;
-    const int n = n0 + wn * S::kWaveN;
-    _Float16 *const dst =
-        reinterpret_cast<_Float16 *>(a.D) + (static_cast<int64_t>(g.row) + wm * S::kWaveM) * a.N + n;
+    const int n = cur.n0 + wn * S::kWaveN;
+    auto rounded = [&](int i, int j) {
+      half4_t h;
 #pragma unroll
-    for (int i = 0; i < S::kFragM; ++i) {
-      const int r = i * 16 + ep_row;
+      for (int e = 0; e < 4; ++e) h[e] = round_out<OUT>(acc[i][j][e]);
+      return h;
+    };
+    if constexpr (ALIGNED) {
+      if (!idle) {
+      uint16_t *const pd = a.D + static_cast<int64_t>(cur.row) * a.N;
+      const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
+          pd, 0, static_cast<int>(static_cast<uint32_t>(cur.rows) * a.N * 2u), 0x00020000);
+      char *const block = smem + S::kRingBytes + wave * 16 * S::kBlockPitch;
+      const char *const from = block + ep_lane / 8 * S::kBlockPitch + ep_lane % 8 * 16;
+      const int row0 = wm * S::kWaveM + ep_lane / 8;
 #pragma unroll
-      for (int j = 0; j < S::kFragN; ++j) {
-        half4_t h;
+      for (int i = 0; i < S::kFragM; ++i) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) h[e] = round_out<OUT>(acc[i][j][e]);
-        *reinterpret_cast<half4_t *>(tile + r * S::kStagePitch + (j * 16 + ep_kgrp * 4) * 2) = h;
+        for (int j0 = 0; j0 < S::kFragN; j0 += 4) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<half4_t *>(block + ep_row * S::kBlockPitch + (j * 16 + ep_kgrp * 4) * 2) =
+                rounded(i, j0 + j);
+          const int c = n + j0 * 16 + ep_lane % 8 * 8;
+#pragma unroll
+          for (int r = 0; r < 16; r += 8) {
+            const uint4_v v = *reinterpret_cast<const uint4_v *>(from + r * S::kBlockPitch);
+            const uint32_t off =
+                c < a.N ? static_cast<uint32_t>(row0 + i * 16 + r) * static_cast<uint32_t>(a.N) * 2u +
+                              static_cast<uint32_t>(c) * 2u
+                        : kOobOffset;
+            __builtin_amdgcn_raw_buffer_store_b128(v, rsrc, static_cast<int>(off), 0, kStreamedStore);
+          }
+        }
       }
+      }
+      stores = !idle;
+    } else {
+      wait_vmcnt<0>();  // the loads past the last K tile have written their zeros
+      workgroup_barrier();
+      char *const tile = smem + wave * S::kWaveM * S::kTilePitch;
+#pragma unroll
+      for (int i = 0; i < S::kFragM; ++i)
+#pragma unroll
+        for (int j = 0; j < S::kFragN; ++j)
+          *reinterpret_cast<half4_t *>(tile + (i * 16 + ep_row) * S::kTilePitch + (j * 16 + ep_kgrp * 4) * 2) = rounded(i, j);
+      _Float16 *const dst =
+          reinterpret_cast<_Float16 *>(a.D) + (static_cast<int64_t>(cur.row) + wm * S::kWaveM) * a.N + n;
+      store_wave_tile<S::kWaveM, S::kWaveN, S::kTilePitch>(tile, dst, a.N, cur.rows - wm * S::kWaveM, a.N - n,
+                                                           a.alignment, ep_lane);
+      __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
+      workgroup_barrier();  // every wave has read its staged tile
+      if (more) load_ahead(after);
     }
-    store_wave_tile<S::kWaveM, S::kWaveN, S::kStagePitch>(tile, dst, a.N, rows - wm * S::kWaveM, a.N - n, a.alignment,
-                                                          ep_lane);
+    if (!more) break;
+    cur = after;
+    u = next_u;
   }
 }
 
@@ -341,13 +455,24 @@ hipError_t launch_shape(Fp8Args a, int num_cus, hipStream_t stream) {
   const int64_t units = GROUPED ? unit_bound(a.M, a.E, S::BM) : (a.M + S::BM - 1) / S::BM;
   const int64_t tiles = units * a.tiles_n;
   // Workgroups that fit the CUs at once: by LDS, and two waves to a SIMD.
-  constexpr int kLds = S::kLdsBytes + (GROUPED ? static_cast<int>(sizeof(GroupTable<kMaxGroups>)) : 0);
-  constexpr int kByLds = 160 * 1024 / kLds, kByWaves = 8 / S::kWaves;
-  constexpr int kPerCu = kByLds < kByWaves ? kByLds : kByWaves;
-  static_assert(kPerCu >= 1, "a workgroup fits a CU");
-  const int64_t fit = static_cast<int64_t>(num_cus) * kPerCu;
-  const dim3 grid(static_cast<unsigned>(tiles < fit ? tiles : fit));
-  hipLaunchKernelGGL((fp8_gemm_kernel<S, OUT, GROUPED, SB>), grid, dim3(S::kThreads), 0, stream, a);
+  auto launch = [&](auto aligned) {
+    constexpr bool kAligned = decltype(aligned)::value;
+    constexpr int kLds = S::lds_bytes(kAligned) + (GROUPED ? static_cast<int>(sizeof(GroupTable<kMaxGroups>)) : 0);
+    constexpr int kByLds = 160 * 1024 / kLds, kByWaves = 8 / S::kWaves;
+    constexpr int kPerCu = kByLds < kByWaves ? kByLds : kByWaves;
+    static_assert(kPerCu >= 1, "a workgroup fits a CU");
+    const int64_t fit = static_cast<int64_t>(num_cus) * kPerCu;
+    const dim3 grid(static_cast<unsigned>(tiles < fit ? tiles : fit));
+    hipLaunchKernelGGL((fp8_gemm_kernel<S, OUT, GROUPED, SB, kAligned>), grid, dim3(S::kThreads), 0, stream, a);
+  };
+  // A tile's rows have to fit a descriptor's range of the output as well.
+  if constexpr (S::kLoadAhead) {
+    if (a.alignment == 16 && static_cast<int64_t>(a.N) * S::BM * 2 < (int64_t{1} << 31)) {
+      launch(std::true_type{});
+      return hipGetLastError();
+    }
+  }
+  launch(std::false_type{});
   return hipGetLastError();
 }
 
