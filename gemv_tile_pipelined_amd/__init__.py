@@ -54,7 +54,6 @@ __all__ = [
     "device_caps",
     "ring_trace",
     "alloc_splitk_workspace",
-    "xcd_block_id",
     "grouped_plan",
     "group_unit",
 ]
@@ -100,7 +99,6 @@ EXPORTED_SYMBOLS = (
     "gemm_grouped_wgrad_bf16",
     "gemm_grouped_fp8_f16",
     "gemm_grouped_fp8_bf16",
-    "gemvtile_xcd_block_id",
     "gemvtile_grouped_plan",
     "gemvtile_group_unit",
 )
@@ -195,8 +193,6 @@ def load_library(path: str = LIBRARY_PATH) -> ctypes.CDLL:
             call = getattr(lib, f"{name}_{fmt}")
             call.argtypes = [*args, vp]
             call.restype = c_int
-    lib.gemvtile_xcd_block_id.argtypes = [i64, i64]
-    lib.gemvtile_xcd_block_id.restype = i64
     lib.gemvtile_grouped_plan.argtypes = [c_int] + [i64] * 5 + [intp] * 2
     lib.gemvtile_grouped_plan.restype = c_int
     lib.gemvtile_group_unit.argtypes = [ctypes.POINTER(ctypes.c_int32)] + [i64] * 4 + [i64p] * 3
@@ -469,10 +465,6 @@ def tile_coord(t: int, tiles_m: int, tiles_n: int, group_m: int):
 
 def xcd_logical_id(w: int, grid: int) -> int:
     return int(load_library().gemvtile_xcd_logical_id(w, grid))
-
-
-def xcd_block_id(w: int, grid: int) -> int:
-    return int(load_library().gemvtile_xcd_block_id(w, grid))
 
 
 def gemm_config() -> dict:

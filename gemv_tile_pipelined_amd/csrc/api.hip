@@ -344,11 +344,6 @@ int64_t gemvtile_xcd_logical_id(int64_t w, int64_t grid) {
   return gt::xcd_logical_id(w, grid);
 }
 
-int64_t gemvtile_xcd_block_id(int64_t w, int64_t grid) {
-  if (grid <= 0 || w < 0 || w >= grid) return -1;
-  return gt::xcd_block_id(w, grid);
-}
-
 void gemvtile_gemm_config(int *bm, int *bn, int *bk, int *stages, int *threads, int *group_m) {
   if (bm) *bm = gt::kGemmBM;
   if (bn) *bn = gt::kGemmBN;

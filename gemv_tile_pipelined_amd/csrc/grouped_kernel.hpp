@@ -32,11 +32,11 @@
 // Between two tiles.  Contractions are short here (a group's rows in wgrad, a
 // projection's width), so a tile's start and end count.  The first loads of the
 // next tile go out as soon as every wave has read its last operands, before
-// this tile's results are rounded and stored; these leave straight from the
-// registers (16 bytes a lane once v_permlane16_swap has joined the halves of
-// two blocks) by buffer stores, always the same number of them, so that the
-// next tile's waits can count them.  Outputs whose rows are not 16-byte
-// aligned go through LDS instead (tile_store.hpp), before the next tile's loads.
+// this tile's results are rounded and stored.  These pass, a block row at a
+// time, through a staging area behind the ring and leave as whole lines by
+// buffer stores, always the same number of them, so that the next tile's waits
+// can count them.  Outputs whose rows are not 16-byte aligned are staged whole
+// over the ring instead (tile_store.hpp), before the next tile's loads.
 #pragma once
 
 #include "gemm_kernel.hpp"
@@ -600,9 +600,22 @@ __device__ __attribute__((always_inline)) inline void grouped_phase(const Groupe
   workgroup_barrier();
 }
 
+// Estimated time, in percent of a round of 256x256 tiles, of `n` of them on
+// `grid` workgroups and `more` quarters, when a last round that would leave half
+// of the workgroups or more without a tile (or any, if there are quarters
+// anyway) is cut into quarters.  128x128 tiles have 71 % of the bigger ones'
+// rate (8192x4096x2048 in one group: 137 us and 97.6 us).
+__host__ __device__ inline int64_t big_rounds(int64_t n, int64_t more, int64_t grid) {
+  const int64_t left = n % grid;
+  if (more == 0 && 2 * left > grid) return 100 * (n / grid + 1);
+  return 100 * (n / grid) + (4 * left + more + grid - 1) / grid * (100 * 25 / 71);
+}
+
 // S tiles in whole rounds of all workgroups.  With Q (a quarter of S; S itself
-// for none), a last round that would leave half of the workgroups or more
-// without a tile is cut into quarters instead.
+// for none), what would be a last round of few tiles is cut into quarters, and
+// where it shortens the estimate so are the groups' last units that have no more
+// than half their rows (at the end, where they read their group's weights
+// again: 8200 rows over 16 groups x 4096 x 2048 149 -> 137 us).
 template <class S, class Q, int OP, bool ALIGNED, int CAP>
 __global__ void __launch_bounds__(S::kThreads) __attribute__((amdgpu_waves_per_eu(S::kWaves / 4, S::kWaves / 4)))
 grouped_gemm_kernel(GroupedArgs a) {
@@ -659,9 +672,24 @@ grouped_gemm_kernel(GroupedArgs a) {
     return r;
   };
 
+  int lights = 0;  // units that are cut into quarters as well
+  if constexpr (kUnits && kQuarters) {
+    lights = table_light_units(&table, a.E, S::BM);
+    const int64_t heavy = num_tiles - static_cast<int64_t>(lights) * tiles_n;
+    const bool apart = big_rounds(heavy, 2 * static_cast<int64_t>(lights) * tiles_n, grid) < big_rounds(num_tiles, 0, grid);
+    __syncthreads();
+    if (apart) {
+      table_drop_light(&table, a.E, S::BM);
+      units -= lights;
+      num_tiles = heavy;
+    } else {
+      lights = 0;
+    }
+    __syncthreads();
+  }
   const int64_t whole = num_tiles / grid;
   const int left = static_cast<int>(num_tiles - whole * grid);
-  const bool quarters = kQuarters && 2 * left <= grid;
+  const bool quarters = kQuarters && (lights > 0 || 2 * left <= grid);
   const int64_t rounds = quarters ? whole : whole + 1;
   int64_t round = 0;
   grouped_phase<S, OP, ALIGNED>(a, smem, [&](GroupedTile *t) {
@@ -677,10 +705,29 @@ grouped_gemm_kernel(GroupedArgs a) {
   });
   if constexpr (!kQuarters) return;
   if (!quarters) return;
-  // Upper halves first, so that halves without rows come last.
-  int s = logical;
+  // Upper halves first, so that halves without rows come last; then the light
+  // units' only halves.
+  const int64_t all = 4 * left + 2 * static_cast<int64_t>(lights) * tiles_n;
+  int64_t at = logical;
   grouped_phase<Q, OP, ALIGNED>(a, smem, [&](GroupedTile *t) {
-    for (; s < 4 * left; s += grid) {
+    for (; at < all; at += grid) {
+      if constexpr (kUnits) {
+        if (at >= 4 * left) {
+          const int rest = static_cast<int>(at - 4 * left);
+          const int k = rest / (2 * tiles_n);
+          const int n0 = (rest - k * 2 * tiles_n) * Q::BN;
+          if (n0 >= cols) continue;
+          const GroupUnit g = table_light_unit(&table, a.E, S::BM, k);
+          GroupedRows r{};
+          r.group = g.group;
+          r.row = g.row;
+          r.rows = g.end - g.row;
+          *t = grouped_tile<OP>(a, r, n0, Q::BM, Q::BN, Q::BK);
+          at += grid;
+          return true;
+        }
+      }
+      const int s = static_cast<int>(at);
       const int low = s >= 2 * left;
       const int rest = s - low * 2 * left;
       int n0;
@@ -690,7 +737,7 @@ grouped_gemm_kernel(GroupedArgs a) {
       n0 += rest % 2 * Q::BN;
       if (r.rows <= 0 || n0 >= cols) continue;
       *t = grouped_tile<OP>(a, r, n0, Q::BM, Q::BN, Q::BK);
-      s += grid;
+      at += grid;
       return true;
     }
     return false;
@@ -721,8 +768,13 @@ inline GemmTile grouped_default_tile(int op, int64_t T, int64_t N, int64_t K, in
   // Times in percent of a round of 256x256 tiles.
   const int64_t small = 100 * rounds(tiles(128, 128)) * 25 / 71;
   const int64_t mid = 100 * rounds(tiles(256, 128)) * 50 / 77;
-  const int64_t n = tiles(256, 256), left = n % num_cus;
-  const int64_t big = 100 * (n / num_cus) + (left == 0 ? 0 : 2 * left > num_cus ? 100 : 100 * rounds(4 * left) * 25 / 71);
+  int64_t big = big_rounds(tiles(256, 256), 0, num_cus);
+  if (op != kGroupWgrad) {
+    // Half the groups' last units are light.
+    const int64_t across = (cols + 255) / 256;
+    const int64_t apart = big_rounds(T / 256 * across, (E < T ? E : T) * across, num_cus);
+    big = apart < big ? apart : big;
+  }
   if (big < small && (big <= mid || E > kGroupedCap)) return kTile256x256;
   return mid < small && E <= kGroupedCap ? kTile256x128 : kTile128x128;
 }

@@ -142,6 +142,61 @@ __device__ inline void build_group_table(GroupTable<CAP> *table, const int *__re
   }
 }
 
+// Groups whose last unit has no more than half its rows ("light").
+template <int CAP>
+__device__ inline bool table_is_light(const GroupTable<CAP> *table, int E, int rows, int e) {
+  if (e >= E) return false;
+  const int tail = max(0, table->begin[e + 1] - table->begin[e]) % rows;
+  return tail != 0 && tail <= rows / 2;
+}
+
+template <int CAP>
+__device__ inline int table_light_units(const GroupTable<CAP> *table, int E, int rows) {
+  const int lane = static_cast<int>(threadIdx.x & 63);
+  int n = 0;
+  for (int e0 = 0; e0 < E; e0 += 64) n += __popcll(__ballot(table_is_light(table, E, rows, e0 + lane)));
+  return n;
+}
+
+// Takes the light units out of the table (the first wave; barriers as for
+// build_group_table).
+template <int CAP>
+__device__ inline void table_drop_light(GroupTable<CAP> *table, int E, int rows) {
+  if (threadIdx.x >= 64) return;
+  const int lane = static_cast<int>(threadIdx.x);
+  int before = 0;
+  for (int e0 = 0; e0 < E; e0 += 64) {
+    const int e = e0 + lane;
+    const int len = e < E ? max(0, table->begin[e + 1] - table->begin[e]) : 0;
+    const int upto = before + wave_scan((len + rows - 1 - rows / 2) / rows);
+    if (e < E) table->upto[e] = upto;
+    before = __builtin_amdgcn_readlane(upto, 63);
+  }
+}
+
+// Light unit `k` (wave-uniform, below table_light_units()).
+template <int CAP>
+__device__ inline GroupUnit table_light_unit(const GroupTable<CAP> *table, int E, int rows, int k) {
+  const int lane = static_cast<int>(threadIdx.x & 63);
+  int e = 0;
+  for (int e0 = 0; e0 < E; e0 += 64) {
+    uint64_t light = __ballot(table_is_light(table, E, rows, e0 + lane));
+    const int n = __popcll(light);
+    if (k < n) {
+      for (; k > 0; --k) light &= light - 1;
+      e = e0 + __builtin_ctzll(light);
+      break;
+    }
+    k -= n;
+  }
+  const int begin = table->begin[e], end = table->begin[e + 1];
+  GroupUnit g;
+  g.group = __builtin_amdgcn_readfirstlane(e);
+  g.row = __builtin_amdgcn_readfirstlane(begin + (end - begin) / rows * rows);
+  g.end = __builtin_amdgcn_readfirstlane(end);
+  return g;
+}
+
 template <int CAP>
 __device__ inline int table_units(const GroupTable<CAP> *table, int E) {
   return __builtin_amdgcn_readfirstlane(table->upto[E - 1]);

@@ -80,16 +80,4 @@ GT_HD inline int64_t xcd_logical_id(int64_t w, int64_t grid) {
   return (w % kNumXcd) * (grid / kNumXcd) + w / kNumXcd;
 }
 
-// Logical id of hardware workgroup `w` when tiles differ in cost: blocks of
-// kXcdBlock consecutive ids go to the XCDs in turn, so neighbours still share
-// an L2 but a run of costly tiles is spread over all XCDs.  A bijection on
-// [0, grid); the ids past the last whole round stay as they are.
-constexpr int64_t kXcdBlock = 32;
-GT_HD inline int64_t xcd_block_id(int64_t w, int64_t grid) {
-  const int64_t whole = grid / (kNumXcd * kXcdBlock) * (kNumXcd * kXcdBlock);
-  if (w >= whole) return w;
-  const int64_t q = w / kNumXcd;
-  return (q / kXcdBlock * kNumXcd + w % kNumXcd) * kXcdBlock + q % kXcdBlock;
-}
-
 }  // namespace gt

@@ -615,13 +615,6 @@ int64_t gemvtile_group_unit(const int32_t *offsets, int64_t E, int64_t T, int64_
  */
 int64_t gemvtile_xcd_logical_id(int64_t w, int64_t grid);
 
-/*
- * gemvtile_xcd_block_id -- the same for launches whose tiles differ in cost
- * (gemm_grouped_wgrad_*): blocks of 32 consecutive ids go to the XCDs in turn;
- * ids past the last whole round of 256 stay as they are.
- */
-int64_t gemvtile_xcd_block_id(int64_t w, int64_t grid);
-
 #ifdef __cplusplus
 }
 #endif

@@ -172,16 +172,6 @@ def test_unit_bound_is_reached():
         assert len(_units(cuts, T, rows)) == gt.group_unit(cuts, T, rows, 0)[3]
 
 
-def test_xcd_block_id_is_a_bijection():
-    for grid in (1, 7, 255, 256, 257, 512, 1000, 2048, 2311):
-        ids = [gt.xcd_block_id(w, grid) for w in range(grid)]
-        assert sorted(ids) == list(range(grid))
-        for w in range(grid - 8):
-            if w + 8 < grid // 256 * 256 and (w // 8) % 32 != 31:
-                assert ids[w + 8] == ids[w] + 1  # the next workgroup of the same XCD takes the next tile
-    assert gt.xcd_block_id(3, 3) == -1 and gt.xcd_block_id(-1, 3) == -1 and gt.xcd_block_id(0, 0) == -1
-
-
 def test_grouped_plan(lib):
     assert gt.grouped_plan("forward", 32, 2048, 2048, 64, 256) == ("stream", 16, 16)
     assert gt.grouped_plan("fp8", 8, 4096, 2048, 64, 256) == ("stream", 16, 16)

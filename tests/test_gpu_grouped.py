@@ -158,9 +158,26 @@ def test_rounds_of_tiles(env, op, kind):
     _run(env, op, "f16", sizes, N, K)
 
 
+# Last units of no more than 128 rows, enough of them that they are set apart: after a whole round and 16 tiles more.
+APART = [1024, 100, 1300, 0, 1, 1790, 128, 64, 129, 127, 3, 90, 50]
+
+
+@pytest.mark.parametrize("op", ["forward", "dgrad"])
+def test_short_units_set_apart(env, op):
+    torch, gt = env
+    N, K = (4000, 136) if op == "forward" else (136, 4000)
+    assert torch.cuda.get_device_properties(0).multi_processor_count == 256
+    across = -(-4000 // 256)
+    light = sum(0 < n % 256 <= 128 for n in APART)
+    heavy = sum(-(-n // 256) for n in APART) - light
+    assert light * across > 128 and heavy * across == 256 + 16
+    assert gt.grouped_plan(op, sum(APART), N, K, len(APART), 256) == ("tiled", 256, 256)
+    _run(env, op, "bf16", APART, N, K)
+
+
 # The smaller tiles, and a plan that expected more rows in each group than there are.
-SMALL = [("forward", (256, 128), [700, 1, 1300, 0], 2001, 200), ("forward", (128, 128), [200, 90], 300, 264),
-         ("dgrad", (256, 128), [800, 0, 1200], 200, 2000), ("dgrad", (128, 128), [200, 90], 264, 304),
+SMALL = [("forward", (256, 128), [700, 1, 1300, 0], 2501, 200), ("forward", (128, 128), [200, 90], 300, 264),
+         ("dgrad", (256, 128), [800, 0, 1200], 200, 2504), ("dgrad", (128, 128), [200, 90], 264, 304),
          ("wgrad", (256, 128), [60, 100, 3, 1, 0, 70, 66], 1000, 1032), ("wgrad", (128, 128), [200, 90], 264, 304)]
 
 
