@@ -451,7 +451,8 @@ int run_gemm_fp8(const void *A, const float *sa, const void *B, const float *sb,
   int cus = 0;
   const int st = current_cu_count(&cus);
   if (st != GEMVTILE_OK) return st;
-  if (M <= gt::kFp8StreamRows) return to_status(gt::launch_stream_fp8(out, A, sa, B, sb, r, D, m, n, k, cus, s));
+  if (M <= gt::kFp8StreamRows) return to_status(gt::launch_stream_fp8(out, A, sa, B, sb, r, D, m, n, k, s));
+  if (gt::fp8_few_tiles(M, N, cus)) return to_status(gt::launch_fp8_deep(out, A, sa, B, sb, r, D, m, n, k, cus, s));
   return to_status(gt::launch_gemm_fp8(out, A, sa, B, sb, r, D, m, n, k, cus, s));
 }
 
@@ -487,10 +488,9 @@ int run_grouped(int op, const void *A, const float *sa, const void *B, const flo
   int cus = 0;
   st = current_cu_count(&cus);
   if (st != GEMVTILE_OK) return st;
-  const int rows = op == kOpForward || op == kOpFp8 ? gt::grouped_stream_rows(T, N, E) : 0;
-  if (rows != 0)
-    return to_status(op == kOpFp8 ? gt::launch_stream_grouped_fp8(dtype, A, sa, B, sb, offsets, D, t, n, k, e, rows, cus, s)
-                                  : gt::launch_stream_grouped(dtype, A, B, offsets, D, t, n, k, e, rows, cus, s));
+  if ((op == kOpForward || op == kOpFp8) && gt::grouped_streams(T, N, E))
+    return to_status(op == kOpFp8 ? gt::launch_stream_grouped_fp8(dtype, A, sa, B, sb, offsets, D, t, n, k, e, cus, s)
+                                  : gt::launch_stream_grouped(dtype, A, B, offsets, D, t, n, k, e, cus, s));
   switch (op) {
     case kOpDgrad: return to_status(gt::launch_grouped_dgrad(dtype, A, B, offsets, D, t, n, k, e, cus, s));
     case kOpWgrad: return to_status(gt::launch_grouped_wgrad(dtype, A, B, offsets, D, t, n, k, e, cus, s));
@@ -562,9 +562,8 @@ int gemvtile_grouped_plan(int op, int64_t T, int64_t N, int64_t K, int64_t E, in
       num_cus > (int64_t{1} << 20) || rows == nullptr || cols == nullptr)
     return -1;
   if (check_grouped_sizes(op, T, N, K, E) != GEMVTILE_OK) return -1;
-  const int stream_rows = op == kOpForward || op == kOpFp8 ? gt::grouped_stream_rows(T, N, E) : 0;
-  if (stream_rows != 0) {
-    *rows = stream_rows;
+  if ((op == kOpForward || op == kOpFp8) && gt::grouped_streams(T, N, E)) {
+    *rows = gt::kStreamUnit;
     *cols = 16;
     return 1;
   }

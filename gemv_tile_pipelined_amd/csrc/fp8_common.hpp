@@ -33,4 +33,13 @@ __device__ inline float4_t mfma_fp8(int8_v a, int8_v b, float4_t c) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
 }
 
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+// As lds_dma_b128, 4 bytes per lane: lane i's dword goes to lds_base + 4 i.
+__device__ inline void lds_dma_b32(int4_t rsrc, uint32_t voffset, uint32_t lds_base) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dword %0, %2, 0 offen lds"
+               : : "v"(voffset), "s"(lds_base), "s"(rsrc) : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
 }  // namespace gt

@@ -78,15 +78,6 @@ struct Fp8Shape {
   __host__ __device__ static constexpr int swz(int row) { return (row & 7) ^ ((row >> 3) & 1); }
 };
 
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-// As lds_dma_b128, 4 bytes per lane: lane i's dword goes to lds_base + 4 i.
-__device__ inline void lds_dma_b32(int4_t rsrc, uint32_t voffset, uint32_t lds_base) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dword %0, %2, 0 offen lds"
-               : : "v"(voffset), "s"(lds_base), "s"(rsrc) : "memory", "m0");
-}
-#pragma clang diagnostic pop
-
 template <class S, int OUT, bool GROUPED, int SB, bool ALIGNED>
 __global__ void __launch_bounds__(S::kThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
 fp8_gemm_kernel(Fp8Args a) {

@@ -45,14 +45,15 @@ GT_HD inline int64_t unit_bound(int64_t T, int64_t E, int64_t rows) {
   return (T - some) / rows + some;
 }
 
-// Rows of a unit when the groups are streamed (stream.hip), by the mean rows
-// of a group, or 0 for the tiled kernels.
-inline int grouped_stream_rows(int64_t T, int64_t N, int64_t E) {
-  const int64_t mean = (T + E - 1) / E;
-  const int rows = mean <= 8 ? 16 : mean <= 16 ? 32 : mean <= 32 ? 64 : 0;
+// Whether the groups are streamed (stream.hip) in units of kStreamUnit rows, by
+// the mean rows of a group, or tiled.  Measured (bf16, us streamed and tiled):
+// 32 groups x 2048 x 2048 with a mean of 4 rows 51 and 62, 8 rows 58 and 66, 12
+// rows 65 and 66, 16 rows 74 and 67, 32 rows 113 and 67; 8 bits, 64 groups x
+// 2048 x 4096: 96 and 125, 110 and 130, 126 and 130, 146 and 131, 228 and 129.
+constexpr int kStreamUnit = 16;
+inline bool grouped_streams(int64_t T, int64_t N, int64_t E) {
   // A grid's threads are counted in 32 bits.
-  if (rows != 0 && unit_bound(T, E, rows) * ((N + 15) / 16) >= (int64_t{1} << 22)) return 0;
-  return rows;
+  return T <= 8 * E && unit_bound(T, E, kStreamUnit) * ((N + 15) / 16) < (int64_t{1} << 22);
 }
 
 }  // namespace gt

@@ -331,14 +331,19 @@ hipError_t launch_quantize_tiles(int dtype, const void *x, void *q, float *scale
 // stream.hip: few rows against weights read once; `out` and dtype kF16 or
 // kBF16, `rows` the rows of a unit (16, 32 or 64).
 hipError_t launch_stream_fp8(int out, const void *x, const float *sx, const void *w, const float *sw, int w_scale_rows,
-                             void *d, int M, int N, int K, int num_cus, hipStream_t stream);
+                             void *d, int M, int N, int K, hipStream_t stream);
 hipError_t launch_stream_grouped(int dtype, const void *x, const void *w, const int *offsets, void *d, int T, int N,
-                                 int K, int E, int rows, int num_cus, hipStream_t stream);
+                                 int K, int E, int num_cus, hipStream_t stream);
 hipError_t launch_stream_grouped_fp8(int out, const void *x, const float *sx, const void *w, const float *sw,
-                                     const int *offsets, void *d, int T, int N, int K, int E, int rows,
-                                     int num_cus, hipStream_t stream);
-// gemm_fp8_* streams B for at most this many rows of A.
-constexpr int64_t kFp8StreamRows = 64;
+                                     const int *offsets, void *d, int T, int N, int K, int E, int num_cus,
+                                     hipStream_t stream);
+// gemm_fp8_* streams B for at most this many rows of A (fp8_deep.hip's figures).
+constexpr int64_t kFp8StreamRows = 4;
+// fp8_deep.hip: dense products of few tiles, those that fp8_few_tiles() is true
+// for.
+bool fp8_few_tiles(int64_t M, int64_t N, int num_cus);
+hipError_t launch_fp8_deep(int out, const void *A, const float *sa, const void *B, const float *sb, int sb_rows, void *D,
+                           int M, int N, int K, int num_cus, hipStream_t stream);
 // fp8_gemm.hip: tiled products of e4m3 operands (K > 0).
 hipError_t launch_gemm_fp8(int out, const void *A, const float *sa, const void *B, const float *sb, int sb_rows, void *D,
                            int M, int N, int K, int num_cus, hipStream_t stream);

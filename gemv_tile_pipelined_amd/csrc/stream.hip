@@ -6,10 +6,10 @@
 //   D[t, n] = sum_b sx[t, b] sw[n / r, b] sum_{k in b} x[t, k] W[n, k]  8-bit
 //
 // Bound by reading W: a workgroup owns 16 or 32 rows of W and all of a unit's
-// rows of x (up to 16 QB of them), so each byte of W is read once per unit.  Its
+// rows of x (up to 16 of them), so each byte of W is read once per unit.  Its
 // waves split K in steps of 128 bytes of a row, which for 8-bit operands is
-// one scale block: a step is one 16x16x128 MFMA per 16 rows of x (two
-// 16x16x32 of 16-bit numbers), W rows first, so that lane l holds outputs
+// one scale block: a step is one 16x16x128 MFMA (two 16x16x32 of
+// 16-bit numbers), W rows first, so that lane l holds outputs
 // n = 4 (l / 16) + e of row l % 16 of x.  Its 8-bit sum is scaled by
 // sx[row] * sw in FP32 as it joins the wave's running sum.  Lane l loads two
 // 16-byte pieces of row l % 16, pieces l / 16 and 4 + l / 16 of the step's
@@ -42,22 +42,22 @@ struct StreamArgs {
 };
 
 // IN: kF16, kBF16 (16-bit operands) or kE4m3.  SW: rows of W per scale (128 or
-// 1).  PB, QB: 16-row blocks of W and of x per workgroup.
+// 1).  PB: 16-row blocks of W per workgroup.
 constexpr int kE4m3 = 2;
-template <int IN, int OUT, int PB, int QB, int WAVES, int UNROLL, bool GROUPED, int SW>
+template <int IN, int OUT, int PB, int WAVES, int UNROLL, bool GROUPED, int SW>
 __global__ void __launch_bounds__(WAVES * 64) stream_kernel(StreamArgs a) {
   constexpr bool kScaled = IN == kE4m3;
   constexpr int kRows = 16 * PB;
-  __shared__ float partial[WAVES][16 * QB][kRows + 1];
+  __shared__ float partial[WAVES][kStreamUnit][kRows + 1];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n0 = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.blocks_n)) * kRows;
   const int unit = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.blocks_n));
-  GroupUnit g{0, unit * 16 * QB, a.T};
+  GroupUnit g{0, unit * kStreamUnit, a.T};
   if constexpr (GROUPED) {
-    if (!find_unit(a.offsets, a.E, a.T, 16 * QB, unit, &g)) return;
+    if (!find_unit(a.offsets, a.E, a.T, kStreamUnit, unit, &g)) return;
   }
-  const int rows = min(16 * QB, g.end - g.row);
+  const int rows = min(kStreamUnit, g.end - g.row);
   const uint32_t rb = static_cast<uint32_t>(a.row_bytes);
   const int steps = (a.row_bytes + kStepBytes - 1) / kStepBytes;
 
@@ -88,18 +88,16 @@ __global__ void __launch_bounds__(WAVES * 64) stream_kernel(StreamArgs a) {
   }
   static_assert(UNROLL <= 4, "the scales of one 16-byte load");
 
-  float4_t acc[PB][QB];
+  float4_t acc[PB];
 #pragma unroll
-  for (int p = 0; p < PB; ++p)
-#pragma unroll
-    for (int q = 0; q < QB; ++q) acc[p][q] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int p = 0; p < PB; ++p) acc[p] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
   // Workgroups that run side by side on an XCD (every eighth) start their
   // waves at different places of K, so that they do not all ask for the same
   // lines of x at once.
   const int first = static_cast<int>((static_cast<unsigned>(wave) + (blockIdx.x >> 3)) % WAVES);
   for (int s0 = first * UNROLL; s0 < steps; s0 += WAVES * UNROLL) {
-    int4_t wv[UNROLL][PB][2], xv[UNROLL][QB][2];
-    float4_t sxv[QB], swv[SW == 1 ? 4 * PB : 1];
+    int4_t wv[UNROLL][PB][2], xv[UNROLL][2];
+    float4_t sxv{}, swv[SW == 1 ? 4 * PB : 1];
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
 #pragma unroll
@@ -108,14 +106,11 @@ __global__ void __launch_bounds__(WAVES * 64) stream_kernel(StreamArgs a) {
         const uint32_t off = at + piece < rb ? lane_off + at : kOobOffset;
 #pragma unroll
         for (int p = 0; p < PB; ++p) wv[u][p][h] = load16(rsrc_w, off + 16u * p * rb);
-#pragma unroll
-        for (int q = 0; q < QB; ++q) xv[u][q][h] = load16(rsrc_x, off + 16u * q * rb);
+        xv[u][h] = load16(rsrc_x, off);
       }
     }
     if constexpr (kScaled) {
-#pragma unroll
-      for (int q = 0; q < QB; ++q)
-        sxv[q] = __builtin_bit_cast(float4_t, load16(rsrc_sx, static_cast<uint32_t>((16 * q + frow) * steps + s0) * 4u));
+      sxv = __builtin_bit_cast(float4_t, load16(rsrc_sx, static_cast<uint32_t>(frow * steps + s0) * 4u));
 #pragma unroll
       for (int r = 0; r < (SW == 1 ? 4 * PB : 1); ++r) {
         const int row = SW == 1 ? 16 * (r / 4) + 4 * fgrp + r % 4 : 0;
@@ -130,27 +125,24 @@ __global__ void __launch_bounds__(WAVES * 64) stream_kernel(StreamArgs a) {
       // next row, may be anything and count as zero.
       const bool past = s0 + u >= steps;
 #pragma unroll
-      for (int q = 0; q < QB; ++q) {
+      for (int p = 0; p < PB; ++p) {
+        if constexpr (kScaled) {
+          const float4_t v =
+              mfma_fp8(join(wv[u][p][0], wv[u][p][1]), join(xv[u][0], xv[u][1]), float4_t{0.0f, 0.0f, 0.0f, 0.0f});
 #pragma unroll
-        for (int p = 0; p < PB; ++p) {
-          if constexpr (kScaled) {
-            const float4_t v =
-                mfma_fp8(join(wv[u][p][0], wv[u][p][1]), join(xv[u][q][0], xv[u][q][1]), float4_t{0.0f, 0.0f, 0.0f, 0.0f});
+          for (int e = 0; e < 4; ++e) {
+            const float scale = sxv[u] * swv[SW == 1 ? 4 * p + e : 0][u];
+            acc[p][e] = __builtin_fmaf(v[e], past ? 0.0f : scale, acc[p][e]);
+          }
+        } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float scale = sxv[q][u] * swv[SW == 1 ? 4 * p + e : 0][u];
-              acc[p][q][e] = __builtin_fmaf(v[e], past ? 0.0f : scale, acc[p][q][e]);
-            }
-          } else {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if constexpr (IN == kF16)
-                acc[p][q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, wv[u][p][h]),
-                                                                   __builtin_bit_cast(half8_t, xv[u][q][h]), acc[p][q], 0, 0, 0);
-              else
-                acc[p][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, wv[u][p][h]),
-                                                                    __builtin_bit_cast(bf16x8_t, xv[u][q][h]), acc[p][q], 0, 0, 0);
-            }
+          for (int h = 0; h < 2; ++h) {
+            if constexpr (IN == kF16)
+              acc[p] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, wv[u][p][h]),
+                                                              __builtin_bit_cast(half8_t, xv[u][h]), acc[p], 0, 0, 0);
+            else
+              acc[p] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, wv[u][p][h]),
+                                                               __builtin_bit_cast(bf16x8_t, xv[u][h]), acc[p], 0, 0, 0);
           }
         }
       }
@@ -160,11 +152,9 @@ __global__ void __launch_bounds__(WAVES * 64) stream_kernel(StreamArgs a) {
 #pragma unroll
   for (int p = 0; p < PB; ++p)
 #pragma unroll
-    for (int q = 0; q < QB; ++q)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) partial[wave][16 * q + frow][16 * p + 4 * fgrp + e] = acc[p][q][e];
+    for (int e = 0; e < 4; ++e) partial[wave][frow][16 * p + 4 * fgrp + e] = acc[p][e];
   __syncthreads();
-  for (int i = threadIdx.x; i < 16 * QB * kRows; i += WAVES * 64) {
+  for (int i = threadIdx.x; i < kStreamUnit * kRows; i += WAVES * 64) {
     const int t = i / kRows, n = i % kRows;
     if (t >= rows || n >= w_rows) continue;
     float sum = 0.0f;
@@ -174,78 +164,64 @@ __global__ void __launch_bounds__(WAVES * 64) stream_kernel(StreamArgs a) {
   }
 }
 
-template <int IN, int OUT, int PB, int QB, int WAVES, int UNROLL, bool GROUPED, int SW>
+template <int IN, int OUT, int PB, int WAVES, int UNROLL, bool GROUPED, int SW>
 hipError_t launch_one(StreamArgs a, int64_t units, hipStream_t stream) {
   a.blocks_n = (a.N + 16 * PB - 1) / (16 * PB);
   const dim3 grid(static_cast<unsigned>(units * a.blocks_n));
-  hipLaunchKernelGGL((stream_kernel<IN, OUT, PB, QB, WAVES, UNROLL, GROUPED, SW>), grid, dim3(WAVES * 64), 0, stream, a);
+  hipLaunchKernelGGL((stream_kernel<IN, OUT, PB, WAVES, UNROLL, GROUPED, SW>), grid, dim3(WAVES * 64), 0, stream, a);
   return hipGetLastError();
 }
 
-// The launch shape.  Measured (MI355X, 8 bits unless said; PB x WAVES x
-// UNROLL):
-//  * x is read once per workgroup, so 32 rows of W pay when x has more than a
-//    few rows and every CU still gets a workgroup (27x8192x4096: 1x8x4 12.7 us,
-//    2x8x4 9.8; 1x32768x4096 24.1 and 25.4; 32x2048x8192 14.0 and 18.2).
-//  * Many groups make many workgroups of little work: small ones with few
-//    loads in flight each, so that more of them share a CU (64 rows in 64
-//    groups x 2048 x 4096: 1x8x4 84 us, 2x8x4 67, 2x4x2 65; 16-bit 32 rows x
-//    2048 x 2048 40.9, 41.8 and 38.7).
-//  * 2 steps in flight instead of 4 where that leaves the slowest wave fewer
-//    steps (1x4096x14336, 112 steps: 12.1 -> 10.7 us).
-template <int IN, int OUT, int QB, bool GROUPED, int SW>
-hipError_t launch_waves(const StreamArgs &a, int64_t units, int num_cus, hipStream_t stream) {
+// The launch shape.  Measured (MI355X; PB x WAVES x UNROLL):
+//  * Many groups make many workgroups of little work: small ones of 32 rows of
+//    W with few loads in flight each, so that more of them share a CU (8 bits,
+//    64 rows in 64 groups x 2048 x 4096: 1x8x4 84 us, 2x8x4 67, 2x4x2 65;
+//    16-bit 32 rows x 2048 x 2048 40.9, 41.8 and 38.7).
+//  * Else 16 rows of W, and 2 steps in flight instead of 4 where that leaves
+//    the slowest wave fewer steps (1x4096x14336, 112 steps: 12.1 -> 10.7 us).
+template <int IN, int OUT, bool GROUPED, int SW>
+hipError_t launch_rows(const StreamArgs &a, int64_t units, int num_cus, hipStream_t stream) {
+  if constexpr (GROUPED) {
+    if (units * ((a.N + 31) / 32) >= 2 * static_cast<int64_t>(num_cus))
+      return launch_one<IN, OUT, 2, 4, 2, GROUPED, SW>(a, units, stream);
+  }
   const int steps = (a.row_bytes + kStepBytes - 1) / kStepBytes;
   const bool two = (steps + 15) / 16 * 2 < (steps + 31) / 32 * 4;
-  const int64_t wide = units * ((a.N + 31) / 32);  // workgroups of 32 rows of W
-  if (GROUPED ? wide >= 2 * num_cus : a.T > 4 && steps < 32 && wide >= num_cus)
-    return launch_one<IN, OUT, 2, QB, 4, 2, GROUPED, SW>(a, units, stream);
-  if (!GROUPED && a.T > 4 && wide >= num_cus)
-    return two ? launch_one<IN, OUT, 2, QB, 8, 2, GROUPED, SW>(a, units, stream)
-               : launch_one<IN, OUT, 2, QB, 8, 4, GROUPED, SW>(a, units, stream);
-  return two ? launch_one<IN, OUT, 1, QB, 8, 2, GROUPED, SW>(a, units, stream)
-             : launch_one<IN, OUT, 1, QB, 8, 4, GROUPED, SW>(a, units, stream);
-}
-
-template <int IN, int OUT, bool GROUPED, int SW>
-hipError_t launch_rows(const StreamArgs &a, int rows, int64_t units, int num_cus, hipStream_t stream) {
-  if (rows <= 16) return launch_waves<IN, OUT, 1, GROUPED, SW>(a, units, num_cus, stream);
-  if (rows <= 32) return launch_waves<IN, OUT, 2, GROUPED, SW>(a, units, num_cus, stream);
-  return launch_waves<IN, OUT, 4, GROUPED, SW>(a, units, num_cus, stream);
+  return two ? launch_one<IN, OUT, 1, 8, 2, GROUPED, SW>(a, units, stream)
+             : launch_one<IN, OUT, 1, 8, 4, GROUPED, SW>(a, units, stream);
 }
 
 }  // namespace
 
 hipError_t launch_stream_fp8(int out, const void *x, const float *sx, const void *w, const float *sw, int w_scale_rows,
-                             void *d, int M, int N, int K, int num_cus, hipStream_t stream) {
+                             void *d, int M, int N, int K, hipStream_t stream) {
   const StreamArgs a{static_cast<const uint8_t *>(x), static_cast<const uint8_t *>(w), sx, sw, nullptr,
                      static_cast<uint16_t *>(d), M, N, 1, K, 0};
-  const int rows = M <= 16 ? 16 : M <= 32 ? 32 : 64;
-  const int64_t units = (M + rows - 1) / rows;
+  static_assert(kFp8StreamRows <= kStreamUnit, "one unit");
   if (w_scale_rows == 1)
-    return out == kBF16 ? launch_rows<kE4m3, kBF16, false, 1>(a, rows, units, num_cus, stream)
-                        : launch_rows<kE4m3, kF16, false, 1>(a, rows, units, num_cus, stream);
-  return out == kBF16 ? launch_rows<kE4m3, kBF16, false, kScaleBlock>(a, rows, units, num_cus, stream)
-                      : launch_rows<kE4m3, kF16, false, kScaleBlock>(a, rows, units, num_cus, stream);
+    return out == kBF16 ? launch_rows<kE4m3, kBF16, false, 1>(a, 1, 0, stream)
+                        : launch_rows<kE4m3, kF16, false, 1>(a, 1, 0, stream);
+  return out == kBF16 ? launch_rows<kE4m3, kBF16, false, kScaleBlock>(a, 1, 0, stream)
+                      : launch_rows<kE4m3, kF16, false, kScaleBlock>(a, 1, 0, stream);
 }
 
 hipError_t launch_stream_grouped(int dtype, const void *x, const void *w, const int *offsets, void *d, int T, int N,
-                                 int K, int E, int rows, int num_cus, hipStream_t stream) {
+                                 int K, int E, int num_cus, hipStream_t stream) {
   const StreamArgs a{static_cast<const uint8_t *>(x), static_cast<const uint8_t *>(w), nullptr, nullptr, offsets,
                      static_cast<uint16_t *>(d), T, N, E, 2 * K, 0};
-  const int64_t units = unit_bound(T, E, rows);
-  return dtype == kBF16 ? launch_rows<kBF16, kBF16, true, kScaleBlock>(a, rows, units, num_cus, stream)
-                        : launch_rows<kF16, kF16, true, kScaleBlock>(a, rows, units, num_cus, stream);
+  const int64_t units = unit_bound(T, E, kStreamUnit);
+  return dtype == kBF16 ? launch_rows<kBF16, kBF16, true, kScaleBlock>(a, units, num_cus, stream)
+                        : launch_rows<kF16, kF16, true, kScaleBlock>(a, units, num_cus, stream);
 }
 
 hipError_t launch_stream_grouped_fp8(int out, const void *x, const float *sx, const void *w, const float *sw,
-                                     const int *offsets, void *d, int T, int N, int K, int E, int rows,
-                                     int num_cus, hipStream_t stream) {
+                                     const int *offsets, void *d, int T, int N, int K, int E, int num_cus,
+                                     hipStream_t stream) {
   const StreamArgs a{static_cast<const uint8_t *>(x), static_cast<const uint8_t *>(w), sx, sw, offsets,
                      static_cast<uint16_t *>(d), T, N, E, K, 0};
-  const int64_t units = unit_bound(T, E, rows);
-  return out == kBF16 ? launch_rows<kE4m3, kBF16, true, kScaleBlock>(a, rows, units, num_cus, stream)
-                      : launch_rows<kE4m3, kF16, true, kScaleBlock>(a, rows, units, num_cus, stream);
+  const int64_t units = unit_bound(T, E, kStreamUnit);
+  return out == kBF16 ? launch_rows<kE4m3, kBF16, true, kScaleBlock>(a, units, num_cus, stream)
+                      : launch_rows<kE4m3, kF16, true, kScaleBlock>(a, units, num_cus, stream);
 }
 
 }  // namespace gt

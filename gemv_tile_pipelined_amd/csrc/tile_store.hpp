@@ -28,7 +28,7 @@ inline int row_alignment(const void *D, int64_t ld) {
 template <int ROWS, int COLS, int PITCH>
 __device__ inline void store_wave_tile(const char *tile, _Float16 *dst, int64_t ld, int rows, int cols, int alignment,
                                        int lane) {
-  static_assert(COLS == 64 || COLS == 128, "tile columns");
+  static_assert(COLS == 32 || COLS == 64 || COLS == 128, "tile columns");
   if (alignment == 16) {
     constexpr int kPieces = COLS / 8;
     constexpr int kPerPass = 64 / kPieces;
@@ -71,7 +71,7 @@ __device__ inline void store_wave_tile(const char *tile, _Float16 *dst, int64_t 
     const int first = odd(row);
     const int n = lane & 1 ? have - 1 : 0;
     const bool single = lane & 1 ? ((have - first) & 1) != 0 : first != 0;
-    if (r < rows && have > 0 && single) row[n] = reinterpret_cast<const _Float16 *>(tile + r * PITCH)[n];
+    if (r < min(rows, ROWS) && have > 0 && single) row[n] = reinterpret_cast<const _Float16 *>(tile + r * PITCH)[n];
   }
 }
 

@@ -41,11 +41,12 @@ def _run(env, M, N, K, fmt, sb_rows):
     _check(D.double().cpu().numpy(), want, tol)
 
 
-# One row to a few blocks of rows (streamed up to 64), columns around the blocks of 16 and 128, K from a part of a
-# scale block to several.
+# One row to a few blocks of rows (streamed up to 4), columns around the blocks of 16 and 128, K from a part of a
+# scale block to several; the last ones have more tiles of 32 x 32, 32 x 64, 64 x 64 and 128 x 64 than there are CUs.
 SHAPES = [(1, 1, 16), (1, 130, 128), (1, 300, 2064), (2, 16, 144), (16, 129, 400), (17, 100, 1040), (33, 257, 112),
           (48, 15, 4112), (64, 300, 272), (65, 129, 144), (65, 1, 16), (130, 7, 256), (200, 300, 400), (513, 260, 1040),
-          (300, 1000, 4112)]
+          (300, 1000, 4112), (3, 33, 272), (4, 70, 4112), (5, 63, 2064), (31, 97, 1936), (100, 3001, 400), (97, 2998, 2192),
+          (200, 3000, 400), (130, 3063, 1168), (500, 3000, 400), (391, 3001, 912), (1100, 3001, 272)]
 
 
 @pytest.mark.parametrize("fmt", ["f16", "bf16"])
