@@ -525,14 +525,14 @@ GROUPED_OPS = {"forward": 0, "dgrad": 1, "wgrad": 2, "fp8": 3}
 
 
 def grouped_plan(op: str, T: int, N: int, K: int, E: int, num_cus: int):
-    """("stream" or "tiled", rows, cols): the kernel a grouped product (op "forward", "dgrad", "wgrad" or "fp8") runs
+    """("stream", "deep" or "tiled", rows, cols): the kernel a grouped product (op "forward", "dgrad", "wgrad" or "fp8") runs
     on num_cus CUs, and the rows and columns of the output that a workgroup takes at a time."""
     rows, cols = ctypes.c_int(), ctypes.c_int()
     kind = int(load_library().gemvtile_grouped_plan(GROUPED_OPS[op], T, N, K, E, num_cus, ctypes.byref(rows),
                                                     ctypes.byref(cols)))
     if kind < 0:
         raise GemvTileError(1, "sizes out of range")
-    return ("stream" if kind else "tiled"), rows.value, cols.value
+    return ("tiled", "stream", "deep")[kind], rows.value, cols.value
 
 
 def group_unit(offsets, T: int, rows: int, unit: int):

@@ -40,7 +40,7 @@ PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 REPO_DIR = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 SOURCES = [os.path.join(CSRC, f) for f in ("api.hip", "gemm.hip", "gemm_plain.hip", "gemm_ws.hip", "gemv.hip", "skinny.hip",
-                                           "quantize.hip", "stream.hip", "fp8_deep.hip", "fp8_gemm.hip", "grouped_forward.hip",
+                                           "quantize.hip", "stream.hip", "deep.hip", "fp8_gemm.hip", "grouped_forward.hip",
                                            "grouped_dgrad.hip", "grouped_wgrad.hip")]
 LIBRARY = os.path.join(PKG_DIR, "libgemvtile.so")
 ARCH = "gfx950"

@@ -451,8 +451,8 @@ int run_gemm_fp8(const void *A, const float *sa, const void *B, const float *sb,
   int cus = 0;
   const int st = current_cu_count(&cus);
   if (st != GEMVTILE_OK) return st;
-  if (M <= gt::kFp8StreamRows) return to_status(gt::launch_stream_fp8(out, A, sa, B, sb, r, D, m, n, k, s));
-  if (gt::fp8_few_tiles(M, N, cus)) return to_status(gt::launch_fp8_deep(out, A, sa, B, sb, r, D, m, n, k, cus, s));
+  if (M <= gt::kStreamRows) return to_status(gt::launch_stream_fp8(out, A, sa, B, sb, r, D, m, n, k, s));
+  if (gt::few_tiles(M, N, 1, cus)) return to_status(gt::launch_deep_fp8(out, A, sa, B, sb, r, D, m, n, k, cus, s));
   return to_status(gt::launch_gemm_fp8(out, A, sa, B, sb, r, D, m, n, k, cus, s));
 }
 
@@ -488,7 +488,11 @@ int run_grouped(int op, const void *A, const float *sa, const void *B, const flo
   int cus = 0;
   st = current_cu_count(&cus);
   if (st != GEMVTILE_OK) return st;
-  if ((op == kOpForward || op == kOpFp8) && gt::grouped_streams(T, N, E))
+  const bool product = op == kOpForward || op == kOpFp8;
+  if (product && T > gt::kStreamRows && gt::few_tiles(T, N, E, cus))
+    return to_status(op == kOpFp8 ? gt::launch_deep_grouped_fp8(dtype, A, sa, B, sb, offsets, D, t, n, k, e, cus, s)
+                                  : gt::launch_deep_grouped(dtype, A, B, offsets, D, t, n, k, e, cus, s));
+  if (product && gt::grouped_streams(T, N, E))
     return to_status(op == kOpFp8 ? gt::launch_stream_grouped_fp8(dtype, A, sa, B, sb, offsets, D, t, n, k, e, cus, s)
                                   : gt::launch_stream_grouped(dtype, A, B, offsets, D, t, n, k, e, cus, s));
   switch (op) {
@@ -562,7 +566,12 @@ int gemvtile_grouped_plan(int op, int64_t T, int64_t N, int64_t K, int64_t E, in
       num_cus > (int64_t{1} << 20) || rows == nullptr || cols == nullptr)
     return -1;
   if (check_grouped_sizes(op, T, N, K, E) != GEMVTILE_OK) return -1;
-  if ((op == kOpForward || op == kOpFp8) && gt::grouped_streams(T, N, E)) {
+  const bool product = op == kOpForward || op == kOpFp8;
+  if (product && T > gt::kStreamRows && gt::few_tiles(T, N, E, static_cast<int>(num_cus))) {
+    gt::few_tiles_plan(T, N, E, static_cast<int>(num_cus), rows, cols);
+    return 2;
+  }
+  if (product && gt::grouped_streams(T, N, E)) {
     *rows = gt::kStreamUnit;
     *cols = 16;
     return 1;

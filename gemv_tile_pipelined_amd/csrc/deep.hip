@@ -1,16 +1,17 @@
-// fp8_deep.hip -- dense products of block-scaled e4m3 operands (fp8_gemm.hip)
-// with fewer tiles than CUs.
+// deep.hip -- products with fewer tiles than CUs: dense ones of block-scaled
+// e4m3 operands (fp8_gemm.hip), and grouped ones of either kind
+// (grouped_kernel.hpp).
 //
 // Such a product is bound by latency: a CU has one tile and walks its K tiles
-// one after another (32 of 128x128 outputs took 0.5 us each, whatever M).  So
+// one after another (128x128 outputs take 0.5 us for each, whatever M).  So
 // tiles are small here, the smallest of which there are no more than CUs, and
-// the waves form TEAMS teams that take K tiles in turn, each with a ring of its
-// own; together the rings fill the LDS.  A step has one barrier: behind it, all
-// waves have the team's K tile kt in registers (its stage is refilled) and kt +
-// 1 has landed, whose operands are read while kt's products are formed.  The
-// teams' sums are joined in LDS, in order.
+// the waves form TEAMS teams that take K tiles (128 bytes of a row) in turn,
+// each with a ring of its own; together the rings fill the LDS.  A step has one
+// barrier: behind it, all waves have the team's K tile kt in registers (its
+// stage is refilled) and kt + 1 has landed, whose operands are read while kt's
+// products are formed.  The teams' sums are joined in LDS, in order.
 //
-// Measured (MI355X, us; rows x 4096 x 4096; one column per kernel):
+// Measured (MI355X, us; M x 4096 x 4096 in 8 bits):
 //             streamed  32x32  32x64  64x64  tiles of fp8_gemm.hip
 //   M =   4        5.4    6.3    8.3    9.5   15.9
 //        17        6.6    6.2    8.2    9.7   16.0
@@ -23,7 +24,11 @@
 // Streaming (stream.hip) reads x again for every 16 rows of W: M = 16 of
 // 4096x14336 16.3 and here 12.6, of 28672x4096 30.8 and 27.5; M = 4 11.9 and
 // 12.3, 23.8 and 26.8; M = 8 13.3 and 12.3, 27.9 and 28.3.
+// Groups (8 of 512 rows in all, x 2048 x 4096, 128x64 tiles): 8 bits 17.7 us,
+// tiles of fp8_gemm.hip 21.6; bf16 28.3, tiles of grouped_kernel.hpp 37.7.  24
+// rows over 8 groups x 2048 x 2048 (32x64): 7.5 and 10.9, streamed 8.8 and 13.0.
 #include "fp8_common.hpp"
+#include "groups.hpp"
 #include "kernels.hpp"
 #include "tile_order.hpp"
 #include "tile_store.hpp"
@@ -37,8 +42,10 @@ namespace {
 struct DeepArgs {
   const uint8_t *A, *B;
   const float *sa, *sb;
+  const int *offsets;
   uint16_t *D;
-  int M, N, K;
+  int M, N, E;    // M: rows of A (all groups)
+  int row_bytes;  // of A and B
   int tiles_m, tiles_n;
   int alignment;  // of D's rows
 };
@@ -70,8 +77,16 @@ struct DeepShape {
   __host__ __device__ static constexpr int swz(int row) { return (row & 7) ^ ((row >> 3) & 1); }
 };
 
-template <class S, int OUT, int SB>
-__global__ void __launch_bounds__(S::kThreads) fp8_deep_kernel(DeepArgs a) {
+constexpr int kE4m3 = 2;
+
+__device__ inline int4_t half_of(int8_v v, int h) {
+  return h == 0 ? __builtin_shufflevector(v, v, 0, 1, 2, 3) : __builtin_shufflevector(v, v, 4, 5, 6, 7);
+}
+
+// IN: kF16, kBF16 (16-bit operands, no scales: two MFMAs of 32 per 128 bytes) or
+// kE4m3.  SB: rows of B per scale.
+template <class S, int IN, int OUT, bool GROUPED, int SB>
+__global__ void __launch_bounds__(S::kThreads) deep_kernel(DeepArgs a) {
   __shared__ __attribute__((aligned(1024))) char smem[S::kRingBytes];
   const int lane = threadIdx.x & 63;
   const int team = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) / S::kWaves);
@@ -80,21 +95,32 @@ __global__ void __launch_bounds__(S::kThreads) fp8_deep_kernel(DeepArgs a) {
   const int wn = wave % S::WAVES_N;
   char *const ring = smem + team * (S::STAGES * S::kStageBytes);
   const uint32_t lds0 = lds_addr(smem) + static_cast<uint32_t>(team) * (S::STAGES * S::kStageBytes);
-  const int KT = (a.K + kScaleBlock - 1) / kScaleBlock;
+  constexpr bool kScaled = IN == kE4m3;
+  const int rb = a.row_bytes;
+  const int KT = (rb + S::kRowBytes - 1) / S::kRowBytes;
 
-  const TileCoord tc = tile_of(xcd_logical_id(blockIdx.x, gridDim.x), a.tiles_m, a.tiles_n, kGemmGroupM);
-  const int m0 = static_cast<int>(tc.tm) * S::BM, n0 = static_cast<int>(tc.tn) * S::BN;
-  const int rows = min(S::BM, a.M - m0), cols = min(S::BN, a.N - n0);
-  const int4_t rsrc_a = make_buffer_rsrc(a.A + static_cast<int64_t>(m0) * a.K, static_cast<uint32_t>(rows) * a.K);
-  const int4_t rsrc_b = make_buffer_rsrc(a.B + static_cast<int64_t>(n0) * a.K, static_cast<uint32_t>(cols) * a.K);
-  const int4_t rsrc_sa = make_buffer_rsrc(a.sa + static_cast<int64_t>(m0) * KT, static_cast<uint32_t>(rows) * KT * 4u);
-  const int sb_rows = SB == 1 ? cols : (cols + kScaleBlock - 1) / kScaleBlock;
-  const int4_t rsrc_sb = make_buffer_rsrc(a.sb + static_cast<int64_t>(n0 / SB) * KT, static_cast<uint32_t>(sb_rows) * KT * 4u);
+  GroupUnit g{0, 0, a.M};
+  int n0;
+  if constexpr (GROUPED) {
+    // A unit's tiles side by side, spread over the XCDs.
+    const int unit = static_cast<int>(blockIdx.x) / a.tiles_n;
+    if (!find_unit(a.offsets, a.E, a.M, S::BM, unit, &g)) return;
+    n0 = (static_cast<int>(blockIdx.x) - unit * a.tiles_n) * S::BN;
+  } else {
+    const TileCoord tc = tile_of(xcd_logical_id(blockIdx.x, gridDim.x), a.tiles_m, a.tiles_n, kGemmGroupM);
+    g.row = static_cast<int>(tc.tm) * S::BM;
+    n0 = static_cast<int>(tc.tn) * S::BN;
+  }
+  const int m0 = g.row;
+  const int rows = min(S::BM, g.end - m0), cols = min(S::BN, a.N - n0);
+  const int64_t b_row = static_cast<int64_t>(g.group) * a.N + n0;
+  const int4_t rsrc_a = make_buffer_rsrc(a.A + static_cast<int64_t>(m0) * rb, static_cast<uint32_t>(rows) * rb);
+  const int4_t rsrc_b = make_buffer_rsrc(a.B + b_row * rb, static_cast<uint32_t>(cols) * rb);
 
   const int ld_row = wave * 8 + lane / 8;
-  const int ld_k = ((lane % 8) ^ S::swz(ld_row)) * 16;
-  const uint32_t ld_off = static_cast<uint32_t>(ld_row) * static_cast<uint32_t>(a.K) + static_cast<uint32_t>(ld_k);
-  const uint32_t ld_step = static_cast<uint32_t>(S::kRowStep) * static_cast<uint32_t>(a.K);
+  const int ld_k = ((lane % 8) ^ S::swz(ld_row)) * 16;  // bytes
+  const uint32_t ld_off = static_cast<uint32_t>(ld_row) * static_cast<uint32_t>(rb) + static_cast<uint32_t>(ld_k);
+  const uint32_t ld_step = static_cast<uint32_t>(S::kRowStep) * static_cast<uint32_t>(rb);
   // Scales: wave w loads those of 64 of A's rows followed by B's; waves that
   // have none left load the first ones again, to a place that nothing reads.
   const int scale_part = wave % S::kScaleWaves;
@@ -102,15 +128,22 @@ __global__ void __launch_bounds__(S::kThreads) fp8_deep_kernel(DeepArgs a) {
   const int scale_row = (scale_a ? scale_part : scale_part - S::kScalesA / 64) * 64 + lane;
   const uint32_t scale_off =
       static_cast<uint32_t>(scale_a || SB == 1 ? scale_row : scale_row / kScaleBlock) * static_cast<uint32_t>(KT) * 4u;
-  const int4_t rsrc_s = scale_a ? rsrc_sa : rsrc_sb;
+  int4_t rsrc_s{};
+  if constexpr (kScaled) {
+    const int64_t sb_row = SB == 1 ? b_row
+                                   : static_cast<int64_t>(g.group) * ((a.N + kScaleBlock - 1) / kScaleBlock) + n0 / kScaleBlock;
+    const int sb_rows = SB == 1 ? cols : 1;
+    rsrc_s = make_buffer_rsrc(scale_a ? a.sa + static_cast<int64_t>(m0) * KT : a.sb + sb_row * KT,
+                              static_cast<uint32_t>(scale_a ? rows : sb_rows) * KT * 4u);
+  }
   // K tiles past the last: operands out of range, i.e. zeros, and scales of
   // another row or out of range, which belong to sums that nothing uses.
   // kt: the team's own count.
   auto issue = [&](int own, int slot) {
     const int kt = own * S::TEAMS + team;
     const uint32_t stage = lds0 + static_cast<uint32_t>(slot) * S::kStageBytes;
-    const int k0 = kt * kScaleBlock;
-    const uint32_t off = k0 + ld_k < a.K ? ld_off + static_cast<uint32_t>(k0) : kOobOffset;
+    const int k0 = kt * S::kRowBytes;
+    const uint32_t off = k0 + ld_k < rb ? ld_off + static_cast<uint32_t>(k0) : kOobOffset;
 #pragma unroll
     for (int d = 0; d < S::kDmaA + S::kDmaB; ++d) {
       const bool is_a = d < S::kDmaA;
@@ -118,13 +151,17 @@ __global__ void __launch_bounds__(S::kThreads) fp8_deep_kernel(DeepArgs a) {
       lds_dma_b128(is_a ? rsrc_a : rsrc_b, off + i * ld_step,
                    __builtin_amdgcn_readfirstlane(stage + (is_a ? 0 : S::kStageA) + (i * S::kWaves + wave) * 1024));
     }
-    lds_dma_b32(rsrc_s, kt < KT ? scale_off + static_cast<uint32_t>(kt) * 4u : kOobOffset,
-                __builtin_amdgcn_readfirstlane(stage + S::kStageScales + static_cast<uint32_t>(wave) * 256u));
+    if constexpr (kScaled)
+      lds_dma_b32(rsrc_s, kt < KT ? scale_off + static_cast<uint32_t>(kt) * 4u : kOobOffset,
+                  __builtin_amdgcn_readfirstlane(stage + S::kStageScales + static_cast<uint32_t>(wave) * 256u));
   };
+  constexpr int kPerStage = S::kDmaA + S::kDmaB + (kScaled ? 1 : 0);
 
   const int frag_row = lane % 16;
   const int frag_kgrp = lane / 16;
-  const int frag_piece = ((frag_kgrp & 1) << 1) | (frag_kgrp >> 1);  // and frag_piece + 4
+  // Pieces frag_piece and frag_piece + 4 of a row: any order does that is the
+  // same for both operands.
+  const int frag_piece = ((frag_kgrp & 1) << 1) | (frag_kgrp >> 1);
   const uint32_t piece0 = static_cast<uint32_t>((frag_piece ^ S::swz(frag_row)) * 16);
   const uint32_t piece1 = static_cast<uint32_t>(((frag_piece + 4) ^ S::swz(frag_row)) * 16);
   const uint32_t a_base = static_cast<uint32_t>(wm * S::kWaveM + frag_row) * S::kRowBytes;
@@ -150,35 +187,52 @@ __global__ void __launch_bounds__(S::kThreads) fp8_deep_kernel(DeepArgs a) {
 #pragma unroll
     for (int i = 0; i < S::kFragM; ++i) {
       fa[P][i] = block(stage + a_base + i * 16 * S::kRowBytes);
-      sa[P][i] = *reinterpret_cast<const float *>(stage + sa_base + i * 64);
+      if constexpr (kScaled) sa[P][i] = *reinterpret_cast<const float *>(stage + sa_base + i * 64);
     }
 #pragma unroll
     for (int j = 0; j < S::kFragN; ++j) {
       fb[P][j] = block(stage + b_base + j * 16 * S::kRowBytes);
-      if constexpr (SB == 1)
-        sb[P][j] = *reinterpret_cast<const float4_t *>(stage + sb_base + j * 64);
-      else if (j == 0)
-        sb[P][0][0] = *reinterpret_cast<const float *>(stage + sb_base);
+      if constexpr (kScaled) {
+        if constexpr (SB == 1)
+          sb[P][j] = *reinterpret_cast<const float4_t *>(stage + sb_base + j * 64);
+        else if (j == 0)
+          sb[P][0][0] = *reinterpret_cast<const float *>(stage + sb_base);
+      }
     }
   };
   auto products = [&](auto buffer) {
     constexpr int P = decltype(buffer)::value;
 #pragma unroll
     for (int j = 0; j < S::kFragN; ++j) {
-      float4_t part[S::kFragM];
+      if constexpr (kScaled) {
+        float4_t part[S::kFragM];
 #pragma unroll
-      for (int i = 0; i < S::kFragM; ++i) part[i] = mfma_fp8(fb[P][j], fa[P][i], float4_t{0.0f, 0.0f, 0.0f, 0.0f});
+        for (int i = 0; i < S::kFragM; ++i) part[i] = mfma_fp8(fb[P][j], fa[P][i], float4_t{0.0f, 0.0f, 0.0f, 0.0f});
 #pragma unroll
-      for (int i = 0; i < S::kFragM; ++i)
+        for (int i = 0; i < S::kFragM; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          acc[i][j][e] = __builtin_fmaf(part[i][e], sa[P][i] * sb[P][SB == 1 ? j : 0][SB == 1 ? e : 0], acc[i][j][e]);
+          for (int e = 0; e < 4; ++e)
+            acc[i][j][e] = __builtin_fmaf(part[i][e], sa[P][i] * sb[P][SB == 1 ? j : 0][SB == 1 ? e : 0], acc[i][j][e]);
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < S::kFragM; ++i) {
+            const int4_t b4 = half_of(fb[P][j], h), a4 = half_of(fa[P][i], h);
+            if constexpr (IN == kF16)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, b4),
+                                                                 __builtin_bit_cast(half8_t, a4), acc[i][j], 0, 0, 0);
+            else
+              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, b4),
+                                                                  __builtin_bit_cast(bf16x8_t, a4), acc[i][j], 0, 0, 0);
+          }
+      }
     }
   };
 
 #pragma unroll
   for (int s = 0; s < S::STAGES; ++s) issue(s, s);
-  wait_vmcnt<(S::STAGES - 1) * S::kPerStage>();
+  wait_vmcnt<(S::STAGES - 1) * kPerStage>();
   workgroup_barrier();
   using Even = std::integral_constant<int, 0>;
   using Odd = std::integral_constant<int, 1>;
@@ -187,7 +241,7 @@ __global__ void __launch_bounds__(S::kThreads) fp8_deep_kernel(DeepArgs a) {
   auto step = [&](auto now, auto then, int kt) {
     const int next = slot + 1 == S::STAGES ? 0 : slot + 1;
     __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
-    wait_vmcnt<(S::STAGES - 2) * S::kPerStage>();
+    wait_vmcnt<(S::STAGES - 2) * kPerStage>();
     workgroup_barrier();
     __builtin_amdgcn_sched_barrier(0);
     issue(kt + S::STAGES, slot);
@@ -248,42 +302,75 @@ using Deep64x64 = DeepShape<64, 64, 2, 2, 2, 4>;
 using Deep32x64 = DeepShape<32, 64, 2, 2, 2, 6>;
 using Deep32x32 = DeepShape<32, 32, 2, 1, 4, 4>;
 
-template <class S, int OUT, int SB>
-hipError_t launch_deep(DeepArgs a, hipStream_t stream) {
-  a.tiles_m = (a.M + S::BM - 1) / S::BM;
+template <class S, int IN, int OUT, bool GROUPED, int SB>
+hipError_t launch_tiles(DeepArgs a, hipStream_t stream) {
+  a.tiles_m = static_cast<int>(GROUPED ? unit_bound(a.M, a.E, S::BM) : (a.M + S::BM - 1) / S::BM);
   a.tiles_n = (a.N + S::BN - 1) / S::BN;
   const dim3 grid(static_cast<unsigned>(a.tiles_m * a.tiles_n));
-  hipLaunchKernelGGL((fp8_deep_kernel<S, OUT, SB>), grid, dim3(S::kThreads), 0, stream, a);
+  hipLaunchKernelGGL((deep_kernel<S, IN, OUT, GROUPED, SB>), grid, dim3(S::kThreads), 0, stream, a);
   return hipGetLastError();
 }
 
-// The smallest tile of which there are no more than CUs.
+// Whether there are no more tiles than CUs (of groups: whether there are
+// expected to be).
 template <class S>
-bool fits(int64_t M, int64_t N, int num_cus) {
-  return (M + S::BM - 1) / S::BM * ((N + S::BN - 1) / S::BN) <= num_cus;
+bool fits(int64_t M, int64_t N, int64_t E, int num_cus) {
+  const int64_t units = E == 1 ? (M + S::BM - 1) / S::BM : expected_units(M, E, S::BM);
+  return units * ((N + S::BN - 1) / S::BN) <= num_cus;
 }
 
-template <int OUT, int SB>
+// The smallest tile that fits.
+template <int IN, int OUT, bool GROUPED, int SB>
 hipError_t launch_fitting(const DeepArgs &a, int num_cus, hipStream_t stream) {
-  if (fits<Deep32x32>(a.M, a.N, num_cus)) return launch_deep<Deep32x32, OUT, SB>(a, stream);
-  if (fits<Deep32x64>(a.M, a.N, num_cus)) return launch_deep<Deep32x64, OUT, SB>(a, stream);
-  if (fits<Deep64x64>(a.M, a.N, num_cus)) return launch_deep<Deep64x64, OUT, SB>(a, stream);
-  return launch_deep<Deep128x64, OUT, SB>(a, stream);
+  if (fits<Deep32x32>(a.M, a.N, a.E, num_cus)) return launch_tiles<Deep32x32, IN, OUT, GROUPED, SB>(a, stream);
+  if (fits<Deep32x64>(a.M, a.N, a.E, num_cus)) return launch_tiles<Deep32x64, IN, OUT, GROUPED, SB>(a, stream);
+  if (fits<Deep64x64>(a.M, a.N, a.E, num_cus)) return launch_tiles<Deep64x64, IN, OUT, GROUPED, SB>(a, stream);
+  return launch_tiles<Deep128x64, IN, OUT, GROUPED, SB>(a, stream);
 }
 
 }  // namespace
 
-bool fp8_few_tiles(int64_t M, int64_t N, int num_cus) {
-  return fits<Deep128x64>(M, N, num_cus);  // the largest: there are no more of it than of any other
+bool few_tiles(int64_t M, int64_t N, int64_t E, int num_cus) {
+  return fits<Deep128x64>(M, N, E, num_cus);  // the largest: there are no more of it than of any other
 }
 
-hipError_t launch_fp8_deep(int out, const void *A, const float *sa, const void *B, const float *sb, int sb_rows, void *D,
+void few_tiles_plan(int64_t M, int64_t N, int64_t E, int num_cus, int *rows, int *cols) {
+  auto is = [&](auto shape) {
+    using S = decltype(shape);
+    if (!fits<S>(M, N, E, num_cus)) return false;
+    *rows = S::BM;
+    *cols = S::BN;
+    return true;
+  };
+  is(Deep32x32{}) || is(Deep32x64{}) || is(Deep64x64{}) || is(Deep128x64{});
+}
+
+hipError_t launch_deep_fp8(int out, const void *A, const float *sa, const void *B, const float *sb, int sb_rows, void *D,
                            int M, int N, int K, int num_cus, hipStream_t stream) {
-  const DeepArgs a{static_cast<const uint8_t *>(A), static_cast<const uint8_t *>(B), sa, sb, static_cast<uint16_t *>(D),
-                   M, N, K, 0, 0, row_alignment(D, N)};
+  const DeepArgs a{static_cast<const uint8_t *>(A), static_cast<const uint8_t *>(B), sa, sb, nullptr,
+                   static_cast<uint16_t *>(D), M, N, 1, K, 0, 0, row_alignment(D, N)};
   if (sb_rows == 1)
-    return out == kBF16 ? launch_fitting<kBF16, 1>(a, num_cus, stream) : launch_fitting<kF16, 1>(a, num_cus, stream);
-  return out == kBF16 ? launch_fitting<kBF16, kScaleBlock>(a, num_cus, stream) : launch_fitting<kF16, kScaleBlock>(a, num_cus, stream);
+    return out == kBF16 ? launch_fitting<kE4m3, kBF16, false, 1>(a, num_cus, stream)
+                        : launch_fitting<kE4m3, kF16, false, 1>(a, num_cus, stream);
+  return out == kBF16 ? launch_fitting<kE4m3, kBF16, false, kScaleBlock>(a, num_cus, stream)
+                      : launch_fitting<kE4m3, kF16, false, kScaleBlock>(a, num_cus, stream);
+}
+
+hipError_t launch_deep_grouped(int dtype, const void *X, const void *W, const int *offsets, void *D, int T, int N, int K,
+                               int E, int num_cus, hipStream_t stream) {
+  const DeepArgs a{static_cast<const uint8_t *>(X), static_cast<const uint8_t *>(W), nullptr, nullptr, offsets,
+                   static_cast<uint16_t *>(D), T, N, E, 2 * K, 0, 0, row_alignment(D, N)};
+  return dtype == kBF16 ? launch_fitting<kBF16, kBF16, true, kScaleBlock>(a, num_cus, stream)
+                        : launch_fitting<kF16, kF16, true, kScaleBlock>(a, num_cus, stream);
+}
+
+hipError_t launch_deep_grouped_fp8(int out, const void *X, const float *sx, const void *W, const float *sw,
+                                   const int *offsets, void *D, int T, int N, int K, int E, int num_cus,
+                                   hipStream_t stream) {
+  const DeepArgs a{static_cast<const uint8_t *>(X), static_cast<const uint8_t *>(W), sx, sw, offsets,
+                   static_cast<uint16_t *>(D), T, N, E, K, 0, 0, row_alignment(D, N)};
+  return out == kBF16 ? launch_fitting<kE4m3, kBF16, true, kScaleBlock>(a, num_cus, stream)
+                      : launch_fitting<kE4m3, kF16, true, kScaleBlock>(a, num_cus, stream);
 }
 
 }  // namespace gt

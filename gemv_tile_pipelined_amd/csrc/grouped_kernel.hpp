@@ -744,16 +744,6 @@ grouped_gemm_kernel(GroupedArgs a) {
   });
 }
 
-// Units of `rows` rows to expect for T rows in E groups whose sizes are not
-// known on the host: T / rows whole ones, and half a unit more for each group
-// that can have rows.
-inline int64_t expected_units(int64_t T, int64_t E, int64_t rows) {
-  const int64_t some = E < T ? E : T;
-  const int64_t units = T / rows + (some + 1) / 2;
-  const int64_t bound = unit_bound(T, E, rows);
-  return units < bound ? units : bound;
-}
-
 // The tile (of kTile256x256, which stands for it with quarters, kTile256x128
 // and kTile128x128) with the least estimated time in rounds of all CUs.  The
 // smaller ones' rates of the 256x256 one are measured (8192x4096x2048 in one

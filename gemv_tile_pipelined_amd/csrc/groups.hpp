@@ -45,6 +45,16 @@ GT_HD inline int64_t unit_bound(int64_t T, int64_t E, int64_t rows) {
   return (T - some) / rows + some;
 }
 
+// Units of `rows` rows to expect for T rows in E groups whose sizes are not
+// known on the host: T / rows whole ones, and half a unit more for each group
+// that can have rows; but one at least for each of these.
+inline int64_t expected_units(int64_t T, int64_t E, int64_t rows) {
+  const int64_t some = E < T ? E : T;
+  const int64_t units = T / rows + (some + 1) / 2;
+  const int64_t bound = unit_bound(T, E, rows);
+  return units < some ? some : units < bound ? units : bound;
+}
+
 // Whether the groups are streamed (stream.hip) in units of kStreamUnit rows, by
 // the mean rows of a group, or tiled.  Measured (bf16, us streamed and tiled):
 // 32 groups x 2048 x 2048 with a mean of 4 rows 51 and 62, 8 rows 58 and 66, 12

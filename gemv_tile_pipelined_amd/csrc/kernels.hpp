@@ -337,13 +337,20 @@ hipError_t launch_stream_grouped(int dtype, const void *x, const void *w, const 
 hipError_t launch_stream_grouped_fp8(int out, const void *x, const float *sx, const void *w, const float *sw,
                                      const int *offsets, void *d, int T, int N, int K, int E, int num_cus,
                                      hipStream_t stream);
-// gemm_fp8_* streams B for at most this many rows of A (fp8_deep.hip's figures).
-constexpr int64_t kFp8StreamRows = 4;
-// fp8_deep.hip: dense products of few tiles, those that fp8_few_tiles() is true
-// for.
-bool fp8_few_tiles(int64_t M, int64_t N, int num_cus);
-hipError_t launch_fp8_deep(int out, const void *A, const float *sa, const void *B, const float *sb, int sb_rows, void *D,
+// B or W is streamed for at most this many rows of A or X, however few tiles
+// there are (figures in deep.hip).
+constexpr int64_t kStreamRows = 4;
+// deep.hip: products of few tiles, those that few_tiles() is true for (E = 1 for
+// a dense one).
+bool few_tiles(int64_t M, int64_t N, int64_t E, int num_cus);
+void few_tiles_plan(int64_t M, int64_t N, int64_t E, int num_cus, int *rows, int *cols);
+hipError_t launch_deep_fp8(int out, const void *A, const float *sa, const void *B, const float *sb, int sb_rows, void *D,
                            int M, int N, int K, int num_cus, hipStream_t stream);
+hipError_t launch_deep_grouped(int dtype, const void *X, const void *W, const int *offsets, void *D, int T, int N, int K,
+                               int E, int num_cus, hipStream_t stream);
+hipError_t launch_deep_grouped_fp8(int out, const void *X, const float *sx, const void *W, const float *sw,
+                                   const int *offsets, void *D, int T, int N, int K, int E, int num_cus,
+                                   hipStream_t stream);
 // fp8_gemm.hip: tiled products of e4m3 operands (K > 0).
 hipError_t launch_gemm_fp8(int out, const void *A, const float *sa, const void *B, const float *sb, int sb_rows, void *D,
                            int M, int N, int K, int num_cus, hipStream_t stream);

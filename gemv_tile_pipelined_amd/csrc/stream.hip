@@ -197,7 +197,7 @@ hipError_t launch_stream_fp8(int out, const void *x, const float *sx, const void
                              void *d, int M, int N, int K, hipStream_t stream) {
   const StreamArgs a{static_cast<const uint8_t *>(x), static_cast<const uint8_t *>(w), sx, sw, nullptr,
                      static_cast<uint16_t *>(d), M, N, 1, K, 0};
-  static_assert(kFp8StreamRows <= kStreamUnit, "one unit");
+  static_assert(kStreamRows <= kStreamUnit, "one unit");
   if (w_scale_rows == 1)
     return out == kBF16 ? launch_rows<kE4m3, kBF16, false, 1>(a, 1, 0, stream)
                         : launch_rows<kE4m3, kF16, false, 1>(a, 1, 0, stream);

@@ -588,7 +588,8 @@ int gemm_grouped_fp8_bf16(const void *X, const float *scale_X, const void *W, co
  * gemvtile_grouped_plan -- how gemm_grouped_* (op 0), _dgrad_ (1), _wgrad_ (2)
  * and _fp8_ (3) run on `num_cus` compute units: *rows is the number of a
  * group's rows that one workgroup takes at a time, *cols the columns of the
- * output, and the return value 1 for the kernel that streams W once (few rows
+ * output, and the return value 2 for the kernel of small tiles (no more of them
+ * than compute units are expected), 1 for the one that streams W once (few rows
  * for each group), 0 for the tiled one (a last round of 256x256 16-bit tiles that
  * would keep at most half of the compute units busy is cut into 128x128 ones).
  * Host-only; returns -1 for arguments out of range.

@@ -178,6 +178,9 @@ def test_grouped_plan(lib):
     for op in gt.GROUPED_OPS:
         kind, rows, cols = gt.grouped_plan(op, 16384, 4096, 4096, 32, 256)
         assert (kind, rows, cols) == ("tiled", 256, 256)
+    assert gt.grouped_plan("fp8", 512, 2048, 4096, 8, 256) == ("deep", 128, 64)
+    assert gt.grouped_plan("forward", 24, 2048, 2048, 8, 256) == ("deep", 32, 64)
+    assert gt.grouped_plan("forward", 4, 2048, 2048, 8, 256) == ("stream", 16, 16)
     # a streamed grid that would not fit is tiled instead
     assert gt.grouped_plan("forward", 4000, 1 << 20, 64, 500, 256)[0] == "tiled"
     for bad in (("forward", 0, 16, 16, 1, 256), ("wgrad", 8, 12, 16, 1, 256), ("fp8", 8, 16, 24, 1, 256),

@@ -176,7 +176,7 @@ def test_short_units_set_apart(env, op):
 
 
 # The smaller tiles, and a plan that expected more rows in each group than there are.
-SMALL = [("forward", (256, 128), [700, 1, 1300, 0], 2501, 200), ("forward", (128, 128), [200, 90], 300, 264),
+SMALL = [("forward", (256, 128), [700, 1, 1300, 0], 2501, 200), ("forward", (128, 128), [1200, 300], 1501, 264),
          ("dgrad", (256, 128), [800, 0, 1200], 200, 2504), ("dgrad", (128, 128), [200, 90], 264, 304),
          ("wgrad", (256, 128), [60, 100, 3, 1, 0, 70, 66], 1000, 1032), ("wgrad", (128, 128), [200, 90], 264, 304)]
 
@@ -190,12 +190,49 @@ def test_smaller_tiles(env, op, tile, sizes, N, K):
 
 
 @pytest.mark.parametrize("tile,sizes,N,K", [(256, [900, 1100, 1000], 4000, 272), (256, [900, 5, 1100, 0, 2600], 4091, 144),
-                                            (128, [700, 1, 300], 264, 400)])
+                                            (128, [700, 1, 1300, 0], 1497, 400)])
 def test_fp8_tiles(env, tile, sizes, N, K):
     torch, gt = env
     cus = torch.cuda.get_device_properties(0).multi_processor_count
     assert gt.grouped_plan("fp8", sum(sizes), N, K, len(sizes), cus) == ("tiled", tile, tile)
     _run(env, "fp8", "bf16", sizes, N, K)
+
+
+# No more tiles than CUs, of each of the sizes that there are for that; the last has more units than were expected.
+DEEP = [((32, 32), [9, 0, 40, 1, 64], 1000, 2064), ((32, 64), [20, 33, 0, 50, 1, 70], 2011, 176),
+        ((64, 64), [100, 0, 65, 200, 1], 1900, 1040), ((128, 64), [400, 129, 0, 1, 300], 1698, 144),
+        ((64, 64), [1] * 30 + [800], 397, 48)]
+
+
+@pytest.mark.parametrize("op", ["forward", "fp8"])
+@pytest.mark.parametrize("tile,sizes,N,K", DEEP)
+def test_few_tiles(env, op, tile, sizes, N, K):
+    torch, gt = env
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    assert gt.grouped_plan(op, sum(sizes) + 9, N, K, len(sizes), cus) == ("deep", *tile)
+    for fmt in ("f16", "bf16"):
+        _run(env, op, fmt, sizes, N, K, first=6, pad=3)
+
+
+# Enough tiles for the tiled kernels: columns and depths that end inside a tile, rows before and behind the groups.
+@pytest.mark.parametrize("op", ["forward", "fp8"])
+@pytest.mark.parametrize("fmt", ["f16", "bf16"])
+@pytest.mark.parametrize("sizes", [[0, 129, 1, 0, 1500, 257], [1887], [70] * 27], ids=["uneven", "one", "even"])
+@pytest.mark.parametrize("N,K", [(1501, 80), (1640, 1040), (1498, 16)])
+def test_many_tiles(env, op, fmt, sizes, N, K):
+    torch, gt = env
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    assert gt.grouped_plan(op, sum(sizes) + 10, N, K, len(sizes), cus)[0] == "tiled"
+    _run(env, op, fmt, sizes, N, K, first=3, pad=7)
+
+
+@pytest.mark.parametrize("op", ["forward", "fp8"])
+def test_most_groups_in_tiles(env, op):
+    torch, gt = env
+    sizes = [9] * 1000 + [0] * 22 + [130, 1]
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    assert gt.grouped_plan(op, sum(sizes), 24, 48, 1024, cus)[0] == "tiled"
+    _run(env, op, "f16", sizes, 24, 48)
 
 
 @pytest.mark.parametrize("op", ["forward", "dgrad", "wgrad", "fp8"])
