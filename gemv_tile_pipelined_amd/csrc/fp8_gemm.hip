@@ -18,7 +18,16 @@
 // that share a scale load it again).  Operand order and epilogue are the
 // GEMM's: B first, so that a lane holds 4 consecutive columns of one row, its
 // row's scale is one number per 16 rows, and rows leave through LDS as whole
-// lines.
+// lines.  With 256x256 tiles and 16-byte aligned rows the next tile's first
+// loads go out before this one's stores (8192x8192x1024 81.5 -> 76.6 us), staged
+// behind the ring; 128x128 tiles keep the LDS that this takes for a second
+// workgroup on the CU (2048 rows over 8 groups x 2048 x 2048: 19.4 us, 29 with
+// loads ahead).
+//
+// Bound by the matrix cores and the power they draw: 4096^3 58 to 61 us, 2.3
+// PFLOP/s, 8192^3 434 us, 2.5 PFLOP/s, matrix cores busy 63 % of the cycles at
+// 4096^3.  With a scale for each row of B (r = 1) every FMA needs a product of
+// scales beside it, eight VALU instructions for each MFMA: 4000x4096x4112 76 us.
 #include "fp8_common.hpp"
 #include "groups.hpp"
 #include "kernels.hpp"
@@ -206,14 +215,14 @@ fp8_gemm_kernel(Fp8Args a) {
     else
       wait_vmcnt<kCount>();
   };
-  using Ahead = std::integral_constant<int, kLate - 1 + S::kPerStage>;   // K tile 0 but for B's second half
-  using AtFirst = std::integral_constant<int, kEarly + kLate>;
-  using AtSecond = std::integral_constant<int, kLate - 1 + kEarly>;
+  using Ahead = std::integral_constant<int, kLate - 1 + S::kPerStage>;  // K tile 0 but for B's second half
+  using AtFirst = std::integral_constant<int, kEarly + kLate>;           // k_tile's first barrier
+  using AtSecond = std::integral_constant<int, kLate - 1 + kEarly>;      // and its second
   for (;;) {
     lane_offsets();
     // A wave whose rows lie behind the last one loads its share, and leaves the
-    // matrix units to the wave that shares its SIMD (wave 4 above or below: 128
-    // rows away).
+    // matrix units to the wave that shares its SIMD (4 waves on or back, 128
+    // rows away): 1000x4096x7168 37.7 -> 36.0 us.
     const bool idle = wm * S::kWaveM >= cur.rows;
     // Operands in registers: all 16-row blocks of A for a K tile, and the
     // current and next block of B; scales of A's rows (times the one of B's
@@ -334,30 +343,30 @@ fp8_gemm_kernel(Fp8Args a) {
       }
     } else {
 #pragma unroll
-    for (int i = 0; i < S::kFragM; ++i) read_a(smem, i);
-    read_b(smem, 0);
-    read_scales(smem, 0);
-    if constexpr (SB == 1) sbv[0] = *reinterpret_cast<const float4_t *>(smem + sb_base);
-    using Even = std::integral_constant<int, 0>;
-    using Odd = std::integral_constant<int, 1>;
-    int kt = 0;
-    if (ALIGNED && KT > 1) {
-      k_tile(Even{}, std::true_type{}, 0);
-      k_tile(Odd{}, std::true_type{}, 1);
-      kt = 2;
-    }
-    for (; kt + 1 < KT; kt += 2) {
-      k_tile(Even{}, std::false_type{}, kt);
-      k_tile(Odd{}, std::false_type{}, kt + 1);
-    }
-    if (kt < KT) {
-      k_tile(Even{}, std::false_type{}, kt);
+      for (int i = 0; i < S::kFragM; ++i) read_a(smem, i);
+      read_b(smem, 0);
+      read_scales(smem, 0);
+      if constexpr (SB == 1) sbv[0] = *reinterpret_cast<const float4_t *>(smem + sb_base);
+      using Even = std::integral_constant<int, 0>;
+      using Odd = std::integral_constant<int, 1>;
+      int kt = 0;
+      if (ALIGNED && KT > 1) {
+        k_tile(Even{}, std::true_type{}, 0);
+        k_tile(Odd{}, std::true_type{}, 1);
+        kt = 2;
+      }
+      for (; kt + 1 < KT; kt += 2) {
+        k_tile(Even{}, std::false_type{}, kt);
+        k_tile(Odd{}, std::false_type{}, kt + 1);
+      }
+      if (kt < KT) {
+        k_tile(Even{}, std::false_type{}, kt);
 #pragma unroll
-      for (int m = kSlots - kBehind; m < kSlots; ++m) accumulate(m, 0);
-    } else {
+        for (int m = kSlots - kBehind; m < kSlots; ++m) accumulate(m, 0);
+      } else {
 #pragma unroll
-      for (int m = kSlots - kBehind; m < kSlots; ++m) accumulate(m, 1);
-    }
+        for (int m = kSlots - kBehind; m < kSlots; ++m) accumulate(m, 1);
+      }
     }
 
     // ---- epilogue ------------------------------------------------------------

@@ -20,11 +20,11 @@ inline int row_alignment(const void *D, int64_t ld) {
 // non-temporal stores (gemm_kernel.hpp).  Others leave in aligned pairs, one a
 // lane and so consecutive over the lanes (cached: neighbouring tiles' rows
 // share lines), and every second row of an odd number of columns has a single
-// element at either end.  Measured for 8192
-// rows over 16 groups x 4095 (4094) x 2048, beside 169 us for 4096 columns:
-// pairs 189 (175) us; 8 elements a lane stored one by one 191 us; one element a
-// lane 206 us; 16-byte pieces of rows staged shifted by their misalignment 188
-// (191) us.
+// element at either end.  8192 rows over 16 groups x 4095 (4094) x 2048 take 173
+// (162) us beside 154 for 4096 columns; stored 8 elements a lane one by one it
+// was 1 % more than in pairs, one element a lane 9 %, and 16-byte pieces of rows
+// staged shifted by their misalignment were level for odd and 9 % more for even
+// numbers of columns.
 template <int ROWS, int COLS, int PITCH>
 __device__ inline void store_wave_tile(const char *tile, _Float16 *dst, int64_t ld, int rows, int cols, int alignment,
                                        int lane) {
