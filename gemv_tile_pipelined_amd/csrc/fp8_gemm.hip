@@ -476,11 +476,19 @@ hipError_t launch_shape(Fp8Args a, int num_cus, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// 256x256 tiles when they give most CUs one (groups: when they are expected to).
+// The tile with the shorter estimate: a round of 256x256 tiles, one on each CU,
+// takes 1.4 times as long as one of 128x128 tiles, two on each.  Measured (us,
+// 128x128 and 256x256): 1024x8192x4096 (one round, one of which half is empty)
+// 39 and 49; 1280x8192x4096 (two, one) 72 and 48; 2500x5000x2048 (two, one) 42
+// and 38; 4096 rows over 8 groups x 2048 x 2048 (two, one) 37 and 29, over 32
+// groups (two, two) 53 and 57.
 bool use_tile256(bool grouped, int64_t M, int64_t N, int64_t E, int num_cus) {
-  const int64_t some = E < M ? E : M;
-  const int64_t units = grouped ? M / 256 + (some + 1) / 2 : (M + 255) / 256;
-  return units * ((N + 255) / 256) >= num_cus * 3 / 4;
+  auto tiles = [&](int64_t side) {
+    return (grouped ? expected_units(M, E, side) : (M + side - 1) / side) * ((N + side - 1) / side);
+  };
+  const int64_t big = (tiles(256) + num_cus - 1) / num_cus;
+  const int64_t small = (tiles(128) + 2 * num_cus - 1) / (2 * num_cus);
+  return 14 * big < 10 * small;
 }
 
 template <int OUT, bool GROUPED, int SB>
