@@ -138,11 +138,17 @@ fp8_gemm_kernel(Fp8Args a) {
     int row, rows, n0;
   };
   auto locate = [&](int64_t u) -> Tile {
-    const TileCoord tc = tile_of(u, units, a.tiles_n, kGemmGroupM);
-    GroupUnit g{0, static_cast<int>(tc.tm) * S::BM, a.M};
-    if constexpr (GROUPED) g = table_unit(&table, a.E, S::BM, static_cast<int>(tc.tm));
+    GroupUnit g{0, 0, a.M};
+    int tn;
+    if constexpr (GROUPED) {
+      g = table_tile(&table, a.E, S::BM, a.tiles_n, u, &tn);
+    } else {
+      const TileCoord tc = tile_of(u, units, a.tiles_n, kGemmGroupM);
+      g.row = static_cast<int>(tc.tm) * S::BM;
+      tn = static_cast<int>(tc.tn);
+    }
     Tile t;
-    t.n0 = static_cast<int>(tc.tn) * S::BN;
+    t.n0 = tn * S::BN;
     t.row = g.row;
     t.rows = min(S::BM, g.end - g.row);
     const int cols = min(S::BN, a.N - t.n0);

@@ -23,7 +23,7 @@
 //
 // Which tiles there are.  Forward and dgrad cut every group's rows into units
 // of BM rows; a persistent workgroup keeps a table of the groups in LDS and
-// walks (unit, column tile) pairs in the GEMM's grouped order, so that units
+// walks (unit, column tile) pairs group by group (table_tile), so that units
 // of one group share the group's weights in L2.  In wgrad the groups' outputs
 // are all alike and the contraction differs: the groups' tiles come in order of
 // falling length and the workgroups take them forwards and backwards in turn,
@@ -647,13 +647,11 @@ grouped_gemm_kernel(GroupedArgs a) {
   const int tiles_m = (a.N + S::BM - 1) / S::BM;  // of a group's dW
   const int grid = static_cast<int>(gridDim.x);
   const int logical = static_cast<int>(xcd_logical_id(blockIdx.x, grid));
-  int units = 0;
   int64_t num_tiles;
   if constexpr (kUnits) {
     build_group_table(&table, a.offsets, a.E, a.T, S::BM);
     __syncthreads();
-    units = table_units(&table, a.E);
-    num_tiles = static_cast<int64_t>(units) * tiles_n;
+    num_tiles = static_cast<int64_t>(table_units(&table, a.E)) * tiles_n;
   } else {
     build_wgrad_table(&table, a.offsets, a.E, a.T, S::kThreads);
     __syncthreads();
@@ -663,9 +661,9 @@ grouped_gemm_kernel(GroupedArgs a) {
   auto big_tile = [&](int64_t u, int *n0) -> GroupedRows {
     GroupedRows r;
     if constexpr (kUnits) {
-      const TileCoord tc = tile_of(u, units, tiles_n, kGemmGroupM);
-      const GroupUnit g = table_unit(&table, a.E, S::BM, static_cast<int>(tc.tm));
-      *n0 = static_cast<int>(tc.tn) * S::BN;
+      int tn;
+      const GroupUnit g = table_tile(&table, a.E, S::BM, tiles_n, u, &tn);
+      *n0 = tn * S::BN;
       r.group = g.group;
       r.row = g.row;
       r.rows = min(S::BM, g.end - g.row);
@@ -687,15 +685,12 @@ grouped_gemm_kernel(GroupedArgs a) {
   if constexpr (kUnits && kQuarters) {
     lights = table_light_units(&table, a.E, S::BM);
     const int64_t heavy = num_tiles - static_cast<int64_t>(lights) * tiles_n;
-    const bool apart = big_rounds(heavy, 2 * static_cast<int64_t>(lights) * tiles_n, grid) < big_rounds(num_tiles, 0, grid);
+    const bool apart =
+        big_rounds(heavy, 2 * static_cast<int64_t>(lights) * tiles_n, grid) < big_rounds(num_tiles, 0, grid);
+    lights = __builtin_amdgcn_readfirstlane(apart ? lights : 0);
+    num_tiles -= static_cast<int64_t>(lights) * tiles_n;
     __syncthreads();
-    if (apart) {
-      table_drop_light(&table, a.E, S::BM);
-      units -= lights;
-      num_tiles = heavy;
-    } else {
-      lights = 0;
-    }
+    if (lights > 0) table_drop_light(&table, a.E, S::BM);
     __syncthreads();
   }
   const int64_t whole = num_tiles / grid;
