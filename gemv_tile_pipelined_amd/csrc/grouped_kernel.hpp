@@ -41,7 +41,7 @@
 // Bound by the matrix cores, and by tiles that are not full or do not fill the
 // last round: 8192 rows in one group x 4096 x 2048 97 to 101 us, 1.4 PFLOP/s, the
 // rate of a plain product; over 16 uneven groups (8200 rows in 38 units; 33 would
-// hold them) 136 us, dgrad 143.  Loads ahead, staged stores and one loop body
+// hold them) 137 us, dgrad 141.  Loads ahead, staged stores and one loop body
 // took forward from 157 to 142, dgrad from 190 to 145, wgrad from 176 to 161 us.
 // Stores straight from the registers, in 64-byte pieces, were slower than staged
 // lines.  In wgrad a tile's sum is as short as its group (8 K tiles here), and of
