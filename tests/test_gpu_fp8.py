@@ -65,6 +65,25 @@ def test_large_tiles(env, M, N, K, sb_rows):
     _run(env, M, N, K, "bf16", sb_rows)
 
 
+@pytest.mark.parametrize("M,N,K", [(540700, 16, 8192), (540700, 4096, 16), (30, 540700, 8192), (3, 540700, 8192)])
+def test_past_32_bits(env, M, N, K):
+    """Operands and outputs of more than 2^32 bytes: what lies at their ends."""
+    torch, gt = env
+
+    def many(seed, rows):
+        (q, s), _, _ = _operand(torch, seed, min(rows, 4099), K, 1)
+        again = lambda t: t.repeat(-(-rows // len(t)), 1)[:rows].contiguous()  # noqa: E731
+        return again(q.view(torch.uint8)).view(q.dtype), again(s)
+
+    (A, sA), (B, sB) = many(1, M), many(2, N)
+    sB = sB[::128].contiguous()
+    D = gt.gemm_fp8_f16(A, sA, B, sB)
+    m, n = max(M - 70, 0), max(N - 70, 0) // 128 * 128
+    a, b = (e4m3_values(t.view(torch.uint8).cpu().numpy()) for t in (A[m:], B[n:]))
+    want = block_product(a, sA[m:].cpu().numpy(), b, sB[n // 128 :].cpu().numpy(), 128, "f16")
+    _check(D[m:, n:].double().cpu().numpy(), *want)
+
+
 @pytest.mark.parametrize("M,N,K", [(5, 40, 4096), (300, 260, 4096), (3500, 3600, 256)])
 def test_integers_are_exact(env, M, N, K):
     """Small integers and scales of powers of two: every partial sum is a number of the format."""

@@ -267,6 +267,103 @@ def test_offsets_out_of_order_stay_inside(env, op, rows):
     assert (out[0] == 0.5).all() and (out[2] == 0.5).all()
 
 
+@pytest.mark.parametrize("op", ["forward", "dgrad", "fp8"])
+@pytest.mark.parametrize("bad", [[-7, 2, 1, 4, 1 << 30, 3005, -(1 << 31)], [2000, 0, 2900, 100, 3000, 50, 3000], [3000] * 7,
+                                 [0, 3000, 0, 3000, 0, 3000, 0]], ids=["wild", "back", "none", "all"])
+def test_offsets_out_of_order_in_tiles(env, op, bad):
+    torch, gt = env
+    T, E, N, K = 3000, 6, 4096, 48
+    offsets = torch.tensor(bad, dtype=torch.int32, device="cuda")
+    one = lambda *s: torch.ones(s, device="cuda")  # noqa: E731
+    out = torch.full((3, T, K if op == "dgrad" else N), 0.5, device="cuda").half()
+    if op == "fp8":
+        e4m3 = torch.float8_e4m3fn
+        gt.gemm_grouped_fp8_f16(one(T, K).to(e4m3), one(T, 1), one(E, N, K).to(e4m3), one(E, N // 128, 1), offsets, out[1])
+    elif op == "dgrad":
+        gt.gemm_grouped_dgrad_f16(one(T, N).half(), one(E, N, K).half(), offsets, out[1])
+    else:
+        assert gt.grouped_plan(op, T, N, K, E, 256)[0] == "tiled"
+        gt.gemm_grouped_f16(one(T, K).half(), one(E, N, K).half(), offsets, out[1])
+    torch.cuda.synchronize()
+    assert (out[0] == 0.5).all() and (out[2] == 0.5).all()
+    assert ((out[1] == 0.5) | (out[1] == (N if op == "dgrad" else K))).all()
+
+
+@pytest.mark.parametrize("op", ["forward", "fp8"])
+@pytest.mark.parametrize("sizes", [[9, 40, 1, 64], [1] * 4, [700, 1300, 500, 3]], ids=["deep", "streamed", "tiled"])
+def test_two_calls_at_once(env, op, sizes):
+    """Two streams run the same product on different inputs, unordered."""
+    torch, gt = env
+    off, T, E, N, K = torch.from_numpy(_offsets(sizes)).cuda(), sum(sizes), len(sizes), 2048, 528
+    X, W = (_half(torch, i, s, "f16", 0.3).cuda() for i, s in enumerate(((2, T, K), (2, E, N, K))))
+    if op == "fp8":
+        ops = [(*gt.quantize_fp8_rows_f16(X[i]), *gt.quantize_fp8_tiles_f16(W[i])) for i in range(2)]
+        call = gt.gemm_grouped_fp8_f16
+    else:
+        ops, call = [(X[i], W[i]) for i in range(2)], gt.gemm_grouped_f16
+    alone = [call(*o, off) for o in ops]
+    outs = [[torch.empty_like(alone[i]) for _ in range(4)] for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for k in range(4):
+        for i in range(2):
+            call(*ops[i], off, outs[i][k], stream=streams[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, alone[i]) for i in range(2) for o in outs[i])
+
+
+# Operands and outputs of more than 2^32 bytes: what lies at their ends.
+FAR = [("forward", 540700, 3, 16, 4096), ("forward", 540700, 3, 4096, 16), ("dgrad", 540700, 3, 16, 4096),
+       ("dgrad", 540700, 3, 4096, 16), ("wgrad", 540700, 3, 4096, 16), ("wgrad", 540700, 3, 16, 4096),
+       ("fp8", 540700, 3, 16, 8192), ("fp8", 540700, 3, 4096, 16),
+       ("forward", 300, 70, 8192, 4096), ("forward", 900, 70, 8192, 4096), ("dgrad", 90, 70, 8192, 4096),
+       ("wgrad", 90, 70, 8192, 4096), ("fp8", 300, 70, 8192, 8192), ("fp8", 900, 70, 8192, 8192)]
+
+
+@pytest.mark.parametrize("op,T,E,N,K", FAR)
+def test_past_32_bits(env, op, T, E, N, K):
+    torch, gt = env
+    sizes = [0] * E
+    sizes[-1] = min(T, 700)
+    sizes[0] = T - sizes[-1]
+    off = _offsets(sizes)
+    offsets = torch.from_numpy(off).cuda()
+
+    def many(seed, rows, cols, scale=1.0):  # a few thousand rows, over and over
+        base = _half(torch, seed, (min(rows, 4099), cols), "f16", scale).cuda()
+        return base.repeat(-(-rows // len(base)), 1)[:rows].contiguous()
+
+    left = many(1, T, N if op in ("dgrad", "wgrad") else K)
+    if op == "wgrad":
+        right = many(2, T, K, 0.05)
+        dW = gt.gemm_grouped_wgrad_f16(left, right, offsets)
+        assert E < 4 or not dW[1:-1].any()
+        rows = slice(off[-2], off[-1])
+        dY, X = (t[rows].double().cpu().numpy() for t in (left, right))
+        _check(dW[-1].double().cpu().numpy(), *product(dY.T, X.T, "f16"), "last group")
+        return
+    weights = many(3, E * N, K, 0.05).view(E, N, K)
+    if op == "fp8":
+        left, weights = left.to(torch.float8_e4m3fn), weights.to(torch.float8_e4m3fn)
+        kb = -(-K // 128)
+        sX = many(4, T, kb).float().abs() + 0.25
+        sW = many(5, E * -(-N // 128), kb).float().abs().view(E, -1, kb) + 0.25
+        D = gt.gemm_grouped_fp8_f16(left, sX, weights, sW, offsets)
+    else:
+        D = (gt.gemm_grouped_dgrad_f16 if op == "dgrad" else gt.gemm_grouped_f16)(left, weights, offsets)
+    for e, rows in ((0, slice(max(off[1] - 70, 0), off[1])), (E - 1, slice(max(T - 70, off[-2]), T))):
+        if rows.start == rows.stop:
+            continue
+        got = D[rows].double().cpu().numpy()
+        if op == "fp8":
+            x, w = (e4m3_values(t.view(torch.uint8).cpu().numpy()) for t in (left[rows], weights[e]))
+            want = block_product(x, sX[rows].cpu().numpy(), w, sW[e].cpu().numpy(), 128, "f16")
+        else:
+            a, b = left[rows].double().cpu().numpy(), weights[e].double().cpu().numpy()
+            want = product(a, b.T if op == "dgrad" else b, "f16")
+        _check(got, *want, f"group {e}")
+
+
 @pytest.mark.parametrize("op", ["forward", "dgrad"])
 def test_sum_over_nothing(env, op):
     torch, gt = env
