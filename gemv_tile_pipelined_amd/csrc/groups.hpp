@@ -38,6 +38,13 @@ GT_HD inline GroupRows group_rows(int first, int next, int T) {
   return g;
 }
 
+// First row of a group's unit `at`, which offsets that are not non-decreasing can
+// make any number (the count of units may then overflow): kept in the group.
+GT_HD inline int unit_row(GroupRows g, int at, int rows) {
+  const int64_t row = g.begin + static_cast<int64_t>(at) * rows;
+  return row < g.begin ? g.begin : row > g.end ? g.end : static_cast<int>(row);
+}
+
 // No more units than this for T rows in E groups: every group's last unit may
 // be short, and no more groups than rows have any.
 GT_HD inline int64_t unit_bound(int64_t T, int64_t E, int64_t rows) {
@@ -115,8 +122,9 @@ __device__ inline bool find_unit(const int *__restrict__ offsets, int E, int T, 
         const int l = __builtin_ctzll(past);
         const int at = u - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(n, l));
         out->group = e0 + 64 * j + l;
-        out->row = __builtin_amdgcn_readlane(g.begin, l) + at * rows;
-        out->end = __builtin_amdgcn_readlane(g.end, l);
+        const GroupRows its{__builtin_amdgcn_readlane(g.begin, l), __builtin_amdgcn_readlane(g.end, l)};
+        out->row = unit_row(its, at, rows);
+        out->end = its.end;
         return true;
       }
       before = __builtin_amdgcn_readlane(upto, 63);
@@ -240,7 +248,8 @@ __device__ inline GroupUnit table_tile(const GroupTable<CAP> *table, int E, int 
   const int next = __builtin_amdgcn_readfirstlane(table->begin[e + 1]);
   const TileCoord tc = tile_of(u - static_cast<int64_t>(before) * tiles_n, units, tiles_n, kUnitsAcross);
   *tn = static_cast<int>(tc.tn);
-  return GroupUnit{__builtin_amdgcn_readfirstlane(e), begin + static_cast<int>(tc.tm) * rows, next < begin ? begin : next};
+  const GroupRows its{begin, next < begin ? begin : next};
+  return GroupUnit{__builtin_amdgcn_readfirstlane(e), unit_row(its, static_cast<int>(tc.tm), rows), its.end};
 }
 
 }  // namespace gt

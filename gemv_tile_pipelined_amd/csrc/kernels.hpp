@@ -329,7 +329,7 @@ hipError_t launch_quantize_rows(int dtype, const void *x, void *q, float *scale,
 hipError_t launch_quantize_tiles(int dtype, const void *x, void *q, float *scale, int E, int N, int K,
                                  hipStream_t stream);
 // stream.hip: few rows against weights read once; `out` and dtype kF16 or
-// kBF16, `rows` the rows of a unit (16, 32 or 64).
+// kBF16.
 hipError_t launch_stream_fp8(int out, const void *x, const float *sx, const void *w, const float *sw, int w_scale_rows,
                              void *d, int M, int N, int K, hipStream_t stream);
 hipError_t launch_stream_grouped(int dtype, const void *x, const void *w, const int *offsets, void *d, int T, int N,
@@ -351,7 +351,7 @@ hipError_t launch_deep_grouped(int dtype, const void *X, const void *W, const in
 hipError_t launch_deep_grouped_fp8(int out, const void *X, const float *sx, const void *W, const float *sw,
                                    const int *offsets, void *D, int T, int N, int K, int E, int num_cus,
                                    hipStream_t stream);
-// fp8_gemm.hip: tiled products of e4m3 operands (K > 0).
+// fp8_gemm.hip: tiled products of e4m3 operands.
 hipError_t launch_gemm_fp8(int out, const void *A, const float *sa, const void *B, const float *sb, int sb_rows, void *D,
                            int M, int N, int K, int num_cus, hipStream_t stream);
 hipError_t launch_grouped_fp8(int out, const void *X, const float *sx, const void *W, const float *sw, const int *offsets,
