@@ -427,7 +427,8 @@ int run_quantize(const void *x, void *q, float *scale, int64_t E, int64_t N, int
   if (x == nullptr || q == nullptr || scale == nullptr) return GEMVTILE_ERR_INVALID_ARG;
   if (K % 16 != 0 || E > kMax32 || N > kMax32 || K > kMax32) return GEMVTILE_ERR_UNSUPPORTED;
   const int64_t rows = tiles ? blocks_of(N) : N;
-  const int64_t most = tiles ? (int64_t{1} << 24) - 1 : (int64_t{1} << 29) - 1;
+  // A grid's threads are counted in 32 bits: 512 to a tile, 8 to a row block.
+  const int64_t most = tiles ? (int64_t{1} << 23) - 1 : (int64_t{1} << 29) - 32;
   if (rows > most / blocks_of(K) || E > most / (rows * blocks_of(K))) return GEMVTILE_ERR_UNSUPPORTED;
   if (misaligned(x, 16) || misaligned(q, 16) || misaligned(scale, 4)) return GEMVTILE_ERR_UNSUPPORTED;
   hipStream_t s = static_cast<hipStream_t>(stream);

@@ -20,8 +20,8 @@
 //
 // Bound by memory: 2 bytes read and 1 written per element, each once; a
 // block's elements stay in registers between the maximum and the rounding.
-// 8192 x 4096 by rows 19 us, 5.3 TB/s (a copy of a large tensor: 5.1); 4095 x
-// 14336 in tiles 39 us, 4.5 TB/s.
+// 8192 x 4096 by rows 19 us, 5.4 TB/s (a copy of a large tensor: 5.1); 4095 x
+// 14336 in tiles 34.5 us, 5.1 TB/s.
 #include "fp8_common.hpp"
 #include "groups.hpp"
 #include "kernels.hpp"
@@ -104,6 +104,8 @@ __device__ inline uint4_v quantize16(uint4_v v0, uint4_v v1, float scale, float 
 // Row blocks: 8 lanes hold a block's 128 columns, 16 each (one 16-byte store;
 // K % 16 == 0, so a lane's columns are all inside the row or all outside).
 // A wave's 8 blocks follow one another along the row and then down the rows.
+// q stays cached: non-temporal stores take 1.5 us off 8192 x 4096 alone (21.4 ->
+// 19.8), but the product that reads q next then takes 3 us longer.
 constexpr int kRowThreads = 256;
 constexpr int kRowBlocks = kRowThreads / 8;
 template <int DT>
@@ -128,13 +130,20 @@ quantize_rows_kernel(const uint16_t *__restrict__ x, uint8_t *__restrict__ q, fl
   if (k < K) *reinterpret_cast<uint4_v *>(q + at) = quantize16<DT>(v0, v1, s, 1.0f / s);
 }
 
-// Tiles: a workgroup holds a 128 x 128 tile, 8 lanes to a row, 32 rows at a
-// time.
-constexpr int kTileThreads = 256;
+// Whether the tiles' q leaves with non-temporal stores: when what is read and
+// written does not fit the L2s (32 MiB), so that a later reader would not find it
+// there anyway.  Cached and non-temporal: 4096 x 4096 12.1 and 10.7 us, 14336 x
+// 4096 35.0 and 33.7, 1000 x 1040 4.1 and 4.5.
+bool streamed(int64_t elements) { return elements > (int64_t{1} << 25) / 3; }
+
+// Tiles: a workgroup holds a 128 x 128 tile, 8 lanes to a row, 64 rows at a
+// time (4095 x 14336: 256 threads, 32 rows at a time, 40.7 us, 512 threads 36.5,
+// 1024 threads 46).
+constexpr int kTileThreads = 512;
 template <int DT>
 __global__ void __launch_bounds__(kTileThreads)
 quantize_tiles_kernel(const uint16_t *__restrict__ x, uint8_t *__restrict__ q, float *__restrict__ scale, int N, int K,
-                      int tiles_n, int tiles_k) {
+                      int tiles_n, int tiles_k, bool past_l2) {
   __shared__ uint32_t wave_max[kTileThreads / 64];
   constexpr int kPasses = kScaleBlock * 8 / kTileThreads;
   const unsigned per = static_cast<unsigned>(tiles_n) * static_cast<unsigned>(tiles_k);
@@ -169,8 +178,14 @@ quantize_tiles_kernel(const uint16_t *__restrict__ x, uint8_t *__restrict__ q, f
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
     const int n = n0 + p * (kTileThreads / 8) + (threadIdx.x >> 3);
-    if (n < N && k < K)
-      *reinterpret_cast<uint4_v *>(q + base + static_cast<int64_t>(n) * K) = quantize16<DT>(v[p][0], v[p][1], s, inv);
+    if (n < N && k < K) {
+      const uint4_v out = quantize16<DT>(v[p][0], v[p][1], s, inv);
+      uint4_v *const dst = reinterpret_cast<uint4_v *>(q + base + static_cast<int64_t>(n) * K);
+      if (past_l2)
+        __builtin_nontemporal_store(out, dst);
+      else
+        *dst = out;
+    }
   }
 }
 
@@ -192,7 +207,8 @@ hipError_t launch_quantize_tiles(int dtype, const void *x, void *q, float *scale
   const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(E) * tiles_n * tiles_k));
   const auto kernel = dtype == kBF16 ? quantize_tiles_kernel<kBF16> : quantize_tiles_kernel<kF16>;
   hipLaunchKernelGGL(kernel, grid, dim3(kTileThreads), 0, stream, static_cast<const uint16_t *>(x),
-                     static_cast<uint8_t *>(q), scale, N, K, tiles_n, tiles_k);
+                     static_cast<uint8_t *>(q), scale, N, K, tiles_n, tiles_k,
+                     streamed(static_cast<int64_t>(E) * N * K));
   return hipGetLastError();
 }
 

@@ -500,8 +500,8 @@ int64_t gemvtile_ring_trace(int variant, int64_t ktu, int32_t *events, int64_t c
  *
  *   x, q      device pointers, row-major, 16-byte aligned
  *   scale     device pointer, FP32, 4-byte aligned
- *   sizes     >= 0; K % 16 == 0; M * ceil(K/128) < 2^29 row blocks, E *
- *             ceil(N/128) * ceil(K/128) < 2^24 tiles, each of M, N, K < 2^31
+ *   sizes     >= 0; K % 16 == 0; M * ceil(K/128) <= 2^29 - 32 row blocks, E *
+ *             ceil(N/128) * ceil(K/128) < 2^23 tiles, each of M, N, K < 2^31
  * A size of 0 returns GEMVTILE_OK and touches nothing.
  */
 int quantize_fp8_rows_f16(const void *x, void *q, float *scale, int64_t M, int64_t K, void *stream);

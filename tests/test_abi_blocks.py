@@ -35,7 +35,7 @@ def test_quantize_rows(lib, fmt):
     assert f(P, P, P, 4, 24, None) == UNSUPPORTED
     for bad, off in ((0, 8), (1, 8), (2, 2)):
         assert f(*[P + off if i == bad else P for i in range(3)], 4, 16, None) == UNSUPPORTED
-    assert f(P, P, P, 1 << 29, 16, None) == UNSUPPORTED
+    assert f(P, P, P, (1 << 29) - 31, 16, None) == UNSUPPORTED
     assert f(P, P, P, 1 << 60, 1 << 60, None) == UNSUPPORTED
 
 
@@ -50,7 +50,7 @@ def test_quantize_tiles(lib, fmt):
         assert f(*[None if i == bad else P for i in range(3)], 1, 4, 16, None) == INVALID
     assert f(P, P, P, 1, 4, 8, None) == UNSUPPORTED
     assert f(P, P + 8, P, 1, 4, 16, None) == UNSUPPORTED
-    assert f(P, P, P, 1 << 24, 4, 16, None) == UNSUPPORTED
+    assert f(P, P, P, 1 << 23, 4, 16, None) == UNSUPPORTED
     assert f(P, P, P, 1 << 60, 1 << 60, 1 << 60, None) == UNSUPPORTED
 
 
