@@ -56,6 +56,7 @@ __all__ = [
     "alloc_splitk_workspace",
     "grouped_plan",
     "group_unit",
+    "grouped_ring_trace",
 ]
 
 LIBRARY_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgemvtile.so")
@@ -101,6 +102,7 @@ EXPORTED_SYMBOLS = (
     "gemm_grouped_fp8_bf16",
     "gemvtile_grouped_plan",
     "gemvtile_group_unit",
+    "gemvtile_grouped_ring_trace",
 )
 
 STATUS_NAMES = {
@@ -197,6 +199,8 @@ def load_library(path: str = LIBRARY_PATH) -> ctypes.CDLL:
     lib.gemvtile_grouped_plan.restype = c_int
     lib.gemvtile_group_unit.argtypes = [ctypes.POINTER(ctypes.c_int32)] + [i64] * 4 + [i64p] * 3
     lib.gemvtile_group_unit.restype = i64
+    lib.gemvtile_grouped_ring_trace.argtypes = [c_int] * 2 + [i64] * 2 + [ctypes.POINTER(ctypes.c_int32), i64, intp]
+    lib.gemvtile_grouped_ring_trace.restype = i64
     if path == LIBRARY_PATH:
         _lib = lib
     return lib
@@ -533,6 +537,20 @@ def grouped_plan(op: str, T: int, N: int, K: int, E: int, num_cus: int):
     if kind < 0:
         raise GemvTileError(1, "sizes out of range")
     return ("tiled", "stream", "deep")[kind], rows.value, cols.value
+
+
+def grouped_ring_trace(rows: int, cols: int, first: int, ktu: int):
+    """K tiles first .. ktu - 1 of the K loop that the tiled grouped kernels run for a rows x cols tile (host-only):
+    (events, info), events as ring_trace gives them and info = {"loads_per_tile", "stages", "ahead"}."""
+    lib = load_library()
+    info = (ctypes.c_int * 3)()
+    n = int(lib.gemvtile_grouped_ring_trace(rows, cols, first, ktu, None, 0, info))
+    if n < 0:
+        raise GemvTileError(1, f"no grouped kernel has {rows} x {cols} tiles, or the K tiles are out of range")
+    buf = (ctypes.c_int32 * (5 * n))()
+    lib.gemvtile_grouped_ring_trace(rows, cols, first, ktu, buf, n, info)
+    events = [(RING_EVENTS[buf[5 * i]], *buf[5 * i + 1 : 5 * i + 5]) for i in range(n)]
+    return events, dict(zip(("loads_per_tile", "stages", "ahead"), info))
 
 
 def group_unit(offsets, T: int, rows: int, unit: int):

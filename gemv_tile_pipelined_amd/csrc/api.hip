@@ -584,6 +584,14 @@ int gemvtile_grouped_plan(int op, int64_t T, int64_t N, int64_t K, int64_t E, in
   return 0;
 }
 
+int64_t gemvtile_grouped_ring_trace(int rows, int cols, int64_t first, int64_t ktu, int32_t *events, int64_t cap,
+                                    int *info) {
+  if (first < 0 || ktu <= first || ktu > kMaxRows / 64 || ktu - first > 4096 || cap < 0 ||
+      (events == nullptr && cap > 0) || info == nullptr)
+    return -1;
+  return gt::grouped_ring_trace(rows, cols, static_cast<int>(first), static_cast<int>(ktu), events, cap, info);
+}
+
 int64_t gemvtile_group_unit(const int32_t *offsets, int64_t E, int64_t T, int64_t rows, int64_t unit, int64_t *group,
                             int64_t *first, int64_t *past) {
   if (offsets == nullptr || E <= 0 || E > gt::kMaxGroups || T < 0 || T > kMaxRows || rows <= 0 || rows > 4096 || unit < 0 ||

@@ -226,38 +226,6 @@ hipError_t noalloc_scratch(void **ptr) {
 // that records each event instead of issuing it.
 namespace {
 template <class S>
-struct RingRecorder {
-  int stages;
-  int32_t *ev;
-  int64_t cap;
-  int64_t n = 0;
-  void push(int32_t code, int32_t a = 0, int32_t b = 0, int32_t c = 0, int32_t d = 0) {
-    if (ev != nullptr && n < cap) {
-      int32_t *e = ev + 5 * n;
-      e[0] = code;
-      e[1] = a;
-      e[2] = b;
-      e[3] = c;
-      e[4] = d;
-    }
-    ++n;
-  }
-  void mfma(int buf, int idx) { push(kRingMfma, buf, idx, S::mfma_i(idx), S::mfma_j(idx)); }
-  void read(int buf, int kt, int ks, int r) { push(kRingRead, kt, ks, r, ring_stage(kt, stages)); }
-  void load(int tile, int d) { push(kRingLoad, tile, d, ring_stage(tile, stages)); }
-  void mfma_load(int buf, int idx, int tile, int d) {
-    mfma(buf, idx);
-    load(tile, d);
-  }
-  void prep(int tile, int part) { push(kRingPrep, tile, part); }
-  void init_acc() { push(kRingInit); }
-  void wait_tile(int vmcnt) { push(kRingWaitTile, vmcnt); }
-  void wait_lds() { push(kRingWaitLds); }
-  void barrier() { push(kRingBarrier); }
-  void fence() {}
-};
-
-template <class S>
 int64_t record_ring(int ktu, int32_t *events, int64_t cap) {
   RingRecorder<S> rec{S::STAGES, events, cap};
   if constexpr (S::EARLY_FREE)

@@ -122,72 +122,82 @@ __device__ inline void build_wgrad_table(WgradTable<CAP> *table, const int *__re
   }
 }
 
-// The ring walker's operations (gemm_kernel.hpp), with waits that let `STORES`
-// younger stores of the tile before stay in flight while `stores` is set.
-template <class S, int STORES, class Base>
-struct GroupedRingOps : Base {
-  bool stores;
+// K tiles whose loads are issued ahead of a K loop.
+template <class S>
+GT_HD constexpr int grouped_ahead() {
+  return S::EARLY_FREE ? S::STAGES : S::STAGES - 1;
+}
+
+// The vmcnts of the loop's waits: the first, for the oldest K tile of those
+// issued ahead, and the one of every K tile after it.
+template <class S>
+struct GroupedWaits {
+  static constexpr int kFirst = (grouped_ahead<S>() - 1) * S::kDmaPerStage;
   static constexpr int loop_count() {
     if constexpr (S::EARLY_FREE)
       return RingEarly<S>::kSteadyVmcnt;
     else
       return (S::STAGES - 2) * S::kDmaPerStage;
   }
-  __device__ __attribute__((always_inline)) void wait_tile(int n) {
-    if (stores)
-      wait_counted<STORES>(n);
-    else
-      wait_counted<0>(n);
-    stores = false;
-  }
-  // n is one of the two counts of grouped_k_loop's waits.
-  template <int MORE>
-  __device__ __attribute__((always_inline)) void wait_counted(int n) {
-    constexpr int kLoop = loop_count();
-    if (n == kLoop)
-      wait_vmcnt<kLoop + MORE>();
-    else
-      wait_vmcnt<(S::STAGES - 1) * S::kDmaPerStage + MORE>();
-  }
+  static constexpr int kLoop = loop_count();
+  // What a K tile waits for where the walker asks for `n`: never fewer loads
+  // than asked for.
+  GT_HD static constexpr int in_loop(int n) { return n >= kLoop ? kLoop : 0; }
 };
 
-// K tiles whose loads are issued ahead of a K loop.
-template <class S>
-constexpr int grouped_ahead() {
-  return S::EARLY_FREE ? S::STAGES : S::STAGES - 1;
-}
+// The ring walker's operations (gemm_kernel.hpp), with waits that let `STORES`
+// younger stores of the tile before stay in flight while `stores` is set.
+template <class S, int STORES, class Base>
+struct GroupedRingOps : Base {
+  bool stores;
+  __device__ __attribute__((always_inline)) void wait_first(bool and_stores) {
+    if (and_stores)
+      wait_vmcnt<GroupedWaits<S>::kFirst + STORES>();
+    else
+      wait_vmcnt<GroupedWaits<S>::kFirst>();
+    stores = and_stores;  // the tile that the next wait is for is older than the stores as well
+  }
+  __device__ __attribute__((always_inline)) void wait_tile(int n) {
+    if (GroupedWaits<S>::in_loop(n) != GroupedWaits<S>::kLoop)
+      wait_vmcnt<0>();
+    else if (stores)
+      wait_vmcnt<GroupedWaits<S>::kLoop + STORES>();
+    else
+      wait_vmcnt<GroupedWaits<S>::kLoop>();
+    stores = false;
+  }
+};
 
 // ring.hpp's K loops from the point where the loads of the first tiles are
 // issued, with every K tile in the steady state: loads past the last K tile are
 // out of range and write zeros to stages that nothing reads any more, and the
-// operands read past it are not used.  One loop body instead of one for each
-// phase of the ring: through several, the accumulators did not keep their
-// registers.
+// operands read past it are not used.  The walker is told of STAGES more K
+// tiles from each one on, so that its counts are those of the steady state
+// however long the sum is.  One loop body instead of one for each phase of the
+// ring: through several, the accumulators did not keep their registers.
+// `first` is 0 but in the host-side trace.
 template <class S, class Ops>
-__device__ __attribute__((always_inline)) inline void grouped_k_loop(Ops &ops, int ktu, bool stores) {
-  constexpr int kEndless = 1 << 24;  // K tiles, for the walker's counts
+GT_RING_INLINE void grouped_k_loop(Ops &ops, int first, int ktu, bool stores) {
   ops.init_acc();
   ops.fence();
-  ops.stores = stores;
-  ops.wait_tile((grouped_ahead<S>() - 1) * S::kDmaPerStage);
-  ops.stores = stores;  // tile 1 is older than the stores as well
+  ops.wait_first(stores);
   ops.barrier();
 #pragma unroll
-  for (int r = 0; r < S::kReads; ++r) ops.read(0, 0, 0, r);
-  int kt = 0;
+  for (int r = 0; r < S::kReads; ++r) ops.read(0, first, 0, r);
+  int kt = first;
   if constexpr (S::EARLY_FREE) {
     for (; kt + 1 < ktu; kt += 2) {
-      ring_ktile_ef<S, true, true>(ops, kt, kEndless);
-      ring_ktile_ef<S, true, true>(ops, kt + 1, kEndless);
+      ring_ktile_ef<S, true, true>(ops, kt, kt + S::STAGES);
+      ring_ktile_ef<S, true, true>(ops, kt + 1, kt + 1 + S::STAGES);
     }
-    if (kt < ktu) ring_ktile_ef<S, true, true>(ops, kt, kEndless);
+    if (kt < ktu) ring_ktile_ef<S, true, true>(ops, kt, kt + S::STAGES);
   } else {
 #pragma unroll
     for (int pos = 0; pos < RingSlots<S>::kAfter; ++pos) {
       const int d = ring_slot_load<S>(pos);
-      if (d >= 0) ops.load(S::STAGES - 1, d);
+      if (d >= 0) ops.load(first + S::STAGES - 1, d);
     }
-    for (; kt < ktu; ++kt) ring_ktile<S, true, true, true>(ops, kt, kEndless);
+    for (; kt < ktu; ++kt) ring_ktile<S, true, true, true>(ops, kt, kt + S::STAGES);
   }
 }
 
@@ -517,7 +527,7 @@ __device__ __attribute__((always_inline)) inline void grouped_phase(const Groupe
     GroupedRingOps<S, kStores, Base> ops{{mfma, read_frag, load_one, mfma_load, prep, init_acc}, false};
     // The loop's last barrier comes after every wave's last read of its
     // operands: the ring is free.
-    grouped_k_loop<S>(ops, cur.KT, stores);
+    grouped_k_loop<S>(ops, 0, cur.KT, stores);
 
     GroupedTile after{};
     const bool more = next(&after);

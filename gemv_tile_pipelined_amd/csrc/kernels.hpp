@@ -364,6 +364,10 @@ hipError_t launch_grouped_dgrad(int dtype, const void *A, const void *B, const i
                                 int E, int num_cus, hipStream_t stream);
 hipError_t launch_grouped_wgrad(int dtype, const void *A, const void *B, const int *offsets, void *D, int T, int N, int K,
                                 int E, int num_cus, hipStream_t stream);
+// The host-side trace of the tiled grouped kernels' K loop (ring.hpp's events)
+// over K tiles first .. ktu - 1; info[0..2]: loads per wave and K tile, ring
+// stages, K tiles loaded ahead.  -1 for a tile that they do not have.
+int64_t grouped_ring_trace(int rows, int cols, int first, int ktu, int32_t *events, int64_t cap, int *info);
 // The output tile of the tiled grouped kernels (op 0 forward, 1 dgrad, 2
 // wgrad), and of the 8-bit ones.
 void grouped_plan_tile(int op, int64_t T, int64_t N, int64_t K, int64_t E, int num_cus, int *rows, int *cols);

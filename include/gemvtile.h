@@ -597,6 +597,20 @@ int gemm_grouped_fp8_bf16(const void *X, const float *scale_X, const void *W, co
 int gemvtile_grouped_plan(int op, int64_t T, int64_t N, int64_t K, int64_t E, int64_t num_cus, int *rows, int *cols);
 
 /*
+ * gemvtile_grouped_ring_trace -- the K loop of the tiled 16-bit grouped kernels
+ * for a `rows` x `cols` output tile (256x256, 256x128 or 128x128), as
+ * gemvtile_ring_trace records that of the tiled GEMM: K tiles first .. ktu - 1
+ * (of 64 elements of the sum; ktu <= 2^25 - 8, at most 4096 of them) as the loop
+ * walks them, after the loads of the first info[2] of them have been issued.
+ * Its loop has no drain: the loads past the last K tile fetch nothing.
+ * `events` as there; info, 3 ints: loads per wave and K tile, ring stages, K
+ * tiles loaded ahead.  Host-only; returns the number of events, or -1 for
+ * arguments out of range.
+ */
+int64_t gemvtile_grouped_ring_trace(int rows, int cols, int64_t first, int64_t ktu, int32_t *events, int64_t cap,
+                                    int *info);
+
+/*
  * gemvtile_group_unit -- the rows that unit `unit` of a grouped product covers
  * when every group's rows are cut into units of `rows`, as the kernels work it
  * out from the offsets (here in host memory).  Writes the group, its unit's
