@@ -5,12 +5,22 @@
 // infinities) and one FP32 scale for each block of `rows` x 128 of them
 // (scales [ceil(R / rows), ceil(K / 128)], rows = 1 or 128).
 //
-// The matrix cores multiply e4m3 numbers exactly and add a step's products in
-// a window aligned to the largest one: a sum over 128 products came out within
-// 2^-11 of its largest product (measured on normal and on uniformly random bit
-// patterns, all three FP8 MFMA shapes alike; 2^-16 relative to the result in
-// the mean).  Each 128-wide block's sum is then scaled and accumulated in
-// FP32.
+// A block's 128 products are added in one of two ways; its sum is then scaled
+// and accumulated in FP32.
+//  * stream.hip and deep.hip, which wait for memory: the numbers are widened to
+//    half precision, which holds every e4m3 number, and multiplied by the 16-bit
+//    MFMAs, which add in FP32.  With 8-bit and with 16-bit MFMAs: 1x4096x14336
+//    10.7 and 10.9 us, 27x8192x4096 8.1 and 8.5, 8 rows in 8 of 64 groups x 4096 x
+//    2048 12.8 and 12.8; 512x4096x4096, the most that deep.hip multiplies, 12 %
+//    more.
+//  * fp8_gemm.hip, which is bound by the matrix cores: the 8-bit MFMAs, at twice
+//    the 16-bit ones' rate (4096^3 in 16 bits takes 97 us, there 58 to 61).  They
+//    multiply exactly, but add products in a window aligned to the largest:
+//    beside 448 x 448, neighbouring products of 4 and less were lost and of 16
+//    kept (2^-15.6 and 2^-13.6 of it).  A sum over 128 came out within 2^-11 of
+//    its largest product (measured on normal and on uniformly random bit
+//    patterns, all three FP8 MFMA shapes alike; 2^-16 relative to the result in
+//    the mean, where rounding a result to bf16 loses up to 2^-8 and to e4m3 2^-4).
 #pragma once
 
 #include "device_common.hpp"
@@ -27,10 +37,39 @@ __device__ inline int8_v join(int4_t lo, int4_t hi) {
   return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// a . b + c over 128 e4m3 numbers of each of 16 rows of a and of b (the form
-// with no operand scales).
+// a . b + c over 128 e4m3 numbers of each of 16 rows of a and of b, added as an
+// 8-bit MFMA adds (the form with no operand scales).
 __device__ inline float4_t mfma_fp8(int8_v a, int8_v b, float4_t c) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
+}
+
+// The 32 bytes of an MFMA operand as 4 operands of 8 half-precision numbers.
+struct WideOperand {
+  half8_t part[4];
+};
+__device__ inline WideOperand widen_fp8(int8_v v) {
+  WideOperand w;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t four = static_cast<uint32_t>(v[i]);
+    const half2_t lo = __builtin_bit_cast(half2_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(four, 1.0f, false));
+    const half2_t hi = __builtin_bit_cast(half2_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(four, 1.0f, true));
+    half8_t &part = w.part[i / 2];
+    const int at = i % 2 * 4;
+    part[at] = lo[0];
+    part[at + 1] = lo[1];
+    part[at + 2] = hi[0];
+    part[at + 3] = hi[1];
+  }
+  return w;
+}
+
+// a . b over 128 widened numbers, added in FP32.
+__device__ inline float4_t mfma_wide(const WideOperand &a, const WideOperand &b) {
+  float4_t c{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.part[i], b.part[i], c, 0, 0, 0);
+  return c;
 }
 
 #pragma clang diagnostic push

@@ -8,9 +8,9 @@
 // Bound by reading W: a workgroup owns 16 or 32 rows of W and all of a unit's
 // rows of x (up to 16 of them), so each byte of W is read once per unit.  Its
 // waves split K in steps of 128 bytes of a row, which for 8-bit operands is
-// one scale block: a step is one 16x16x128 MFMA (two 16x16x32 of
-// 16-bit numbers), W rows first, so that lane l holds outputs
-// n = 4 (l / 16) + e of row l % 16 of x.  Its 8-bit sum is scaled by
+// one scale block: a step is two 16x16x32 MFMAs of 16-bit numbers or four of
+// widened 8-bit ones (fp8_common.hpp), W rows first, so that lane l holds
+// outputs n = 4 (l / 16) + e of row l % 16 of x.  Its 8-bit sum is scaled by
 // sx[row] * sw in FP32 as it joins the wave's running sum.  Lane l loads two
 // 16-byte pieces of row l % 16, pieces l / 16 and 4 + l / 16 of the step's
 // eight, so that an instruction reads 64 contiguous bytes of each of 16 rows;
@@ -124,11 +124,12 @@ __global__ void __launch_bounds__(WAVES * 64) stream_kernel(StreamArgs a) {
       // A step past the end multiplies zeros; its scales, which belong to the
       // next row, may be anything and count as zero.
       const bool past = s0 + u >= steps;
+      WideOperand wide_x;
+      if constexpr (kScaled) wide_x = widen_fp8(join(xv[u][0], xv[u][1]));
 #pragma unroll
       for (int p = 0; p < PB; ++p) {
         if constexpr (kScaled) {
-          const float4_t v =
-              mfma_fp8(join(wv[u][p][0], wv[u][p][1]), join(xv[u][0], xv[u][1]), float4_t{0.0f, 0.0f, 0.0f, 0.0f});
+          const float4_t v = mfma_wide(widen_fp8(join(wv[u][p][0], wv[u][p][1])), wide_x);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float scale = sxv[u] * swv[SW == 1 ? 4 * p + e : 0][u];

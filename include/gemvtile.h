@@ -526,9 +526,11 @@ int quantize_fp8_tiles_bf16(const void *x, void *q, float *scale, int64_t E, int
  *   D        device pointer, [M,N] fp16 / bf16, row-major, 2-byte aligned
  *   M, N, K  sizes; 0 <= M, N <= 2^25; 0 <= K <= 4,194,288 and K % 16 == 0
  *
- * The products within a block of 128 are exact; the matrix cores add them in
- * a window aligned to the largest (within 2^-11 of it); blocks are scaled and
- * added in FP32.  scale_A * scale_B is formed in FP32 and has to be a finite
+ * The products within a block of 128 are exact.  Up to 4 rows of A, or with no
+ * more 128x64 tiles of D than compute units, they are added in FP32; larger
+ * products use the 8-bit matrix instructions, which add them in a window
+ * aligned to the largest (within 2^-11 of it).  Blocks are scaled and added in
+ * FP32.  scale_A * scale_B is formed in FP32 and has to be a finite
  * number there for the result to be.  M == 0 or N == 0 touches nothing; K == 0
  * fills D with +0.  Results are deterministic.
  */
