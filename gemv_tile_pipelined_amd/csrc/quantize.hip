@@ -7,7 +7,8 @@
 // scale is the correctly rounded FP32 quotient.  The floor keeps the scale of
 // a block of zeros (or of values below 448 * 2^-80) a normal number whose
 // residuals below stay representable.  A NaN or an infinity in a block makes its
-// scale NaN or infinite, so that everything multiplied with the block is NaN.
+// scale NaN or infinite, so that everything multiplied with the block is NaN
+// (over an infinite scale finite numbers are zeros and infinities NaN).
 //
 // The nearest e4m3 number of the real quotient, not of its FP32 rounding: the
 // FP32 quotient may land exactly between two e4m3 numbers when the real one
@@ -68,6 +69,11 @@ __device__ inline float block_scale(uint32_t amax_bits) {
   return s < kMinScale ? kMinScale : s;  // a NaN stays
 }
 
+// What quotient_to_odd divides by.  An infinite scale (inv = 0) would make its
+// residuals NaN: beside any finite divisor finite x come out below the smallest
+// e4m3 number, and infinite ones NaN.
+__device__ inline float divisor(float scale) { return scale == __builtin_inff() ? 0x1.fffffep127f : scale; }
+
 // x / scale rounded to odd (see the top of the file); inv is about 1 / scale.
 __device__ inline float quotient_to_odd(float x, float scale, float inv) {
   const float a = __builtin_fabsf(x);
@@ -127,7 +133,7 @@ quantize_rows_kernel(const uint16_t *__restrict__ x, uint8_t *__restrict__ q, fl
   m = max_of_8_lanes(umax(m & 0xffffu, m >> 16));
   const float s = block_scale<DT>(m);
   if ((threadIdx.x & 7) == 0) scale[b] = s;
-  if (k < K) *reinterpret_cast<uint4_v *>(q + at) = quantize16<DT>(v0, v1, s, 1.0f / s);
+  if (k < K) *reinterpret_cast<uint4_v *>(q + at) = quantize16<DT>(v0, v1, divisor(s), 1.0f / s);
 }
 
 // Whether the tiles' q leaves with non-temporal stores: when what is read and
@@ -174,12 +180,12 @@ quantize_tiles_kernel(const uint16_t *__restrict__ x, uint8_t *__restrict__ q, f
   for (int w = 0; w < kTileThreads / 64; ++w) m = umax(m, wave_max[w]);
   const float s = block_scale<DT>(m);
   if (threadIdx.x == 0) scale[blockIdx.x] = s;
-  const float inv = 1.0f / s;
+  const float d = divisor(s), inv = 1.0f / s;
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
     const int n = n0 + p * (kTileThreads / 8) + (threadIdx.x >> 3);
     if (n < N && k < K) {
-      const uint4_v out = quantize16<DT>(v[p][0], v[p][1], s, inv);
+      const uint4_v out = quantize16<DT>(v[p][0], v[p][1], d, inv);
       uint4_v *const dst = reinterpret_cast<uint4_v *>(q + base + static_cast<int64_t>(n) * K);
       if (past_l2)
         __builtin_nontemporal_store(out, dst);

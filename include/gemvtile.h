@@ -495,8 +495,9 @@ int64_t gemvtile_ring_trace(int variant, int64_t ktu, int32_t *events, int64_t c
  *   q     = the e4m3 number nearest to x / scale (the real quotient), ties to even
  *
  * A block of zeros has scale 2^-80 and q = 0.  A block with an infinity has an
- * infinite scale and one with a NaN a NaN scale, so whatever is multiplied
- * with it comes out NaN.
+ * infinite scale (q = 0 for its finite numbers, NaN for the infinite) and one
+ * with a NaN a NaN scale (q = NaN), so whatever is multiplied with it comes out
+ * NaN.
  *
  *   x, q      device pointers, row-major, 16-byte aligned
  *   scale     device pointer, FP32, 4-byte aligned
