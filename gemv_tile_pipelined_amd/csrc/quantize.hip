@@ -116,14 +116,14 @@ constexpr int kRowThreads = 256;
 constexpr int kRowBlocks = kRowThreads / 8;
 template <int DT>
 __global__ void __launch_bounds__(kRowThreads)
-quantize_rows_kernel(const uint16_t *__restrict__ x, uint8_t *__restrict__ q, float *__restrict__ scale, int64_t blocks,
-                     int per_row, int K) {
-  const int64_t b = static_cast<int64_t>(blockIdx.x) * kRowBlocks + (threadIdx.x >> 3);
+quantize_rows_kernel(const uint16_t *__restrict__ x, uint8_t *__restrict__ q, float *__restrict__ scale, uint32_t blocks,
+                     uint32_t per_row, int K) {
+  // Fewer than 2^29 blocks (the library's limit): 32-bit numbers.
+  const uint32_t b = blockIdx.x * kRowBlocks + (threadIdx.x >> 3);
   if (b >= blocks) return;  // all 8 lanes of a block alike
-  const int64_t row = blocks <= 0x7fffffff ? static_cast<int64_t>(static_cast<uint32_t>(b) / static_cast<uint32_t>(per_row))
-                                           : b / per_row;
-  const int k = static_cast<int>(b - row * per_row) * kScaleBlock + (threadIdx.x & 7) * 16;
-  const int64_t at = row * K + k;
+  const uint32_t row = b / per_row;
+  const int k = static_cast<int>(b - row * per_row) * kScaleBlock + static_cast<int>(threadIdx.x & 7) * 16;
+  const int64_t at = static_cast<int64_t>(row) * K + k;
   uint4_v v0 = {0, 0, 0, 0}, v1 = {0, 0, 0, 0};
   if (k < K) {
     v0 = *reinterpret_cast<const uint4_v *>(x + at);
@@ -203,7 +203,7 @@ hipError_t launch_quantize_rows(int dtype, const void *x, void *q, float *scale,
   const dim3 grid(static_cast<unsigned>((blocks + kRowBlocks - 1) / kRowBlocks));
   const auto kernel = dtype == kBF16 ? quantize_rows_kernel<kBF16> : quantize_rows_kernel<kF16>;
   hipLaunchKernelGGL(kernel, grid, dim3(kRowThreads), 0, stream, static_cast<const uint16_t *>(x),
-                     static_cast<uint8_t *>(q), scale, blocks, per_row, K);
+                     static_cast<uint8_t *>(q), scale, static_cast<uint32_t>(blocks), static_cast<uint32_t>(per_row), K);
   return hipGetLastError();
 }
 
