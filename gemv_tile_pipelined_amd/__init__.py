@@ -55,6 +55,7 @@ __all__ = [
     "ring_trace",
     "alloc_splitk_workspace",
     "grouped_plan",
+    "grouped_stream_blocks",
     "group_unit",
     "grouped_ring_trace",
 ]
@@ -101,6 +102,7 @@ EXPORTED_SYMBOLS = (
     "gemm_grouped_fp8_f16",
     "gemm_grouped_fp8_bf16",
     "gemvtile_grouped_plan",
+    "gemvtile_grouped_stream_blocks",
     "gemvtile_group_unit",
     "gemvtile_grouped_ring_trace",
 )
@@ -197,6 +199,8 @@ def load_library(path: str = LIBRARY_PATH) -> ctypes.CDLL:
             call.restype = c_int
     lib.gemvtile_grouped_plan.argtypes = [c_int] + [i64] * 5 + [intp] * 2
     lib.gemvtile_grouped_plan.restype = c_int
+    lib.gemvtile_grouped_stream_blocks.argtypes = [c_int] + [i64] * 5
+    lib.gemvtile_grouped_stream_blocks.restype = c_int
     lib.gemvtile_group_unit.argtypes = [ctypes.POINTER(ctypes.c_int32)] + [i64] * 4 + [i64p] * 3
     lib.gemvtile_group_unit.restype = i64
     lib.gemvtile_grouped_ring_trace.argtypes = [c_int] * 2 + [i64] * 2 + [ctypes.POINTER(ctypes.c_int32), i64, intp]
@@ -530,13 +534,22 @@ GROUPED_OPS = {"forward": 0, "dgrad": 1, "wgrad": 2, "fp8": 3}
 
 def grouped_plan(op: str, T: int, N: int, K: int, E: int, num_cus: int):
     """("stream", "deep" or "tiled", rows, cols): the kernel a grouped product (op "forward", "dgrad", "wgrad" or "fp8") runs
-    on num_cus CUs, and the rows and columns of the output that a workgroup takes at a time."""
+    on num_cus CUs, and the rows and columns of the output that a workgroup takes at a time (of a streamed one: one block
+    of columns, see grouped_stream_blocks)."""
     rows, cols = ctypes.c_int(), ctypes.c_int()
     kind = int(load_library().gemvtile_grouped_plan(GROUPED_OPS[op], T, N, K, E, num_cus, ctypes.byref(rows),
                                                     ctypes.byref(cols)))
     if kind < 0:
         raise GemvTileError(1, "sizes out of range")
     return ("tiled", "stream", "deep")[kind], rows.value, cols.value
+
+
+def grouped_stream_blocks(op: str, T: int, N: int, K: int, E: int, num_cus: int) -> int:
+    """Blocks of 16 columns that a workgroup of a streamed grouped product takes (1 or 2)."""
+    n = int(load_library().gemvtile_grouped_stream_blocks(GROUPED_OPS[op], T, N, K, E, num_cus))
+    if n < 0:
+        raise GemvTileError(1, "not a streamed product, or sizes out of range")
+    return n
 
 
 def grouped_ring_trace(rows: int, cols: int, first: int, ktu: int):

@@ -574,7 +574,7 @@ int gemvtile_grouped_plan(int op, int64_t T, int64_t N, int64_t K, int64_t E, in
   }
   if (product && gt::grouped_streams(T, N, E)) {
     *rows = gt::kStreamUnit;
-    *cols = 16;
+    *cols = 16;  // a block; grouped_stream_blocks() says how many a workgroup has
     return 1;
   }
   if (op == kOpFp8)
@@ -582,6 +582,12 @@ int gemvtile_grouped_plan(int op, int64_t T, int64_t N, int64_t K, int64_t E, in
   else
     gt::grouped_plan_tile(op, T, N, K, E, static_cast<int>(num_cus), rows, cols);
   return 0;
+}
+
+int gemvtile_grouped_stream_blocks(int op, int64_t T, int64_t N, int64_t K, int64_t E, int64_t num_cus) {
+  int rows, cols;
+  if (gemvtile_grouped_plan(op, T, N, K, E, num_cus, &rows, &cols) != 1) return -1;
+  return gt::grouped_stream_blocks(T, N, E, static_cast<int>(num_cus));
 }
 
 int64_t gemvtile_grouped_ring_trace(int rows, int cols, int64_t first, int64_t ktu, int32_t *events, int64_t cap,

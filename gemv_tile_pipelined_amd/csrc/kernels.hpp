@@ -332,6 +332,9 @@ hipError_t launch_quantize_tiles(int dtype, const void *x, void *q, float *scale
 // kBF16.
 hipError_t launch_stream_fp8(int out, const void *x, const float *sx, const void *w, const float *sw, int w_scale_rows,
                              void *d, int M, int N, int K, hipStream_t stream);
+// 16-row blocks of W (columns of the output) that a workgroup of a streamed
+// grouped product takes.
+int grouped_stream_blocks(int64_t T, int64_t N, int64_t E, int num_cus);
 hipError_t launch_stream_grouped(int dtype, const void *x, const void *w, const int *offsets, void *d, int T, int N,
                                  int K, int E, int num_cus, hipStream_t stream);
 hipError_t launch_stream_grouped_fp8(int out, const void *x, const float *sx, const void *w, const float *sw,

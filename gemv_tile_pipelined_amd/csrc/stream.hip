@@ -180,11 +180,14 @@ hipError_t launch_one(StreamArgs a, int64_t units, hipStream_t stream) {
 //    16-bit 32 rows x 2048 x 2048 40.9, 41.8 and 38.7).
 //  * Else 16 rows of W, and 2 steps in flight instead of 4 where that leaves
 //    the slowest wave fewer steps (1x4096x14336, 112 steps: 12.1 -> 10.7 us).
+int stream_blocks(int64_t units, int64_t N, int num_cus) {
+  return units * ((N + 31) / 32) >= 2 * static_cast<int64_t>(num_cus) ? 2 : 1;
+}
+
 template <int IN, int OUT, bool GROUPED, int SW>
 hipError_t launch_rows(const StreamArgs &a, int64_t units, int num_cus, hipStream_t stream) {
   if constexpr (GROUPED) {
-    if (units * ((a.N + 31) / 32) >= 2 * static_cast<int64_t>(num_cus))
-      return launch_one<IN, OUT, 2, 4, 2, GROUPED, SW>(a, units, stream);
+    if (stream_blocks(units, a.N, num_cus) == 2) return launch_one<IN, OUT, 2, 4, 2, GROUPED, SW>(a, units, stream);
   }
   const int steps = (a.row_bytes + kStepBytes - 1) / kStepBytes;
   const bool two = (steps + 15) / 16 * 2 < (steps + 31) / 32 * 4;
@@ -193,6 +196,10 @@ hipError_t launch_rows(const StreamArgs &a, int64_t units, int num_cus, hipStrea
 }
 
 }  // namespace
+
+int grouped_stream_blocks(int64_t T, int64_t N, int64_t E, int num_cus) {
+  return stream_blocks(unit_bound(T, E, kStreamUnit), N, num_cus);
+}
 
 hipError_t launch_stream_fp8(int out, const void *x, const float *sx, const void *w, const float *sw, int w_scale_rows,
                              void *d, int M, int N, int K, hipStream_t stream) {

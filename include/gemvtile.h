@@ -593,11 +593,22 @@ int gemm_grouped_fp8_bf16(const void *X, const float *scale_X, const void *W, co
  * group's rows that one workgroup takes at a time, *cols the columns of the
  * output, and the return value 2 for the kernel of small tiles (no more of them
  * than compute units are expected), 1 for the one that streams W once (few rows
- * for each group), 0 for the tiled one (a last round of 256x256 16-bit tiles that
- * would keep at most half of the compute units busy is cut into 128x128 ones).
- * Host-only; returns -1 for arguments out of range.
+ * for each group; *cols is then one block of columns, of which a workgroup takes
+ * as many as gemvtile_grouped_stream_blocks says), 0 for the tiled one (a last
+ * round of 256x256 16-bit tiles that would keep at most half of the compute
+ * units busy is cut into 128x128 ones).  Host-only; returns -1 for arguments out
+ * of range.
  */
 int gemvtile_grouped_plan(int op, int64_t T, int64_t N, int64_t K, int64_t E, int64_t num_cus, int *rows, int *cols);
+
+/*
+ * gemvtile_grouped_stream_blocks -- for a grouped product that is streamed, the
+ * blocks of 16 columns of the output that a workgroup takes: 1, or 2 where there
+ * are then two workgroups for each compute unit.  Arguments as for
+ * gemvtile_grouped_plan.  Host-only; returns -1 for a product that is not
+ * streamed and for arguments out of range.
+ */
+int gemvtile_grouped_stream_blocks(int op, int64_t T, int64_t N, int64_t K, int64_t E, int64_t num_cus);
 
 /*
  * gemvtile_grouped_ring_trace -- the K loop of the tiled 16-bit grouped kernels
