@@ -154,8 +154,8 @@ def _gemm_fp8(A, scale_A, B, scale_B, D, stream, dtype, call):
 def gemm_fp8_f16(A, scale_A, B, scale_B, D=None, stream=None):
     """D = (A scaled) · (B scaled)ᵀ, rounded once to fp16.  A [M,K] and B [N,K] float8_e4m3fn, scale_A
     [M, ceil(K/128)], scale_B [ceil(N/128), ceil(K/128)] (a weight) or [N, ceil(K/128)] (both sides quantised by rows)
-    FP32, D [M,N]; all contiguous, K % 16 == 0.  Enqueued on `stream` (default: the current stream), not
-    synchronised.
+    FP32, D [M,N]; all contiguous, K % 16 == 0.  The product of two scales has to be a normal FP32 number (finite, 2^-126
+    or more) or zero.  Enqueued on `stream` (default: the current stream), not synchronised.
 
     The gradients of an 8-bit product are this call again: dA = dD · B takes dD quantised by rows and Bᵀ with its
     scales transposed; dB = dDᵀ · A takes dDᵀ and Aᵀ both quantised by rows."""

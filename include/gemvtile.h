@@ -531,8 +531,11 @@ int quantize_fp8_tiles_bf16(const void *x, void *q, float *scale, int64_t E, int
  * more 128x64 tiles of D than compute units, they are added in FP32; larger
  * products use the 8-bit matrix instructions, which add them in a window
  * aligned to the largest (within 2^-11 of it).  Blocks are scaled and added in
- * FP32.  scale_A * scale_B is formed in FP32 and has to be a finite
- * number there for the result to be.  M == 0 or N == 0 touches nothing; K == 0
+ * FP32.  scale_A * scale_B is formed in FP32 first: it has to be finite there
+ * for the result to be, and 2^-126 or more for full accuracy (below that it
+ * loses bits, and below 2^-149 it is 0, even where a block's sum of up to 2.5e7
+ * would bring the result into range; scales of the quantisers are 2^-80 or
+ * more).  M == 0 or N == 0 touches nothing; K == 0
  * fills D with +0.  Results are deterministic.
  */
 int gemm_fp8_f16(const void *A, const float *scale_A, const void *B, const float *scale_B, void *D, int64_t M, int64_t N,
