@@ -60,6 +60,12 @@ __all__ = [
     "grouped_ring_trace",
 ]
 
+# The tensor calls of blocks.py, found through __getattr__ below.
+BLOCK_CALLS = tuple(f"{name}_{fmt}" for name in ("quantize_fp8_rows", "quantize_fp8_tiles", "gemm_fp8", "gemm_grouped",
+                                                 "gemm_grouped_dgrad", "gemm_grouped_wgrad", "gemm_grouped_fp8")
+                    for fmt in ("f16", "bf16"))
+__all__ += BLOCK_CALLS
+
 LIBRARY_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgemvtile.so")
 
 # Every symbol include/gemvtile.h declares.
@@ -580,13 +586,16 @@ def group_unit(offsets, T: int, rows: int, unit: int):
 def __getattr__(name):
     # The 8-bit and grouped products (blocks.py) need torch to be imported; the
     # rest of the module imports it only when a tensor is passed.
-    if name == "blocks" or name.endswith(("_f16", "_bf16")):
+    if name == "blocks" or name in BLOCK_CALLS:
         import importlib
 
         blocks = importlib.import_module(".blocks", __name__)
         if name == "blocks":
             return blocks
-        if name in blocks.__all__:
-            value = globals()[name] = getattr(blocks, name)
-            return value
+        value = globals()[name] = getattr(blocks, name)
+        return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+def __dir__():
+    return sorted({*globals(), *BLOCK_CALLS, "blocks"})

@@ -17,11 +17,9 @@ import torch
 from torch import Tensor
 from torch._C import _cuda_getCurrentRawStream as _raw_stream
 
-from . import _check, _require, load_library
+from . import BLOCK_CALLS, _check, _require, load_library
 
-__all__ = [f"{name}_{fmt}" for name in ("quantize_fp8_rows", "quantize_fp8_tiles", "gemm_fp8", "gemm_grouped",
-                                        "gemm_grouped_dgrad", "gemm_grouped_wgrad", "gemm_grouped_fp8")
-           for fmt in ("f16", "bf16")]
+__all__ = list(BLOCK_CALLS)
 
 FP8 = torch.float8_e4m3fn
 BLOCK = 128
