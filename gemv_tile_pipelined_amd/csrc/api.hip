@@ -335,7 +335,7 @@ int gemvtile_tile_coord(int64_t t, int64_t tiles_m, int64_t tiles_n, int64_t gro
 
 int64_t gemvtile_ring_trace(int variant, int64_t ktu, int32_t *events, int64_t cap, int *info) {
   if (ktu < 1 || ktu > (int64_t{1} << 20) || cap < 0 || (events == nullptr && cap > 0)) return -1;
-  int dummy[8];
+  int dummy[gt::kRingInfo];
   return gt::ring_trace(variant, static_cast<int>(ktu), events, cap, info != nullptr ? info : dummy);
 }
 

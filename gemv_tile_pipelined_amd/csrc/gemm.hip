@@ -249,6 +249,7 @@ int64_t ring_trace(int variant, int ktu, int32_t *events, int64_t cap, int *info
     info[7] = S::EARLY_FREE ? 1 : 0;
     info[8] = S::WAVES_M;
     info[9] = S::WAVES_N;
+    static_assert(kRingInfo == 10, "all of info, and no more");
     return record_ring<S>(ktu, events, cap);
   };
   switch (variant) {

@@ -281,9 +281,11 @@ constexpr unsigned kWaitLgkm0 = 0xC07F;
 // ktu K tiles, as the host-side trace of the ring walker (ring.hpp): up to
 // `cap` events of five int32 each are written to `events` (which may be
 // NULL); returns the number of events, or -1 for a variant without a ring.
-// info[0..7] receive the kernel's loads per wave per K tile, operand reads
-// and MFMAs per wave per K step, K steps per K tile, ring stages, bm, bn and
-// whether it runs the early-free schedule (1) or not (0).
+// info[0 .. kRingInfo - 1] receive the kernel's loads per wave per K tile,
+// operand reads per wave per K step, K steps per K tile, MFMAs per wave per K
+// step, ring stages, bm, bn, whether it runs the early-free schedule (1) or not
+// (0), and the waves along the tile's rows and columns.
+constexpr int kRingInfo = 10;
 int64_t ring_trace(int variant, int ktu, int32_t *events, int64_t cap, int *info);
 // The 256x256 tiled kernel of gemm_f16 with per-workgroup timestamps
 // (kEpiTimed in gemm_kernel.hpp) written to stamps[8 * workgroup ...].
