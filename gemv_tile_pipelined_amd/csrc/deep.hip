@@ -84,7 +84,7 @@ __device__ inline int4_t half_of(int8_v v, int h) {
 }
 
 // IN: kF16, kBF16 (16-bit operands, no scales: two MFMAs of 32 per 128 bytes) or
-// kE4m3 (four, of widened numbers: fp8_common.hpp).  SB: rows of B per scale.
+// kE4m3.  SB: rows of B per scale.
 template <class S, int IN, int OUT, bool GROUPED, int SB>
 __global__ void __launch_bounds__(S::kThreads) deep_kernel(DeepArgs a) {
   __shared__ __attribute__((aligned(1024))) char smem[S::kRingBytes];
@@ -202,18 +202,12 @@ __global__ void __launch_bounds__(S::kThreads) deep_kernel(DeepArgs a) {
   };
   auto products = [&](auto buffer) {
     constexpr int P = decltype(buffer)::value;
-    WideOperand wide_a[S::kFragM];
-    if constexpr (kScaled) {
-#pragma unroll
-      for (int i = 0; i < S::kFragM; ++i) wide_a[i] = widen_fp8(fa[P][i]);
-    }
 #pragma unroll
     for (int j = 0; j < S::kFragN; ++j) {
       if constexpr (kScaled) {
-        const WideOperand wide_b = widen_fp8(fb[P][j]);
         float4_t part[S::kFragM];
 #pragma unroll
-        for (int i = 0; i < S::kFragM; ++i) part[i] = mfma_wide(wide_b, wide_a[i]);
+        for (int i = 0; i < S::kFragM; ++i) part[i] = mfma_fp8(fb[P][j], fa[P][i], float4_t{0.0f, 0.0f, 0.0f, 0.0f});
 #pragma unroll
         for (int i = 0; i < S::kFragM; ++i)
 #pragma unroll

@@ -7,20 +7,21 @@
 //
 // A block's 128 products are added in one of two ways; its sum is then scaled
 // and accumulated in FP32.
-//  * stream.hip and deep.hip, which wait for memory: the numbers are widened to
-//    half precision, which holds every e4m3 number, and multiplied by the 16-bit
+//  * stream.hip, which waits for memory: the numbers are widened to half
+//    precision, which holds every e4m3 number, and multiplied by the 16-bit
 //    MFMAs, which add in FP32.  With 8-bit and with 16-bit MFMAs: 1x4096x14336
-//    10.7 and 10.9 us, 27x8192x4096 8.1 and 8.5, 8 rows in 8 of 64 groups x 4096 x
-//    2048 12.8 and 12.8; 512x4096x4096, the most that deep.hip multiplies, 12 %
-//    more.
-//  * fp8_gemm.hip, which is bound by the matrix cores: the 8-bit MFMAs, at twice
-//    the 16-bit ones' rate (4096^3 in 16 bits takes 97 us, there 58 to 61).  They
-//    multiply exactly, but add products in a window aligned to the largest:
-//    beside 448 x 448, neighbouring products of 4 and less were lost and of 16
-//    kept (2^-15.6 and 2^-13.6 of it).  A sum over 128 came out within 2^-11 of
-//    its largest product (measured on normal and on uniformly random bit
-//    patterns, all three FP8 MFMA shapes alike; 2^-16 relative to the result in
-//    the mean, where rounding a result to bf16 loses up to 2^-8 and to e4m3 2^-4).
+//    10.8 and 10.9 us, 4x4096x4096 5.1 and 5.3, 4x28672x4096 22.7 and 23.4, 256
+//    rows in 64 groups x 2048 x 4096 97.6 and 97.0.
+//  * deep.hip and fp8_gemm.hip: the 8-bit MFMAs, at twice the 16-bit ones' rate
+//    and with nothing to widen (4096^3 in 16 bits takes 97 us, in fp8_gemm.hip 58
+//    to 61; deep.hip took 12.4 us with them and 15.9 with widened numbers for
+//    16x4096x14336, 11.3 and 14.7 for 256x4096x4096).  They multiply exactly,
+//    but add products in a window aligned to the largest: beside 448 x 448,
+//    neighbouring products of 4 and less were lost and of 16 kept (2^-15.6 and
+//    2^-13.6 of it).  A sum over 128 came out within 2^-11 of its largest product
+//    (measured on normal and on uniformly random bit patterns, all three FP8 MFMA
+//    shapes alike; 2^-16 relative to the result in the mean, where rounding a
+//    result to bf16 loses up to 2^-8 and to e4m3 2^-4).
 #pragma once
 
 #include "device_common.hpp"
@@ -64,12 +65,20 @@ __device__ inline WideOperand widen_fp8(int8_v v) {
   return w;
 }
 
-// a . b over 128 widened numbers, added in FP32.
+// a . b over 128 widened numbers, added in FP32: in one chain of MFMAs, or in
+// two, which take half as long one after another where a wave has no other MFMAs
+// to run meanwhile.
+template <int CHAINS>
 __device__ inline float4_t mfma_wide(const WideOperand &a, const WideOperand &b) {
-  float4_t c{0.0f, 0.0f, 0.0f, 0.0f};
+  static_assert(CHAINS == 1 || CHAINS == 2, "4 MFMAs");
+  float4_t c[CHAINS];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.part[i], b.part[i], c, 0, 0, 0);
-  return c;
+  for (int i = 0; i < CHAINS; ++i) c[i] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    c[i % CHAINS] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.part[i], b.part[i], c[i % CHAINS], 0, 0, 0);
+  if constexpr (CHAINS == 2) c[0] += c[1];
+  return c[0];
 }
 
 #pragma clang diagnostic push

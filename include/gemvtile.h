@@ -527,10 +527,10 @@ int quantize_fp8_tiles_bf16(const void *x, void *q, float *scale, int64_t E, int
  *   D        device pointer, [M,N] fp16 / bf16, row-major, 2-byte aligned
  *   M, N, K  sizes; 0 <= M, N <= 2^25; 0 <= K <= 4,194,288 and K % 16 == 0
  *
- * The products within a block of 128 are exact.  Up to 4 rows of A, or with no
- * more 128x64 tiles of D than compute units, they are added in FP32; larger
- * products use the 8-bit matrix instructions, which add them in a window
- * aligned to the largest (within 2^-11 of it).  Blocks are scaled and added in
+ * The products within a block of 128 are exact.  With up to 4 rows of A they
+ * are added in FP32; larger products use the 8-bit matrix instructions, which
+ * add them in a window aligned to the largest (within 2^-11 of it).  (Grouped:
+ * in FP32 where gemvtile_grouped_plan returns 1.)  Blocks are scaled and added in
  * FP32.  scale_A * scale_B is formed in FP32 first: it has to be finite there
  * for the result to be, and 2^-126 or more for full accuracy (below that it
  * loses bits, and below 2^-149 it is 0, even where a block's sum of up to 2.5e7
