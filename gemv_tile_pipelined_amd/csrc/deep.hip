@@ -13,20 +13,25 @@
 //
 // Measured (MI355X, us; M x 4096 x 4096 in 8 bits):
 //             streamed  32x32  32x64  64x64  tiles of fp8_gemm.hip
-//   M =   4        5.4    6.3    8.3    9.5   15.9
-//        17        6.6    6.2    8.2    9.7   16.0
-//        64       12.5    7.1    8.6   11.1   16.3
-//       128               11.8    9.0   11.0   19.0
-//       256               21.5   15.9   11.3   19.0
-//       512 (128x64: 17.7)                     19.4
+//   M =   4        5.2    6.2    8.3    9.5   15.9
+//        16        6.1    6.3                 15.9
+//        17               6.2    8.2    9.7   15.9
+//        64               7.1    8.6   11.1   16.3
+//       128              11.8    8.7   11.0   18.8
+//       256              21.5   15.9   11.3   19.0
+//       512 (128x64: 18.0)                    19.2
 // One team (64x64, 8 stages) 13.8 us at M = 128, four of half the depth 13.2, two
 // 11.1; loads issued before a step's reads and MFMAs 11.1, between them 11.6.
-// Streaming (stream.hip) reads x again for every 16 rows of W: M = 16 of
-// 4096x14336 16.3 and here 12.6, of 28672x4096 30.8 and 27.5; M = 4 11.9 and
-// 12.3, 23.8 and 26.8; M = 8 13.3 and 12.3, 27.9 and 28.3.
-// Groups (8 of 512 rows in all, x 2048 x 4096, 128x64 tiles): 8 bits 17.7 us,
-// tiles of fp8_gemm.hip 21.6; bf16 28.3, tiles of grouped_kernel.hpp 37.7.  24
-// rows over 8 groups x 2048 x 2048 (32x64): 7.5 and 10.9, streamed 8.8 and 13.0.
+// Streaming (stream.hip) reads x again for every 16 rows of W: against 4096x14336
+// it takes 11.8, 13.0 and 15.9 us for M = 4, 8 and 16, and small tiles 12.0, 12.2
+// and 12.4.  (28672x4096 has more 128x64 tiles than there are CUs: from M = 5 on
+// it goes to fp8_gemm.hip, 28.4 and 28.5 us for M = 8 and 16; streamed 27.0 and
+// 31.7, and 23.6 for M = 4, which is streamed.)
+// Just past a fit the larger tile costs: 1024x1024x8192 (64x64) 18.4 us,
+// 1024x1025x8192 (128x64) 31.9.
+// Groups (512 uneven rows over 8, x 2048 x 4096, 128x64 tiles): 8 bits 17.4 us,
+// tiles of fp8_gemm.hip 20.5; bf16 33.7, tiles of grouped_kernel.hpp 40.9.  24
+// rows over 8 groups x 2048 x 2048 (32x64): 8.0 and 10.7, streamed 8.5 and 12.8.
 #include "fp8_common.hpp"
 #include "groups.hpp"
 #include "kernels.hpp"

@@ -9,8 +9,10 @@
 // matrix cores cannot accumulate across blocks themselves.  The FMAs need the
 // accumulators in ordinary VGPRs (not AGPRs), 256 of which a wave has beside
 // nothing else if two waves share a SIMD; hence 8 waves with 64x128 outputs
-// each (128 accumulators) on a 256x256 tile, two to a SIMD, so that one wave's
-// FMAs and LDS reads run beside the other's MFMAs.
+// each (128 accumulators) on a 256x256 tile, two to a SIMD.  One wave's FMAs and
+// LDS reads were to run beside the other's MFMAs, but the counters show little
+// of that: MFMAs take 63 % of a SIMD's cycles at 4096^3 and vector instructions
+// 38 %, one after the other.
 //
 // The ring holds STAGES K tiles: the operands' rows (direct-to-LDS loads,
 // swizzled as in gemm_kernel.hpp) and the scale of every row of A and of B for
@@ -24,10 +26,11 @@
 // workgroup on the CU (2048 rows over 8 groups x 2048 x 2048: 19.4 us, 29 with
 // loads ahead).
 //
-// Bound by the matrix cores and the power they draw: 4096^3 58 to 61 us, 2.3
-// PFLOP/s, 8192^3 434 us, 2.5 PFLOP/s, matrix cores busy 63 % of the cycles at
-// 4096^3.  With a scale for each row of B (r = 1) every FMA needs a product of
-// scales beside it, eight VALU instructions for each MFMA: 4000x4096x4112 76 us.
+// Bound by MFMAs and vector instructions in sum, and by the power they draw:
+// 4096^3 58 to 61 us, 2.3 PFLOP/s, 8192^3 434 us, 2.5 PFLOP/s.  With a scale for
+// each row of B (r = 1) every FMA needs a product of scales beside it, eight VALU
+// instructions for each MFMA: 4000x4096x4112 76 us (with 4035 odd columns 85;
+// there MFMAs take 38 % of the cycles and vector instructions 45 %).
 #include "fp8_common.hpp"
 #include "groups.hpp"
 #include "kernels.hpp"

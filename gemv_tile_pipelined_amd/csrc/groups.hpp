@@ -66,7 +66,7 @@ inline int64_t expected_units(int64_t T, int64_t E, int64_t rows) {
 // the mean rows of a group, or tiled.  Measured (bf16, us streamed and tiled):
 // 32 groups x 2048 x 2048 with a mean of 4 rows 51 and 62, 8 rows 58 and 66, 12
 // rows 65 and 66, 16 rows 74 and 67, 32 rows 113 and 67; 8 bits, 64 groups x
-// 2048 x 4096: 96 and 125, 110 and 130, 126 and 130, 146 and 131, 228 and 129.
+// 2048 x 4096: 97 and 120, 107 and 121, 113 and 121, 121 and 120, 202 and 115.
 constexpr int kStreamUnit = 16;
 inline bool grouped_streams(int64_t T, int64_t N, int64_t E) {
   // A grid's threads are counted in 32 bits.

@@ -178,10 +178,10 @@ hipError_t launch_one(StreamArgs a, int64_t units, hipStream_t stream) {
 // The launch shape.  Measured (MI355X; PB x WAVES x UNROLL):
 //  * Many groups make many workgroups of little work: small ones of 32 rows of
 //    W with few loads in flight each, so that more of them share a CU (8 bits,
-//    64 rows in 64 groups x 2048 x 4096: 1x8x4 84 us, 2x8x4 67, 2x4x2 65;
+//    a row in each of 64 groups x 2048 x 4096: 1x8x4 109 us, 2x8x4 115, 2x4x2 93;
 //    16-bit 32 rows x 2048 x 2048 40.9, 41.8 and 38.7).
 //  * Else 16 rows of W, and 2 steps in flight instead of 4 where that leaves
-//    the slowest wave fewer steps (1x4096x14336, 112 steps: 12.1 -> 10.7 us).
+//    the slowest wave fewer steps (1x4096x14336, 112 steps: 11.8 -> 10.9 us).
 int stream_blocks(int64_t units, int64_t N, int num_cus) {
   return units * ((N + 31) / 32) >= 2 * static_cast<int64_t>(num_cus) ? 2 : 1;
 }
