@@ -4,8 +4,10 @@
     gemv_f16(x, W, y=None)   y = x · Wᵀ   x [K],   W [N,K], y [N]
 
 Block-scaled 8-bit products, their quantisers and products grouped by expert
-(gemm_fp8_*, quantize_fp8_*, gemm_grouped_*) are in blocks.py and reached from
-here as well.
+(gemm_fp8_*, quantize_fp8_*, gemm_grouped_*) are in blocks.py; products with 4-bit
+weights, norms, the routing to experts and the rows' way there and back
+(quantize_fp4_*, gemv_fp4_*, rmsnorm_*, route_*) in layer.py.  Both are reached
+from here as well.
 
 This module only marshals arguments: it checks tensor dtypes, devices and
 shapes, passes raw device pointers, sizes and the current HIP stream to
@@ -66,6 +68,14 @@ BLOCK_CALLS = tuple(f"{name}_{fmt}" for name in ("quantize_fp8_rows", "quantize_
                     for fmt in ("f16", "bf16"))
 __all__ += BLOCK_CALLS
 
+# The library's calls that layer.py makes on tensors, and what else it offers, found the same way.
+LAYER_CALLS = tuple(f"{name}_{fmt}" for name in ("quantize_fp4", "gemv_fp4", "rmsnorm", "rmsnorm_fp8", "rmsnorm_grad",
+                                                 "route_topk", "route_topk_grad", "route_gather", "route_combine",
+                                                 "route_combine_grad")
+                    for fmt in ("f16", "bf16")) + ("route_topk_f32", "route_topk_grad_f32", "route_gather_fp8", "route_sort")
+LAYER_NAMES = LAYER_CALLS + ("alloc_rmsnorm_grad_workspace", "alloc_route_sort_workspace")
+__all__ += LAYER_NAMES
+
 LIBRARY_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgemvtile.so")
 
 # Every symbol include/gemvtile.h declares.
@@ -111,6 +121,9 @@ EXPORTED_SYMBOLS = (
     "gemvtile_grouped_stream_blocks",
     "gemvtile_group_unit",
     "gemvtile_grouped_ring_trace",
+    *LAYER_CALLS,
+    "gemvtile_rmsnorm_grad_workspace",
+    "gemvtile_route_sort_workspace",
 )
 
 STATUS_NAMES = {
@@ -203,6 +216,27 @@ def load_library(path: str = LIBRARY_PATH) -> ctypes.CDLL:
             call = getattr(lib, f"{name}_{fmt}")
             call.argtypes = [*args, vp]
             call.restype = c_int
+    f32 = ctypes.c_float
+    for name, args in (("quantize_fp4", [vp] * 3 + [i64] * 2), ("gemv_fp4", [vp] * 4 + [i64] * 3),
+                       ("rmsnorm", [vp] * 6 + [i64] * 2 + [f32]), ("rmsnorm_fp8", [vp] * 8 + [i64] * 2 + [f32]),
+                       ("rmsnorm_grad", [vp] * 7 + [i64] * 2 + [vp, i64]),
+                       ("route_topk", [vp] * 4 + [i64] * 5 + [c_int] * 3 + [f32]),
+                       ("route_topk_grad", [vp] * 4 + [i64] * 3 + [c_int] * 2 + [f32]),
+                       ("route_gather", [vp] * 3 + [i64] * 4), ("route_combine", [vp] * 4 + [i64] * 4),
+                       ("route_combine_grad", [vp] * 6 + [i64] * 4)):
+        for fmt in ("f16", "bf16", "f32"):
+            if f"{name}_{fmt}" in LAYER_CALLS:
+                call = getattr(lib, f"{name}_{fmt}")
+                call.argtypes = [*args, vp]
+                call.restype = c_int
+    lib.route_gather_fp8.argtypes = [vp] * 5 + [i64] * 4 + [vp]
+    lib.route_gather_fp8.restype = c_int
+    lib.route_sort.argtypes = [vp] * 3 + [i64] * 3 + [vp, i64, vp]
+    lib.route_sort.restype = c_int
+    lib.gemvtile_rmsnorm_grad_workspace.argtypes = [i64] * 2
+    lib.gemvtile_rmsnorm_grad_workspace.restype = i64
+    lib.gemvtile_route_sort_workspace.argtypes = [i64] * 3
+    lib.gemvtile_route_sort_workspace.restype = i64
     lib.gemvtile_grouped_plan.argtypes = [c_int] + [i64] * 5 + [intp] * 2
     lib.gemvtile_grouped_plan.restype = c_int
     lib.gemvtile_grouped_stream_blocks.argtypes = [c_int] + [i64] * 5
@@ -584,18 +618,19 @@ def group_unit(offsets, T: int, rows: int, unit: int):
 
 
 def __getattr__(name):
-    # The 8-bit and grouped products (blocks.py) need torch to be imported; the
-    # rest of the module imports it only when a tensor is passed.
-    if name == "blocks" or name in BLOCK_CALLS:
-        import importlib
+    # The calls of blocks.py and layer.py need torch to be imported; the rest of
+    # the module imports it only when a tensor is passed.
+    home = "blocks" if name == "blocks" or name in BLOCK_CALLS else "layer" if name == "layer" or name in LAYER_NAMES else None
+    if home is None:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    import importlib
 
-        blocks = importlib.import_module(".blocks", __name__)
-        if name == "blocks":
-            return blocks
-        value = globals()[name] = getattr(blocks, name)
-        return value
-    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    module = importlib.import_module(f".{home}", __name__)
+    if name == home:
+        return module
+    value = globals()[name] = getattr(module, name)
+    return value
 
 
 def __dir__():
-    return sorted({*globals(), *BLOCK_CALLS, "blocks"})
+    return sorted({*globals(), *BLOCK_CALLS, *LAYER_NAMES, "blocks", "layer"})

@@ -41,7 +41,8 @@ REPO_DIR = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 SOURCES = [os.path.join(CSRC, f) for f in ("api.hip", "gemm.hip", "gemm_plain.hip", "gemm_ws.hip", "gemv.hip", "skinny.hip",
                                            "quantize.hip", "stream.hip", "deep.hip", "fp8_gemm.hip", "grouped_forward.hip",
-                                           "grouped_dgrad.hip", "grouped_wgrad.hip")]
+                                           "grouped_dgrad.hip", "grouped_wgrad.hip", "layer_api.hip", "fp4.hip",
+                                           "norm.hip", "route.hip", "rows.hip")]
 LIBRARY = os.path.join(PKG_DIR, "libgemvtile.so")
 ARCH = "gfx950"
 

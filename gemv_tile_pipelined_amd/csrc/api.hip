@@ -7,14 +7,17 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <atomic>
-
 #include "../../include/gemvtile.h"
+#include "api_common.hpp"
 #include "groups.hpp"
 #include "kernels.hpp"
 #include "tile_order.hpp"
 
 namespace {
+
+using gt::current_cu_count;
+using gt::misaligned;
+using gt::to_status;
 
 // Largest M or N: tile origins and row indices are 32-bit in the kernels, and
 // a whole tile past the last row must still be addressable.
@@ -24,30 +27,6 @@ constexpr int64_t kMaxRows = (int64_t{1} << 31) - 512;
 constexpr int64_t kMaxGemmK = 4194296;
 // Largest K of the GEMV (chunk indices are 32-bit).
 constexpr int64_t kMaxGemvK = (int64_t{1} << 31) - 8;
-
-constexpr int kMaxDevices = 64;
-std::atomic<int> g_cu_count[kMaxDevices];
-
-bool misaligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) != 0; }
-
-// Compute units of the current device, cached per device.
-int current_cu_count(int *out) {
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess) return GEMVTILE_ERR_DEVICE;
-  if (dev >= 0 && dev < kMaxDevices) {
-    const int cached = g_cu_count[dev].load(std::memory_order_relaxed);
-    if (cached > 0) {
-      *out = cached;
-      return GEMVTILE_OK;
-    }
-  }
-  int cus = 0;
-  if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0)
-    return GEMVTILE_ERR_DEVICE;
-  if (dev >= 0 && dev < kMaxDevices) g_cu_count[dev].store(cus, std::memory_order_relaxed);
-  *out = cus;
-  return GEMVTILE_OK;
-}
 
 int check_gemm(const void *A, const void *B, const void *D, int64_t M, int64_t N, int64_t K, bool *noop) {
   *noop = false;
@@ -80,8 +59,6 @@ int check_gemv(const void *x, const void *W, const void *y, int64_t N, int64_t K
   if (K > 0 && (misaligned(x, 16) || misaligned(W, 16))) return GEMVTILE_ERR_UNSUPPORTED;
   return GEMVTILE_OK;
 }
-
-int to_status(hipError_t e) { return e == hipSuccess ? GEMVTILE_OK : GEMVTILE_ERR_LAUNCH; }
 
 // The kernel family and index of a gemvtile_gemm_f16_variant number.
 enum class Family { kTiled, kSkinny, kWs, kInvalid };

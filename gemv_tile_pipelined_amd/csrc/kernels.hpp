@@ -378,4 +378,53 @@ int64_t grouped_ring_trace(int rows, int cols, int first, int ktu, int32_t *even
 void grouped_plan_tile(int op, int64_t T, int64_t N, int64_t K, int64_t E, int num_cus, int *rows, int *cols);
 void fp8_tile(bool grouped, int64_t M, int64_t N, int64_t E, int num_cus, int *rows, int *cols);
 
+// fp4.hip: the product of M rows with 4-bit weights, and their quantiser
+// (`elements` numbers in blocks of 32).
+hipError_t launch_gemv_fp4(int dtype, const void *x, const void *W, const void *sW, void *y, int M, int N, int K,
+                           hipStream_t stream);
+hipError_t launch_quantize_fp4(int dtype, const void *x, void *q, void *scale, int64_t elements, hipStream_t stream);
+// norm.hip.  residual and h, y, q and scale, rstd, dh may be NULL.
+struct NormArgs {
+  const void *x, *residual, *weight;
+  void *h, *y, *q;
+  float *scale, *rstd;
+  int T, C;
+  float eps;
+};
+hipError_t launch_rmsnorm(int dtype, const NormArgs &a, hipStream_t stream);
+struct NormGradArgs {
+  const void *dy, *dh, *h, *weight;
+  const float *rstd;
+  void *dx;
+  float *dweight, *workspace;
+  int T, C;
+};
+// Rows of partial sums of dweight that the gradient of T rows leaves in its
+// workspace.
+int rmsnorm_grad_parts(int64_t T);
+hipError_t launch_rmsnorm_grad(int dtype, const NormGradArgs &a, hipStream_t stream);
+// route.hip; dtype kF16, kBF16 or kF32 (logits only).
+constexpr int kF32 = 2;
+struct RouteArgs {
+  int64_t T;
+  int E, k, groups, top_groups, group_best, score, norm;
+  float scale;
+};
+hipError_t launch_route_topk(int dtype, const void *logits, const float *bias, int *ids, float *weights, const RouteArgs &r,
+                             hipStream_t stream);
+hipError_t launch_route_topk_grad(int dtype, const void *logits, const int *ids, const float *dweights, void *dlogits,
+                                  const RouteArgs &r, hipStream_t stream);
+// Workgroups of the sort of that many slots; `hist` holds as many counts of E
+// experts where there is more than one.
+int route_sort_blocks(int64_t slots);
+hipError_t launch_route_sort(const int *ids, int *offsets, int *pos, int *hist, int64_t slots, int E, hipStream_t stream);
+// rows.hip; `vecs` 16-byte pieces to a row, scale and scales NULL or per_row
+// numbers.
+hipError_t launch_route_gather(const void *X, const float *scale, const int *pos, void *Xs, float *scales, int64_t T,
+                               int64_t rows, int vecs, int per_row, int k, hipStream_t stream);
+hipError_t launch_route_combine(int dtype, const void *D, const int *pos, const float *w, void *Y, int64_t T, int64_t rows,
+                                int vecs, int k, hipStream_t stream);
+hipError_t launch_route_combine_grad(int dtype, const void *dY, const void *D, const int *pos, const float *w, void *dD,
+                                     float *dw, int64_t T, int64_t rows, int vecs, int k, hipStream_t stream);
+
 }  // namespace gt

@@ -1,6 +1,7 @@
 /*
  * gemvtile.h -- C ABI of the MI355X (gfx950) FP16 / BF16 GEMM and GEMV library,
- * with block-scaled 8-bit products and products grouped by expert.
+ * with block-scaled 8-bit products, products grouped by expert, products with
+ * 4-bit weights, and the norm and routing around them.
  *
  * Every entry point takes plain pointers and sizes; no C++ or framework type
  * crosses this boundary.  All matrices are dense and row-major.  "fp16" means
@@ -636,6 +637,200 @@ int64_t gemvtile_grouped_ring_trace(int rows, int cols, int64_t first, int64_t k
  */
 int64_t gemvtile_group_unit(const int32_t *offsets, int64_t E, int64_t T, int64_t rows, int64_t unit, int64_t *group,
                             int64_t *first, int64_t *past);
+
+/*
+ * Operators around the products: weights in 4 bits, the norm before a product,
+ * the router before the products by expert, and the rows' way there and back.
+ * All of them are asynchronous, keep nothing between calls, allocate nothing,
+ * use no atomics that decide an order (results are deterministic) and can be
+ * captured.
+ *
+ * "e2m1" is the 4-bit format with 2 exponent bits (bias 1) and 1 fraction bit:
+ * 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives.  An operand [N,K] of them is
+ * held as bytes [N,K/2], column 2i in the low half of byte i, and scale bytes
+ * [N,K/32]: byte s of 32 columns of a row stands for 2^(s - 127), 255 for NaN (the
+ * OCP microscaling format MXFP4).
+ *
+ * quantize_fp4_f16, _bf16 -- x [N,K] to such numbers q and scales:
+ *   s = the least with amax <= 6 * 2^(s - 127) (at least 0), amax the block's
+ *       largest |x|: no number is beyond the format's largest
+ *   q = the e2m1 number nearest to x / 2^(s - 127), ties to even; the sign of
+ *       zero is kept
+ * A block with an infinity or a NaN has s = 255 and q = 0.
+ *   x, q      16-byte aligned; sizes >= 0, K % 32 == 0, N * K <= 2^36 - 4096
+ * (E matrices of [N,K] are one of [E N, K].)
+ *
+ * gemv_fp4_f16, _bf16 -- a matrix-vector product with such weights for each of M
+ * rows, rounded once (nearest, ties to even):
+ *
+ *   y[m,n] = sum_b 2^(scale_W[n,b] - 127) * sum_{k in block b} x[m,k] * W[n,k]
+ *
+ * Products are exact; a block's are added in FP32, then scaled and added in FP32.
+ * Meant for decode batches: W is read once for up to 64 rows, and again for each
+ * 64 more.
+ *   x        [M,K] fp16 / bf16, 16-byte aligned
+ *   W        [N,K/2] bytes, 16-byte aligned;  scale_W  [N,K/32] bytes
+ *   y        [M,N] fp16 / bf16, 2-byte aligned
+ *   M, N, K  >= 0; M <= 2^19, N <= 2^25, K <= 4,194,272 and K % 32 == 0
+ * M == 0 or N == 0 touches nothing; K == 0 fills y with +0.
+ */
+int quantize_fp4_f16(const void *x, void *q, void *scale, int64_t N, int64_t K, void *stream);
+int quantize_fp4_bf16(const void *x, void *q, void *scale, int64_t N, int64_t K, void *stream);
+int gemv_fp4_f16(const void *x, const void *W, const void *scale_W, void *y, int64_t M, int64_t N, int64_t K,
+                 void *stream);
+int gemv_fp4_bf16(const void *x, const void *W, const void *scale_W, void *y, int64_t M, int64_t N, int64_t K,
+                  void *stream);
+
+/*
+ * rmsnorm_f16, _bf16, rmsnorm_fp8_f16, _bf16 -- root-mean-square norm of T rows of
+ * C, with the residual's addition before it:
+ *
+ *   h = x + residual, rounded once     (residual and h both NULL: h is x)
+ *   r = 1 / sqrt(sum_c h^2 / C + eps)
+ *   y = h * r * weight                 in FP32
+ *
+ * rmsnorm_* rounds y to 16 bits.  rmsnorm_fp8_* gives q [T,C] e4m3 and scale
+ * [T, ceil(C/128)] FP32 with one scale for each 128 columns of a row, as
+ * quantize_fp8_rows_* does, of y in FP32 (not rounded to 16 bits first): scale =
+ * max(amax / 448, 2^-80), q = e4m3(y / scale); y itself too if it is not NULL.
+ * What a block with an infinity or a NaN becomes is as there.
+ *   x, residual, weight [C], h, y, q  16-byte aligned; h may be x or residual
+ *            (the stream is then updated in place), other outputs overlap nothing
+ *   scale, rstd                       4-byte aligned; rstd [T] takes r for the
+ *            gradient, or NULL
+ *   T, C     >= 0; T <= 2^31 - 512, C <= 65536, C % 8 == 0 (16 for rmsnorm_fp8_*)
+ *   eps      >= 0.  The sum of squares has to be finite in FP32.
+ * T == 0 or C == 0 touches nothing.
+ *
+ * rmsnorm_grad_f16, _bf16 -- the gradients, given dy, h, weight and rstd, and dh, the
+ * gradient that reaches h elsewhere (along the residual; NULL: none):
+ *
+ *   dx[t,c]    = r weight dy - h r^3 (sum_c weight dy h) / C + dh     one rounding;
+ *                the gradient of x and of residual alike
+ *   dweight[c] = sum_t dy h r                                        FP32
+ *
+ * The rows' shares of dweight are added in FP32, in an order that T alone decides.
+ *   dy, dh, h, weight, dx  16-byte aligned; rstd, dweight 4-byte aligned; dx
+ *            overlaps nothing
+ *   workspace  gemvtile_rmsnorm_grad_workspace(T, C) bytes of device memory, owned
+ *            by the caller, 16-byte aligned; its contents do not matter.  Too small
+ *            or NULL: GEMVTILE_ERR_INVALID_ARG.  Calls that share one have to be
+ *            ordered, captured ones included
+ *   T, C     as above, C % 8 == 0.  T == 0 fills dweight with zeros.
+ */
+int rmsnorm_f16(const void *x, const void *residual, const void *weight, void *h, void *y, float *rstd, int64_t T,
+                int64_t C, float eps, void *stream);
+int rmsnorm_bf16(const void *x, const void *residual, const void *weight, void *h, void *y, float *rstd, int64_t T,
+                 int64_t C, float eps, void *stream);
+int rmsnorm_fp8_f16(const void *x, const void *residual, const void *weight, void *h, void *y, void *q, float *scale,
+                    float *rstd, int64_t T, int64_t C, float eps, void *stream);
+int rmsnorm_fp8_bf16(const void *x, const void *residual, const void *weight, void *h, void *y, void *q, float *scale,
+                     float *rstd, int64_t T, int64_t C, float eps, void *stream);
+int rmsnorm_grad_f16(const void *dy, const void *dh, const void *h, const void *weight, const float *rstd, void *dx,
+                     float *dweight, int64_t T, int64_t C, void *workspace, int64_t workspace_bytes, void *stream);
+int rmsnorm_grad_bf16(const void *dy, const void *dh, const void *h, const void *weight, const float *rstd, void *dx,
+                      float *dweight, int64_t T, int64_t C, void *workspace, int64_t workspace_bytes, void *stream);
+int64_t gemvtile_rmsnorm_grad_workspace(int64_t T, int64_t C);
+
+/* Scores of a router. */
+enum gemvtile_score {
+    GEMVTILE_SCORE_SOFTMAX = 0, /* exp(logit) / sum over the token's experts */
+    GEMVTILE_SCORE_SIGMOID = 1  /* 1 / (1 + exp(-logit)) */
+};
+
+/*
+ * route_topk_f16, _bf16, _f32 -- the k experts of each of T tokens, and their weights.
+ *
+ *   choice[e]  = score[e] + bias[e], or, with bias NULL, logit[e]
+ *   The E experts are `groups` groups of E / groups that follow one another.  A
+ *   group counts by its best choice (group_best 1) or by the sum of its two best
+ *   (2; with bias NULL the sum of its two best scores), and the top_groups best
+ *   groups are kept, ties to the lowest.
+ *   ids [T,k] int32  the k largest choices of the kept groups, largest first, ties
+ *                    to the lowest expert
+ *   weights [T,k]    FP32: scale * score[id] (no bias), divided by the sum of the k
+ *                    scores if norm is 1
+ *
+ * Ids are those of choices computed in 64 bits, whatever the logits' type.  A logit
+ * of -inf is an expert with score 0, chosen after all others; where every score
+ * that is divided by is 0 (all logits -inf) the weights are 0.  A NaN choice ranks
+ * below all others.  With softmax a NaN or +inf among a token's logits makes its
+ * weights NaN (and with a bias, or sums of two, every choice: ids are the lowest
+ * then); with a sigmoid a NaN does so where it is chosen.  Ids are always k
+ * different numbers of 0 .. E - 1.
+ *
+ *   logits   [T,E] fp16 / bf16 / FP32, 16-byte aligned
+ *   bias     [E] FP32 or NULL; ids, weights 4-byte aligned
+ *   T >= 0, T <= 2^26 - 64; 1 <= k <= 32, E <= 1024, groups <= 64 dividing E,
+ *   1 <= top_groups <= groups, k <= top_groups * E / groups
+ *
+ * route_topk_grad_f16, _bf16, _f32 -- dlogits [T,E] (16-byte aligned, the logits'
+ * type, written whole, one rounding) for dweights [T,k], with the ids held fixed as
+ * the choice among them is not differentiated.  The ids of a token are different;
+ * one outside 0 .. E - 1 is left out.
+ */
+int route_topk_f16(const void *logits, const float *bias, int32_t *ids, float *weights, int64_t T, int64_t E, int64_t k,
+                   int64_t groups, int64_t top_groups, int group_best, int score, int norm, float scale, void *stream);
+int route_topk_bf16(const void *logits, const float *bias, int32_t *ids, float *weights, int64_t T, int64_t E, int64_t k,
+                    int64_t groups, int64_t top_groups, int group_best, int score, int norm, float scale, void *stream);
+int route_topk_f32(const void *logits, const float *bias, int32_t *ids, float *weights, int64_t T, int64_t E, int64_t k,
+                   int64_t groups, int64_t top_groups, int group_best, int score, int norm, float scale, void *stream);
+int route_topk_grad_f16(const void *logits, const int32_t *ids, const float *dweights, void *dlogits, int64_t T,
+                        int64_t E, int64_t k, int score, int norm, float scale, void *stream);
+int route_topk_grad_bf16(const void *logits, const int32_t *ids, const float *dweights, void *dlogits, int64_t T,
+                         int64_t E, int64_t k, int score, int norm, float scale, void *stream);
+int route_topk_grad_f32(const void *logits, const int32_t *ids, const float *dweights, void *dlogits, int64_t T,
+                        int64_t E, int64_t k, int score, int norm, float scale, void *stream);
+
+/*
+ * route_sort -- the T * k slots (t, j) sorted by expert, those of an expert in their
+ * order: offsets [E+1] int32 as gemm_grouped_* take them (expert e has rows
+ * offsets[e] .. offsets[e+1] - 1), and pos [T,k] int32, the row of each slot.  A slot
+ * whose id is outside 0 .. E - 1 has no row (pos -1; so a card that holds some of the
+ * experts sorts the slots of those).
+ *   ids, offsets, pos  4-byte aligned, not overlapping
+ *   workspace  gemvtile_route_sort_workspace(T, k, E) bytes (0 for up to 4096 slots;
+ *            it may then be NULL), 16-byte aligned, owned by the caller; as for
+ *            rmsnorm_grad_*
+ *   T >= 0, k >= 1, 1 <= E <= 1024, T * k <= 2^31 - 512.  T == 0: offsets are zeros.
+ */
+int route_sort(const int32_t *ids, int32_t *offsets, int32_t *pos, int64_t T, int64_t k, int64_t E, void *workspace,
+               int64_t workspace_bytes, void *stream);
+int64_t gemvtile_route_sort_workspace(int64_t T, int64_t k, int64_t E);
+
+/*
+ * The rows of T tokens and the R rows sorted by expert.  pos [T,k] is the row of each
+ * slot; a slot whose pos is outside 0 .. R - 1 is left out, and no row may stand in
+ * pos twice (what is written there is then one of the two).  Rows that no slot has
+ * stay as they were.
+ *
+ * route_gather_f16, _bf16, _fp8        Xs[pos[t,j]] = X[t]; _fp8 moves e4m3 rows with
+ *                                      their scales [.., ceil(K/128)]
+ * route_combine_f16, _bf16             Y[t] = sum_j weights[t,j] * D[pos[t,j]]
+ *                                      (weights NULL: ones, the gradient of a gather)
+ * route_combine_grad_f16, _bf16        dD[pos[t,j]] = weights[t,j] * dY[t]
+ *                                      dweights[t,j] = sum_c dY[t,c] * D[pos[t,j],c]
+ *                                      (0 for a slot that is left out)
+ *
+ * Sums in FP32, one rounding of each 16-bit output.
+ *   X, Y, dY [T,K]; Xs, D, dD [R,K]  16-byte aligned; pos, scales and weights 4-byte
+ *   T < 2^24, 1 <= k <= 32, R <= 2^31 - 512, K <= 2^20, K % 8 == 0 (16 for _fp8)
+ * T == 0 or K == 0 touches nothing, but for dweights, which are then zeros where T > 0.
+ */
+int route_gather_f16(const void *X, const int32_t *pos, void *Xs, int64_t T, int64_t k, int64_t R, int64_t K,
+                     void *stream);
+int route_gather_bf16(const void *X, const int32_t *pos, void *Xs, int64_t T, int64_t k, int64_t R, int64_t K,
+                      void *stream);
+int route_gather_fp8(const void *X, const float *scale, const int32_t *pos, void *Xs, float *scales, int64_t T, int64_t k,
+                     int64_t R, int64_t K, void *stream);
+int route_combine_f16(const void *D, const int32_t *pos, const float *weights, void *Y, int64_t T, int64_t k, int64_t R,
+                      int64_t K, void *stream);
+int route_combine_bf16(const void *D, const int32_t *pos, const float *weights, void *Y, int64_t T, int64_t k, int64_t R,
+                       int64_t K, void *stream);
+int route_combine_grad_f16(const void *dY, const void *D, const int32_t *pos, const float *weights, void *dD,
+                           float *dweights, int64_t T, int64_t k, int64_t R, int64_t K, void *stream);
+int route_combine_grad_bf16(const void *dY, const void *D, const int32_t *pos, const float *weights, void *dD,
+                            float *dweights, int64_t T, int64_t k, int64_t R, int64_t K, void *stream);
 
 /*
  * gemvtile_xcd_logical_id -- the logical workgroup id the persistent GEMM
