@@ -9,17 +9,25 @@
 //   y[m,n] = sum_b 2^(s[n,b] - 127) * sum_{k in block b} x[m,k] * W[n,k]
 //
 // The product reads 17 bytes of W for 32 numbers, each once, and is bound by
-// that.  One v_cvt_scalef32_pk_*_fp4 turns a byte into two numbers of x's
-// format, which holds every e2m1 number, so a product of 16-bit MFMAs
-// (16x16x32) adds exact products in FP32; a block's sum is then scaled in FP32,
-// which is exact but for results below FP32's normal numbers.  (Scaled in the
-// conversion instead, half precision would overflow or lose bits of small
-// blocks.)
+// that.  One v_cvt_scalef32_pk_*_fp4 turns a byte into two numbers of x's format
+// times the scale, and 16-bit MFMAs (16x16x32) multiply exactly and add in FP32.
+// Lane n + 16 g of a wave holds the whole block g of four that follow one another
+// in row n, and as many of x: an MFMA takes 8 numbers of each of the four blocks.
 //
-// Lane n + 16 g of a wave loads 16 bytes of row n: the whole block g of four
-// blocks that follow one another.  An MFMA wants all four lane rows to hold 8
-// numbers each of one block, which is the transpose of 4 x 4 dwords across lane
-// rows: two v_permlane32_swap and two v_permlane16_swap.
+// That is exact where scaled numbers are numbers of the 16-bit format: scales of
+// 2^-125 to 2^125 in bf16, 2^-23 to 2^13 in half precision, which weights have.
+// Four blocks with another scale among them (blocks of zeros have the smallest),
+// and those at a ragged end of K, take the exact way for any scale: numbers
+// converted without it, one MFMA for each block, whose sum is then scaled in FP32.
+// That wants all four lane rows to hold 8 numbers each of one block, which is the
+// transpose of 4 x 4 dwords across lane rows (two v_permlane32_swap and two
+// v_permlane16_swap), of W and of x.
+//
+// Loads go straight to LDS.  A wave's 64 x 16 bytes are 16 rows of 64 bytes: where
+// neighbouring lanes load from the rows of an MFMA's operand, 16 different cache
+// lines each, a CU gets 10 bytes a cycle (1x4096x14336 11.3 us however deep the
+// prefetch); with neighbouring lanes along the rows it is what memory gives.  LDS
+// hands them to the lanes that multiply.
 #include "device_common.hpp"
 #include "kernels.hpp"
 #include "wave_ops.hpp"
@@ -33,32 +41,38 @@ typedef unsigned short ushort2_v __attribute__((ext_vector_type(2)));
 constexpr int kFp4Block = 32;   // numbers that share a scale; also the K of one MFMA
 constexpr int kFp4Chunk = 128;  // columns that a wave takes at a time
 
-// The 8 numbers of a dword in x's format.
+// The 8 numbers of a dword times a scale (a power of two) in x's format.
 template <int DT>
-__device__ inline half8_t widen_fp4(uint32_t v) {
+__device__ inline half8_t widen_fp4(uint32_t v, float scale) {
   half8_t w;
   if constexpr (DT == kF16) {
-    const half2_t a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(v, 1.0f, 0);
-    const half2_t b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(v, 1.0f, 1);
-    const half2_t c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(v, 1.0f, 2);
-    const half2_t d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(v, 1.0f, 3);
+    const half2_t a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(v, scale, 0);
+    const half2_t b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(v, scale, 1);
+    const half2_t c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(v, scale, 2);
+    const half2_t d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(v, scale, 3);
     w = half8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
   } else {
-    const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, 1.0f, 0);
-    const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, 1.0f, 1);
-    const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, 1.0f, 2);
-    const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, 1.0f, 3);
+    const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, scale, 0);
+    const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, scale, 1);
+    const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, scale, 2);
+    const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, scale, 3);
     w = __builtin_bit_cast(half8_t, bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]});
   }
   return w;
 }
 
+// Scale bytes with which every scaled number is one of the 16-bit format.
 template <int DT>
-__device__ inline float4_t mfma_16x16x32(half8_t a, half8_t b) {
-  const float4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
-  if constexpr (DT == kF16) return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, zero, 0, 0, 0);
+__device__ inline bool scale_fits(uint32_t s) {
+  constexpr uint32_t kLow = DT == kF16 ? 127 - 23 : 127 - 125, kHigh = DT == kF16 ? 127 + 13 : 127 + 125;
+  return s - kLow <= kHigh - kLow;
+}
+
+template <int DT>
+__device__ inline float4_t mfma_16x16x32(half8_t a, half8_t b, float4_t c) {
+  if constexpr (DT == kF16) return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
   else
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), zero, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
 }
 
 // 4 x 4 dwords across the four lane rows: v[i] of lane row g <-> v[g] of row i.
@@ -70,144 +84,206 @@ __device__ inline uint4_v transpose_rows(uint4_v v) {
   return uint4_v{c[0], c[1], d[0], d[1]};
 }
 
-// 2^(s - 127) of byte i: the byte as an FP32 exponent, but for 0 (2^-127, below
-// the normal numbers) and 255 (NaN).
-__device__ inline float scale_of(uint32_t bytes, int i) {
-  const uint32_t s = (bytes >> (8 * i)) & 0xffu;
+// 2^(s - 127): the byte as an FP32 exponent, but for 0 (2^-127, below the normal
+// numbers) and 255 (NaN).
+__device__ inline float scale_of(uint32_t s) {
   const uint32_t bits = s << 23;
   const float f = __builtin_bit_cast(float, bits > 0x00400000u ? bits : 0x00400000u);
   return s == 0xffu ? __builtin_nanf("") : f;
 }
 
-// A workgroup has NT * 16 rows of W and up to MT * 16 rows of x; its waves take
-// the chunks of K in turn and their sums meet in LDS, added in wave order.
-// FULL: all 16 rows of each block of x, four sums to a lane; otherwise one row,
-// which only the first register of each sum holds.
-template <int DT, int MT, int NT, int WAVES, int DEPTH, bool FULL>
+// What lane row i holds, in every lane row, for i = 0 .. 3.
+__device__ inline float4_t spread_rows(float v) {
+  const int lane = threadIdx.x & 15;
+  return float4_t{__shfl(v, lane), __shfl(v, lane + 16), __shfl(v, lane + 32), __shfl(v, lane + 48)};
+}
+
+// A workgroup has NT * 16 rows of W and up to XQ * 4 rows of x.  Its waves take
+// the chunks of K in turn; each has a ring of its own in LDS, DEPTH chunks of W and
+// x on their way, and waits for its own loads only.  Loads outside the matrices
+// (rows past the last, the end of a ragged K, chunks past the last) go to an offset
+// that buffer loads answer with zeros, so the number in flight is always the same.
+// The scales of the workgroup's rows are in LDS too, 16384 columns at a time.  The
+// waves' sums meet in LDS and are added in wave order.
+//
+// Places in LDS, in 16-byte pieces.  W: piece g of row n at 4 n + (g ^ (n >> 2)), so
+// that the 16 rows' pieces g are spread over all banks.  x: piece p (of 16) of row m
+// at 16 m + (p ^ (m & 15)), likewise.
+constexpr int kSegmentChunks = 128;
+template <int DT, int XQ, int NT, int WAVES, int DEPTH>
 __global__ void __launch_bounds__(WAVES * 64)
 gemv_fp4_kernel(const uint16_t *__restrict__ x, const uint8_t *__restrict__ W, const uint8_t *__restrict__ sW,
                 uint16_t *__restrict__ y, int M, int N, int K) {
-  constexpr int R = FULL ? 4 : 1;
+  constexpr int MT = (XQ + 3) / 4;               // blocks of 16 rows of x
+  constexpr int kChains = NT * MT == 1 ? 2 : 1;  // of MFMAs that wait for one another
+  constexpr int kSums = NT * MT * 256;
+  constexpr int kLoads = NT + XQ;  // of a chunk, 1 KiB each
+  constexpr int kScaleBytes = NT * 16 * kSegmentChunks * 4;
+  static_assert(kSums * 4 <= DEPTH * kLoads * 1024, "the sums fit where the ring was");
+  __shared__ __attribute__((aligned(16))) char ring[WAVES * DEPTH * kLoads * 1024];
+  __shared__ __attribute__((aligned(16))) uint8_t scales[kScaleBytes];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, i16 = lane & 15;
   const int n0 = static_cast<int>(blockIdx.x) * (NT * 16);
-  const int m0 = static_cast<int>(blockIdx.y) * (MT * 16);
-  // Rows past the last read the last one again; what they give is not stored.
-  const uint16_t *xrow[MT];
+  const int m0 = static_cast<int>(blockIdx.y) * (XQ * 4);
+  const int rows = N - n0 < NT * 16 ? N - n0 : NT * 16;
+  const int xrows = M - m0 < XQ * 4 ? M - m0 : XQ * 4;
+  // Below 2^31 bytes by the limits of the entry point.
+  const int4_t wbuf = make_buffer_rsrc(W + static_cast<int64_t>(n0) * (K / 2), static_cast<uint32_t>(rows) * (K / 2));
+  const int4_t xbuf = make_buffer_rsrc(x + static_cast<int64_t>(m0) * K, static_cast<uint32_t>(xrows) * K * 2);
+  char *const mine = ring + wave * (DEPTH * kLoads * 1024);
+  const uint32_t mine_lds = __builtin_amdgcn_readfirstlane(lds_addr(mine));
+
+  // This lane's piece of each load: of W's row lane / 4, and of x's row lane / 16.
+  const uint32_t wpiece = (lane & 3) ^ (lane >> 4);
+  const uint32_t wat = static_cast<uint32_t>(lane >> 2) * (K / 2) + wpiece * 16;
+  const uint32_t wcol = wpiece * kFp4Block;
+  auto issue = [&](int chunk, int stage) {
+    const int k = chunk * kFp4Chunk;
+    const uint32_t to = mine_lds + stage * (kLoads * 1024);
 #pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    int m = m0 + t * 16 + i16;
-    if (m >= M) m = M - 1;
-    xrow[t] = x + static_cast<int64_t>(m) * K + g * 8;
-  }
-  const uint8_t *wrow[NT], *srow[NT];
+    for (int t = 0; t < NT; ++t)
+      lds_dma_b128(wbuf, k + wcol < static_cast<uint32_t>(K) ? wat + t * 16 * (K / 2) + k / 2 : kOobOffset, to + t * 1024);
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    int n = n0 + t * 16 + i16;
-    if (n >= N) n = N - 1;
-    wrow[t] = W + static_cast<int64_t>(n) * (K / 2);
-    srow[t] = sW + static_cast<int64_t>(n) * (K / kFp4Block);
-  }
-  float acc[NT][MT][R];
+    for (int q = 0; q < XQ; ++q) {
+      const uint32_t m = q * 4 + g;
+      const uint32_t col = k + (i16 ^ (m & 15)) * 8;
+      lds_dma_b128(xbuf, col < static_cast<uint32_t>(K) ? (m * K + col) * 2 : kOobOffset, to + (NT + q) * 1024);
+    }
+  };
+
+  float4_t acc[NT][MT][kChains];
 #pragma unroll
   for (int a = 0; a < NT; ++a)
 #pragma unroll
     for (int b = 0; b < MT; ++b)
 #pragma unroll
-      for (int r = 0; r < R; ++r) acc[a][b][r] = 0.0f;
+      for (int r = 0; r < kChains; ++r) acc[a][b][r] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-  struct Chunk {
-    uint4_v w[NT];
-    uint32_t s[NT];
-    half8_t x[MT][4];
+  // Where this lane reads: W's piece g of row i16, x's pieces of row i16 (of one
+  // that is there where a block has fewer: what it gives is not stored).
+  const uint32_t wread = (4 * i16 + (g ^ (i16 >> 2))) * 16;
+  const uint32_t xrow = XQ >= 4 ? i16 : i16 & (XQ * 4 - 1);
+  auto read = [&](const char *stage, uint4_v (&w)[NT], uint4_v (&xv)[MT][4]) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) w[t] = *reinterpret_cast<const uint4_v *>(stage + t * 1024 + wread);
+#pragma unroll
+    for (int u = 0; u < MT; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        xv[u][i] = *reinterpret_cast<const uint4_v *>(stage + NT * 1024 + (u * 256 + xrow * 16 + ((4 * g + i) ^ xrow)) * 16);
   };
-  auto load = [&](Chunk &c, int chunk) {
-    const int64_t k = static_cast<int64_t>(chunk) * kFp4Chunk;
+  auto multiply = [&](const uint4_v (&w)[NT], const uint4_v (&xv)[MT][4], const uint32_t (&s)[NT]) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      c.w[t] = *reinterpret_cast<const uint4_v *>(wrow[t] + k / 2 + g * 16);
-      __builtin_memcpy(&c.s[t], srow[t] + k / kFp4Block, 4);
-    }
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) c.x[t][i] = *reinterpret_cast<const half8_t *>(xrow[t] + k + i * kFp4Block);
-  };
-  auto multiply = [&](const Chunk &c, int blocks) {
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const uint4_v w = transpose_rows(c.w[t]);
+      const float scale = __builtin_bit_cast(float, s[t] << 23);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (i < blocks) {
-          const half8_t b = widen_fp4<DT>(w[i]);
-          const float s = scale_of(c.s[t], i);
+        const half8_t b = widen_fp4<DT>(w[t][i], scale);
 #pragma unroll
-          for (int u = 0; u < MT; ++u) {
-            const float4_t part = mfma_16x16x32<DT>(c.x[u][i], b);
+        for (int u = 0; u < MT; ++u)
+          acc[t][u][i % kChains] = mfma_16x16x32<DT>(__builtin_bit_cast(half8_t, xv[u][i]), b, acc[t][u][i % kChains]);
+      }
+    }
+  };
+  auto multiply_exactly = [&](const uint4_v (&wv)[NT], const uint4_v (&xv)[MT][4], const uint32_t (&sv)[NT]) {
+    uint4_v xt[MT][4];
 #pragma unroll
-            for (int r = 0; r < R; ++r) acc[t][u][r] = __builtin_fmaf(part[r], s, acc[t][u][r]);
-          }
+    for (int u = 0; u < MT; ++u)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint4_v v = transpose_rows(uint4_v{xv[u][0][j], xv[u][1][j], xv[u][2][j], xv[u][3][j]});
+#pragma unroll
+        for (int i = 0; i < 4; ++i) xt[u][i][j] = v[i];
+      }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const uint4_v w = transpose_rows(wv[t]);
+      const float4_t s = spread_rows(scale_of(sv[t]));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const half8_t b = widen_fp4<DT>(w[i], 1.0f);
+#pragma unroll
+        for (int u = 0; u < MT; ++u) {
+          const float4_t part =
+              mfma_16x16x32<DT>(__builtin_bit_cast(half8_t, xt[u][i]), b, float4_t{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[t][u][0][r] = __builtin_fmaf(part[r], s[i], acc[t][u][0][r]);
         }
       }
     }
   };
 
-  const int whole = K / kFp4Chunk;
-  int chunk = wave;
-  for (; chunk + (DEPTH - 1) * WAVES < whole; chunk += DEPTH * WAVES) {
-    Chunk c[DEPTH];
+  const int chunks = (K + kFp4Chunk - 1) / kFp4Chunk, row_blocks = K / kFp4Block;
 #pragma unroll
-    for (int d = 0; d < DEPTH; ++d) load(c[d], chunk + d * WAVES);
-#pragma unroll
-    for (int d = 0; d < DEPTH; ++d) multiply(c[d], 4);
-  }
-  for (; chunk < whole; chunk += WAVES) {
-    Chunk c;
-    load(c, chunk);
-    multiply(c, 4);
-  }
-  // The blocks behind the last whole chunk, by the wave whose turn it is.
-  const int rest = K / kFp4Block - whole * 4;
-  if (rest > 0 && chunk == whole) {
-    Chunk c;
-    const int64_t k = static_cast<int64_t>(whole) * kFp4Chunk;
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      c.w[t] = uint4_v{0, 0, 0, 0};
-      c.s[t] = 0;
-      if (g < rest) c.w[t] = *reinterpret_cast<const uint4_v *>(wrow[t] + k / 2 + g * 16);
-      for (int i = 0; i < rest; ++i) c.s[t] |= static_cast<uint32_t>(srow[t][whole * 4 + i]) << (8 * i);
+  for (int d = 0; d < DEPTH; ++d) issue(wave + d * WAVES, d);
+  int chunk = wave, stage = 0;
+  for (int first = 0; first < chunks; first += kSegmentChunks) {
+    // The scales of the segment: the workgroup's rows one after another.
+    const int b0 = first * 4, nb = row_blocks - b0 < kSegmentChunks * 4 ? row_blocks - b0 : kSegmentChunks * 4;
+    const uint8_t *src = sW + static_cast<int64_t>(n0) * row_blocks + b0;
+    if (first > 0) __syncthreads();
+    const int bytes = rows * nb;
+    if (nb == row_blocks && (reinterpret_cast<uintptr_t>(src) & 15) == 0) {
+      // all of K: the rows' scales follow one another in memory too
+      for (int i = threadIdx.x * 16; i < bytes; i += WAVES * 64 * 16) {
+        if (i + 16 <= bytes) {
+          *reinterpret_cast<uint4_v *>(scales + i) = *reinterpret_cast<const uint4_v *>(src + i);
+        } else {
+          for (int j = i; j < bytes; ++j) scales[j] = src[j];
+        }
+      }
+    } else {
+      for (int i = threadIdx.x; i < bytes; i += WAVES * 64) {
+        const int r = i / nb;
+        scales[i] = src[static_cast<int64_t>(r) * row_blocks + (i - r * nb)];
+      }
     }
+    __syncthreads();
+    const int past = first + kSegmentChunks < chunks ? first + kSegmentChunks : chunks;
+    for (; chunk < past; chunk += WAVES) {
+      // Lanes behind the last row or the end of K: zeros of W, any scale but NaN.
+      const int block = chunk * 4 + g;
+      bool fits = (chunk + 1) * kFp4Chunk <= K;
+      uint32_t s[NT];
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        c.x[t][i] = i < rest ? *reinterpret_cast<const half8_t *>(xrow[t] + k + i * kFp4Block) : half8_t{};
-    multiply(c, rest);
+      for (int t = 0; t < NT; ++t) {
+        const int r = t * 16 + i16;
+        s[t] = r < rows && block < row_blocks ? scales[r * nb + block - b0] : 127u;
+        fits &= scale_fits<DT>(s[t]);
+      }
+      wait_vmcnt<(DEPTH - 1) * kLoads>();
+      uint4_v w[NT], xv[MT][4];
+      read(mine + stage * (kLoads * 1024), w, xv);
+      if (__all(fits)) multiply(w, xv, s);
+      else multiply_exactly(w, xv, s);
+      wait_lgkmcnt0();  // this stage has been read
+      issue(chunk + DEPTH * WAVES, stage);
+      stage = stage + 1 == DEPTH ? 0 : stage + 1;
+    }
   }
-
-  // One row of x: its sums are in the first register of lanes 0 .. 15.
-  constexpr int kLanes = FULL ? 64 : 16;
-  constexpr int kSums = NT * MT * R * kLanes;
-  __shared__ float part[WAVES][kSums];
-  if (lane < kLanes) {
+  wait_vmcnt<0>();  // loads past the last chunk, before their places are written
+  __syncthreads();
+  float(*part)[kSums] = reinterpret_cast<float(*)[kSums]>(ring);
 #pragma unroll
-    for (int a = 0; a < NT; ++a)
+  for (int a = 0; a < NT; ++a)
 #pragma unroll
-      for (int b = 0; b < MT; ++b)
+    for (int b = 0; b < MT; ++b) {
+      float4_t sum = acc[a][b][0];
+      if constexpr (kChains == 2) sum += acc[a][b][1];
 #pragma unroll
-        for (int r = 0; r < R; ++r) part[wave][((a * MT + b) * R + r) * kLanes + lane] = acc[a][b][r];
-  }
+      for (int r = 0; r < 4; ++r) part[wave][((a * MT + b) * 4 + r) * 64 + lane] = sum[r];
+    }
   __syncthreads();
   for (int i = threadIdx.x; i < kSums; i += WAVES * 64) {
+    const int l = i % 64, r = i / 64 % 4, b = i / 256 % MT, a = i / (256 * MT);
+    const int m = m0 + b * 16 + (l >> 4) * 4 + r, n = n0 + a * 16 + (l & 15);
+    if (m >= m0 + xrows || n >= N) continue;
     float sum = part[0][i];
 #pragma unroll
     for (int w = 1; w < WAVES; ++w) sum += part[w][i];
-    const int l = i % kLanes, r = i / kLanes % R, b = i / (kLanes * R) % MT, a = i / (kLanes * R * MT);
-    const int m = m0 + b * 16 + (l >> 4) * 4 + r, n = n0 + a * 16 + (l & 15);
-    if (m < M && n < N) y[static_cast<int64_t>(m) * N + n] = __builtin_bit_cast(uint16_t, round_out<DT>(sum));
+    y[static_cast<int64_t>(m) * N + n] = __builtin_bit_cast(uint16_t, round_out<DT>(sum));
   }
 }
 
@@ -265,29 +341,60 @@ quantize_fp4_kernel(const uint16_t *__restrict__ x, uint8_t *__restrict__ q, uin
   if ((threadIdx.x & 1) == 0) scale[half >> 1] = static_cast<uint8_t>(s);
 }
 
-template <int DT, int MT, int NT, int WAVES, int DEPTH, bool FULL>
+template <int DT, int XQ, int NT, int WAVES, int DEPTH>
 hipError_t launch_gemv(const void *x, const void *W, const void *sW, void *y, int M, int N, int K, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>((N + NT * 16 - 1) / (NT * 16)), static_cast<unsigned>((M + MT * 16 - 1) / (MT * 16)));
-  hipLaunchKernelGGL((gemv_fp4_kernel<DT, MT, NT, WAVES, DEPTH, FULL>), grid, dim3(WAVES * 64), 0, stream,
+  const dim3 grid(static_cast<unsigned>((N + NT * 16 - 1) / (NT * 16)), static_cast<unsigned>((M + XQ * 4 - 1) / (XQ * 4)));
+  hipLaunchKernelGGL((gemv_fp4_kernel<DT, XQ, NT, WAVES, DEPTH>), grid, dim3(WAVES * 64), 0, stream,
                      static_cast<const uint16_t *>(x), static_cast<const uint8_t *>(W), static_cast<const uint8_t *>(sW),
                      static_cast<uint16_t *>(y), M, N, K);
   return hipGetLastError();
 }
 
+// Rows of W for a workgroup: 16 as long as that leaves compute units idle or gives
+// each only one or two workgroups, more beyond, as every workgroup reads all of x
+// (figures: us, 16 / 32 / 64 rows).
+//   up to 4 rows of x   4096x14336 8.3 / 11.4, 8192x4096 5.9 / 6.0, 14336x4096 10.3 / 8.4, 28672x8192 28.7 / 27.1
+//   up to 16            4096x4096 5.3 / 5.8 / 7.5, 8192x8192 15.0 / 12.8 / 15.8, 28672x4096 28.3 / 20.7 / 19.4
+//   up to 32            4096x14336 20.4 / 23.4 / 32.6, 8195x4128 16.2 / 11.8 / 11.2, 28672x4096 46.3 / 31.8 / 24.7
+//   up to 64            4096x4096 10.6 / 13.0 / 19.1, 8192x8192 35.6 / 26.0 / 35.7, 28672x4096 70.6 / 55.3 / 41.6
+// The ring is as deep as the LDS holds with one or two workgroups to a CU; with few
+// rows of x two stages do unless a wave has more than four chunks (4096x14336 9.5 us
+// with two, 8.3 with three; 4096x4096 4.2 and 4.5).
 template <int DT>
-hipError_t launch_gemv_dt(const void *x, const void *W, const void *sW, void *y, int M, int N, int K, hipStream_t stream) {
-  if (M == 1) return launch_gemv<DT, 1, 1, 8, 2, false>(x, W, sW, y, M, N, K, stream);
-  if (M <= 16) return launch_gemv<DT, 1, 1, 8, 2, true>(x, W, sW, y, M, N, K, stream);
-  if (M <= 32) return launch_gemv<DT, 2, 1, 8, 2, true>(x, W, sW, y, M, N, K, stream);
-  return launch_gemv<DT, 4, 1, 8, 1, true>(x, W, sW, y, M, N, K, stream);
+hipError_t launch_gemv_dt(const void *x, const void *W, const void *sW, void *y, int M, int N, int K, int cus,
+                          hipStream_t stream) {
+  const int tiles = (N + 15) / 16;
+  const bool deep = K > 4 * 8 * kFp4Chunk;
+  if (M <= 8) {
+    if (M <= 4) {
+      if (tiles > 2 * cus) return launch_gemv<DT, 1, 2, 8, 2>(x, W, sW, y, M, N, K, stream);
+      if (deep) return launch_gemv<DT, 1, 1, 8, 3>(x, W, sW, y, M, N, K, stream);
+      return launch_gemv<DT, 1, 1, 8, 2>(x, W, sW, y, M, N, K, stream);
+    }
+    if (tiles > 2 * cus) return launch_gemv<DT, 2, 2, 8, 2>(x, W, sW, y, M, N, K, stream);
+    return launch_gemv<DT, 2, 1, 8, 2>(x, W, sW, y, M, N, K, stream);
+  }
+  if (M <= 16) {
+    if (tiles <= cus) return launch_gemv<DT, 4, 1, 8, 2>(x, W, sW, y, M, N, K, stream);
+    if (tiles < 4 * cus) return launch_gemv<DT, 4, 2, 8, 1>(x, W, sW, y, M, N, K, stream);
+    return launch_gemv<DT, 4, 4, 8, 1>(x, W, sW, y, M, N, K, stream);
+  }
+  if (M <= 32) {
+    if (tiles <= cus) return launch_gemv<DT, 8, 1, 8, 1>(x, W, sW, y, M, N, K, stream);
+    if (tiles < 2 * cus) return launch_gemv<DT, 8, 2, 4, 1>(x, W, sW, y, M, N, K, stream);
+    return launch_gemv<DT, 8, 4, 8, 1>(x, W, sW, y, M, N, K, stream);
+  }
+  if (tiles <= cus) return launch_gemv<DT, 16, 1, 8, 1>(x, W, sW, y, M, N, K, stream);
+  if (tiles < 4 * cus) return launch_gemv<DT, 16, 2, 4, 1>(x, W, sW, y, M, N, K, stream);
+  return launch_gemv<DT, 16, 4, 4, 1>(x, W, sW, y, M, N, K, stream);
 }
 
 }  // namespace
 
-hipError_t launch_gemv_fp4(int dtype, const void *x, const void *W, const void *sW, void *y, int M, int N, int K,
+hipError_t launch_gemv_fp4(int dtype, const void *x, const void *W, const void *sW, void *y, int M, int N, int K, int num_cus,
                            hipStream_t stream) {
-  return dtype == kBF16 ? launch_gemv_dt<kBF16>(x, W, sW, y, M, N, K, stream)
-                        : launch_gemv_dt<kF16>(x, W, sW, y, M, N, K, stream);
+  return dtype == kBF16 ? launch_gemv_dt<kBF16>(x, W, sW, y, M, N, K, num_cus, stream)
+                        : launch_gemv_dt<kF16>(x, W, sW, y, M, N, K, num_cus, stream);
 }
 
 hipError_t launch_quantize_fp4(int dtype, const void *x, void *q, void *scale, int64_t elements, hipStream_t stream) {

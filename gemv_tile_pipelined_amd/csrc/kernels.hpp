@@ -381,7 +381,7 @@ void fp8_tile(bool grouped, int64_t M, int64_t N, int64_t E, int num_cus, int *r
 // fp4.hip: the product of M rows with 4-bit weights, and their quantiser
 // (`elements` numbers in blocks of 32).
 hipError_t launch_gemv_fp4(int dtype, const void *x, const void *W, const void *sW, void *y, int M, int N, int K,
-                           hipStream_t stream);
+                           int num_cus, hipStream_t stream);
 hipError_t launch_quantize_fp4(int dtype, const void *x, void *q, void *scale, int64_t elements, hipStream_t stream);
 // norm.hip.  residual and h, y, q and scale, rstd, dh may be NULL.
 struct NormArgs {

@@ -38,7 +38,11 @@ int run_gemv_fp4(int dtype, const void *x, const void *W, const void *sW, void *
   if (misaligned(y, 2) || (K > 0 && (misaligned(x, 16) || misaligned(W, 16)))) return GEMVTILE_ERR_UNSUPPORTED;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (K == 0) return to_status(gt::launch_fill_zero_f16(y, M * N, s));
-  return to_status(gt::launch_gemv_fp4(dtype, x, W, sW, y, static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), s));
+  int cus = 0;
+  const int st = gt::current_cu_count(&cus);
+  if (st != GEMVTILE_OK) return st;
+  return to_status(
+      gt::launch_gemv_fp4(dtype, x, W, sW, y, static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), cus, s));
 }
 
 // fp8: q and scale wanted, y optional; otherwise y wanted.

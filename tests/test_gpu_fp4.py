@@ -84,7 +84,10 @@ def _weights(r, N, K, low=110, high=130):
 
 SHAPES = [(1, 1, 32), (1, 16, 128), (1, 17, 160), (2, 15, 64), (3, 33, 96), (4, 300, 1024), (5, 40, 4128), (15, 31, 224), (16, 100, 512),
           (17, 47, 2080), (27, 515, 1056), (32, 64, 256), (33, 65, 1056), (48, 70, 320), (64, 130, 2080), (65, 50, 256), (200, 33, 160),
-          (1, 1000, 14336), (1, 5000, 96), (1, 9000, 544), (7, 8200, 288), (40, 4200, 160)]
+          (1, 1000, 14336), (1, 5000, 96), (1, 9000, 544), (7, 8200, 288), (40, 4200, 160),
+          # each number of rows of a workgroup, and scales past one segment of 16384 columns
+          (12, 4100, 160), (16, 16400, 96), (20, 4128, 224), (32, 8208, 64), (64, 16390, 96), (2, 20, 16416), (1, 35, 33024),
+          (13, 33, 20000), (70, 18, 16512)]
 
 
 @FMT
@@ -101,6 +104,33 @@ def test_gemv(env, M, N, K, fmt):
     if M == 1:
         one = env.call("gemv_fp4", fmt)(x[0], env.whole(q), env.whole(s))
         assert one.shape == (N,) and env.torch.equal(one, got[0])
+
+
+@pytest.mark.parametrize("K", [96, 160, 16416])
+def test_gemv_of_one_of_several_matrices(env, K):
+    """Weights and scales of one expert: scales that begin at any byte."""
+    r = np.random.default_rng(K)
+    q, s = _weights(r, 3 * 5, K)
+    x = env.device(r.standard_normal((2, K)), "bf16")
+    tq, ts = env.whole(q).reshape(3, 5, -1), env.whole(s).reshape(3, 5, -1)
+    for e in range(3):
+        want, tol = ref.gemv_fp4(host(x), q[5 * e : 5 * e + 5], s[5 * e : 5 * e + 5], "bf16")
+        near(host(env.gt.gemv_fp4_bf16(x, tq[e], ts[e])), want, tol)
+
+
+@FMT
+def test_gemv_mixed_scales(env, fmt):
+    """Chunks in which a few blocks have scales that 16-bit numbers do not hold, among others, for every block of rows."""
+    r = np.random.default_rng(8)
+    for M, N, K in ((1, 40, 1056), (6, 33, 640), (14, 50, 1024), (30, 40, 512), (64, 48, 384), (50, 300, 256)):
+        q, s = _weights(r, N, K, 118, 124)
+        s[r.random(s.shape) < 0.05] = 20
+        s[r.random(s.shape) < 0.02] = 0
+        if fmt == "bf16":
+            s[r.random(s.shape) < 0.002] = 230
+        x = env.device(r.standard_normal((M, K)), fmt)
+        want, tol = ref.gemv_fp4(host(x), q, s, fmt)
+        near(host(env.call("gemv_fp4", fmt)(x, env.whole(q), env.whole(s))), want, tol)
 
 
 @FMT
