@@ -8,17 +8,20 @@
 //   ids       = the k largest choices in kept groups, largest first, ties to the lowest index
 //   weights   = scale * score[id], over their sum if they are normalised
 //
-// One wave has one token, its lanes V experts each that follow one another (V a
-// power of two).  A choice becomes an unsigned key that orders as the numbers do
-// (NaN below all of them), so that one of the k rounds is a maximum over the lane's
-// keys, a maximum over the wave through DPP, and a ballot: the lowest lane that
-// has the maximum has the lowest index.
+// 16 lanes have one token (64 lanes where there are more than 256 experts or 14
+// choices), each V experts that follow one another.  An expert's key is its choice,
+// rounded down to 31 bits less those of its number, and the number, inverted: keys
+// are all different and tied choices are in order.  A round of the choice is then
+// the largest key below the last one, one subtraction and half a maximum an expert
+// and a maximum over the lanes through DPP; nothing is marked as taken, and the
+// key says whose it is.
 //
-// Ids are those of exact arithmetic.  Logits are compared as they are; where
-// scores matter (a bias, or sums of two) they are computed in FP32 and every
-// decision (each choice against the next, the last kept group against the first
-// dropped) is checked against the error that these can have; a token with a
-// closer decision, few in ten thousand of random ones, is done again in FP64.
+// Ids are those of exact arithmetic.  16-bit logits fit a key as they are.  Scores,
+// and logits of 32 bits, are rounded; each decision (a choice against the next, the
+// last kept group against the first dropped) is checked afterwards against the
+// rounding and against what FP32 scores can be off.  Of a closer decision, one in some
+// hundred tokens, the few numbers that it is about are worked out in FP64, and where
+// that does not settle it the token is done again in FP64 by the whole wave.
 #include "device_common.hpp"
 #include "../../include/gemvtile.h"
 #include "kernels.hpp"
@@ -28,21 +31,24 @@ namespace gt {
 
 namespace {
 
-constexpr int kWaves = 4;  // tokens of a workgroup
+constexpr int kWaves = 4;  // of a workgroup
 constexpr float kNegInf = -__builtin_inff();
 
-// What FP32 choices can be off.  Exponentials and quotients lose a few units of
-// 2^-24 each and a sum over E <= 1024 scores, added in a tree of 4 + 6 levels, at
-// most 10 more: 2^-20 of the token's largest score bounds every score.  Adding a
-// bias rounds by 2^-24 of the choice.  A choice x that is far below in FP32 cannot
-// be ahead of c in truth, however large it is: it would take |x| within 2^-22 of
-// |c|.  The bounds below are twice what that takes.
-__device__ inline float choice_margin(float top_score, float a, float b) {
-  return 0x1p-18f * top_score + 0x1p-22f * (__builtin_fabsf(a) + __builtin_fabsf(b));
+// What FP32 scores can be off, u = 2^-24.  fast_exp(v) is off by |v| + 2 units.  A
+// sigmoid's share of that is s (1 - s) (|v| + 2) <= 0.6 u, its sum and reciprocal are
+// 3 u more: 4 u.  A softmax is off by e^v (|v| + 2) <= 2.4 u over the sum, the sum of
+// E <= 1024 exponentials, added in a tree of 4 + 6 levels, by 10 u and what they are
+// off, quotient and product by 3: 16 u of the token's largest score.  Adding a bias
+// rounds by u of the choice.  A choice x that is far below in FP32 cannot be ahead of
+// c in truth, however large it is: it would take |x| within 2^-22 of |c|.
+__device__ inline float score_error(bool softmax, float top_score) { return softmax ? 0x1p-20f * top_score : 0x1p-22f; }
+// How far apart two choices have to be; `step` is that of the keys.
+__device__ inline float choice_margin(float score_error, float a, float b, float step) {
+  return 2.0f * score_error + 0x1p-23f * (__builtin_fabsf(a) + __builtin_fabsf(b)) + step;
 }
-// The same of a group's one or two best.
-__device__ inline float group_error(float top_score, float first, float second) {
-  return 0x1p-18f * top_score + 0x1p-22f * (__builtin_fabsf(first) + __builtin_fabsf(second));
+// What a group's one or two best can be off, and their sum.
+__device__ inline float group_error(float score_error, float first, float second) {
+  return 2.0f * score_error + 0x1p-23f * (__builtin_fabsf(first) + __builtin_fabsf(second));
 }
 
 // ---- keys --------------------------------------------------------------------
@@ -73,13 +79,9 @@ struct KeyOf<double> {
 // Key 0: no expert, or one taken or of a group that is not kept.
 
 using gt::wave_max;
-__device__ inline uint64_t wave_max(uint64_t v) {
-#pragma unroll
-  for (int lane = 1; lane < 64; lane <<= 1) {
-    const uint64_t o = static_cast<uint64_t>(__shfl_xor(static_cast<unsigned long long>(v), lane));
-    v = o > v ? o : v;
-  }
-  return v;
+__device__ inline uint64_t wave_max(uint64_t v) {  // the upper halves, then the lower ones of those that have it
+  const uint32_t high = static_cast<uint32_t>(v >> 32), top = wave_max(high);
+  return static_cast<uint64_t>(top) << 32 | wave_max(high == top ? static_cast<uint32_t>(v) : 0u);
 }
 __device__ inline float wave_add(float v) { return wave_sum(v); }
 __device__ inline double wave_add(double v) {
@@ -133,6 +135,23 @@ __device__ inline void load_logits(const typename Element<DT>::type *row, int E,
   }
 }
 
+// The lane's V biases, 0 behind the last expert.
+template <int V>
+__device__ inline void load_bias(const float *bias, int E, int lane, float *out) {
+  const int e0 = lane * V;
+  if (V % 4 == 0 && E % V == 0 && (reinterpret_cast<uintptr_t>(bias) & 15) == 0) {
+    if (e0 < E) {
+      __builtin_memcpy(out, __builtin_assume_aligned(bias + e0, V % 4 == 0 ? 16 : 4), V * sizeof(float));
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) out[i] = 0.0f;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) out[i] = e0 + i < E ? bias[e0 + i] : 0.0f;
+  }
+}
+
 template <typename F>
 __device__ inline F exp_of(F v) {
   if constexpr (sizeof(F) == 8) return ::exp(v);
@@ -140,214 +159,521 @@ __device__ inline F exp_of(F v) {
 }
 template <typename F>
 __device__ inline F sigmoid(F v) {
-  if (v < 0) {
-    const F e = exp_of(v);
-    return e / (1 + e);
-  }
-  return 1 / (1 + exp_of(-v));
+  const F e = exp_of(v < 0 ? v : -v);
+  return (v < 0 ? e : 1) / (1 + e);
 }
 
-// ---- the choice, in F --------------------------------------------------------
 struct TopkArgs {
   int E, k, groups, top_groups, group_best, score, norm;
   float scale;
 };
 
-// The choice of one token: lane j < k gets the id of its j-th expert, lane k that
-// of the best one left (-1 if there is none).  `buf` holds E numbers of the
-// wave's own.  Returns whether a group was kept by a margin that FP32 does not
-// vouch for (F = float).
-template <typename F, int V>
-__device__ inline bool choose(const float *logit, const float *bias, const TopkArgs &a, int lane, F *buf, int *id) {
-  typedef typename KeyOf<F>::type Key;
-  const bool ranked_by_logit = bias == nullptr;
-  const bool scores = !ranked_by_logit || (a.groups > 1 && a.group_best == 2);
-  F top_score = 1;  // at least the largest score
-  F score[V];
-  F choice[V];
-  if (scores) {
-    if (a.score == GEMVTILE_SCORE_SOFTMAX) {
-      float m = kNegInf;
-#pragma unroll
-      for (int i = 0; i < V; ++i) m = logit[i] > m ? logit[i] : m;
-      m = wave_max_logit(m);
-      F sum = 0;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        score[i] = m == kNegInf && logit[i] == kNegInf ? 0 : exp_of(static_cast<F>(logit[i]) - static_cast<F>(m));
-        sum += score[i];
-      }
-      sum = wave_add(sum);
-      if (sum == 0) sum = 1;  // every logit is -inf
-      top_score = 1 / sum;
-#pragma unroll
-      for (int i = 0; i < V; ++i) score[i] /= sum;
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) score[i] = sigmoid(static_cast<F>(logit[i]));
+// ---- the choice in FP64 --------------------------------------------------------
+// By a whole wave for one token: lane j < k gets the id of the j-th choice.  `buf`
+// holds E numbers of the wave's own.  Few tokens come here, so the code is never in
+// the instruction cache and its length is what it costs: loops, nothing unrolled.
+template <int DT>
+__device__ __attribute__((noinline)) int choose_exactly(const typename Element<DT>::type *row, const float *bias, TopkArgs a,
+                                                        double *buf) {
+  typedef KeyOf<double> Keys;
+  const int lane = threadIdx.x & 63;
+  const bool softmax = a.score == GEMVTILE_SCORE_SOFTMAX;
+  const int size = a.E / a.groups;
+  const bool sums = a.groups > 1 && a.group_best == 2 && size > 1;
+  const bool scored = bias != nullptr || sums;
+  float m = 0.0f;
+  double inv = 1;
+  if (scored && softmax) {
+    m = kNegInf;
+#pragma clang loop unroll(disable)
+    for (int e = lane; e < a.E; e += 64) {
+      const float l = widen_logit<DT>(row[e]);
+      m = l > m ? l : m;
     }
+    m = wave_max_logit(m);
   }
-  Key key[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = lane * V + i;
-    choice[i] = ranked_by_logit ? static_cast<F>(logit[i]) : score[i] + static_cast<F>(e < a.E ? bias[e] : 0.0f);
-    key[i] = e < a.E ? KeyOf<F>::of(choice[i]) : 0;
+  // A softmax's exponentials, or a sigmoid.
+  double sum = 0;
+#pragma clang loop unroll(disable)
+  for (int e = lane; e < a.E; e += 64) {
+    const double l = static_cast<double>(widen_logit<DT>(row[e]));
+    double v = l;
+    if (scored) {
+      const double x = softmax ? l - static_cast<double>(m) : l < 0 ? l : -l;
+      const double p = softmax && l == kNegInf ? 0 : exp(x);
+      sum += p;
+      v = softmax ? p : (l < 0 ? p : 1) / (1 + p);
+    }
+    buf[e] = v;
   }
-  bool close = false;
+  if (scored && softmax) {
+    sum = wave_add(sum);
+    inv = sum == 0 ? 1 : sum;  // 0: every logit is -inf
+  }
+#pragma clang loop unroll(disable)
+  for (int e = lane; e < a.E; e += 64)
+    if (scored) buf[e] = buf[e] / inv + (bias != nullptr ? static_cast<double>(bias[e]) : 0.0);
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  uint64_t kept = 1;
   if (a.groups > 1) {
-    const int size = a.E / a.groups;
-    const bool sums = a.group_best == 2 && size > 1;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (lane * V + i < a.E) buf[lane * V + i] = sums ? (ranked_by_logit ? score[i] : choice[i]) : choice[i];
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
     // Lane g works out group g.
-    F value = 0;
-    Key gkey = 0;
-    float error = 0.0f;
+    uint64_t gkey = 0;
     if (lane < a.groups) {
-      F first = buf[lane * size], second = 0;
-      Key k1 = KeyOf<F>::of(first), k2 = 0;
+      double first = buf[lane * size], second = 0;
+      uint64_t k1 = Keys::of(first), k2 = 0;
+#pragma unroll 4
       for (int i = 1; i < size; ++i) {
-        const F v = buf[lane * size + i];
-        const Key kv = KeyOf<F>::of(v);
-        if (kv > k1) {
-          second = first;
-          k2 = k1;
-          first = v;
-          k1 = kv;
-        } else if (kv > k2) {
-          second = v;
-          k2 = kv;
-        }
+        const double v = buf[lane * size + i];
+        const uint64_t kv = Keys::of(v);
+        const bool ahead = kv > k1, next = kv > k2;
+        second = ahead ? first : next ? v : second;
+        k2 = ahead ? k1 : next ? kv : k2;
+        first = ahead ? v : first;
+        k1 = ahead ? kv : k1;
       }
-      value = sums ? first + second : first;
-      if (!sums) second = 0;
-      if constexpr (sizeof(F) == 4) error = group_error(top_score, first, second);
-      gkey = KeyOf<F>::of(value);
+      gkey = Keys::of(sums ? first + second : first);
     }
     int rank = 0;  // groups ahead of this one
+#pragma clang loop unroll(disable)
     for (int o = 0; o < a.groups; ++o) {
-      Key other;
-      if constexpr (sizeof(Key) == 8)
-        other = static_cast<Key>(__shfl(static_cast<unsigned long long>(gkey), o));
-      else
-        other = static_cast<Key>(__builtin_amdgcn_readlane(static_cast<int>(gkey), o));
+      const uint64_t other =
+          static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(gkey >> 32), o))) << 32 |
+          static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(gkey), o));
       rank += other > gkey || (other == gkey && o < lane) ? 1 : 0;
     }
-    const uint64_t kept = __ballot(lane < a.groups && rank < a.top_groups);
-    if constexpr (sizeof(F) == 4) {
-      // The last kept group against the first dropped one.
-      if (scores && a.top_groups < a.groups) {
-        const int last = __builtin_ctzll(__ballot(lane < a.groups && rank == a.top_groups - 1));
-        const int next = __builtin_ctzll(__ballot(lane < a.groups && rank == a.top_groups));
-        const float v1 = __shfl(value, last), v2 = __shfl(value, next);
-        // The largest error of any group (as bits; a NaN above all).
-        const float most = __builtin_bit_cast(float, wave_max(__builtin_bit_cast(uint32_t, error)));
-        close = !(v1 - v2 > 2.0f * most);
+    kept = __ballot(lane < a.groups && rank < a.top_groups);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+  // Each lane has a run of experts; buf holds their keys from here on.
+  const int run = (a.E + 63) / 64, e0 = lane * run;
+  uint64_t *keys = reinterpret_cast<uint64_t *>(buf);
+  uint64_t best = 0;
+  int at = 0;
+#pragma clang loop unroll(disable)
+  for (int e = e0; e < e0 + run && e < a.E; ++e) {
+    const uint64_t key = (kept >> (e / size)) & 1 ? Keys::of(bias != nullptr ? buf[e] : static_cast<double>(widen_logit<DT>(row[e]))) : 0;
+    keys[e] = key;
+    at = key > best ? e : at;
+    best = key > best ? key : best;
+  }
+  int mine = -1;
+#pragma clang loop unroll(disable)
+  for (int j = 0; j < a.k; ++j) {
+    const uint64_t top = wave_max(best);
+    const int from = __builtin_ctzll(__ballot(best == top));  // the lowest lane, and in it the lowest expert
+    const int chosen = __builtin_amdgcn_readlane(at, from);
+    if (lane == j) mine = chosen;
+    if (lane == from) {
+      keys[chosen] = 0;
+      best = 0;
+#pragma clang loop unroll(disable)
+      for (int e = e0; e < e0 + run && e < a.E; ++e) {
+        const uint64_t key = keys[e];
+        at = key > best ? e : at;
+        best = key > best ? key : best;
       }
     }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = lane * V + i;
-      if (e < a.E && !((kept >> (e / size)) & 1)) key[i] = 0;
-    }
   }
-  // One more than is wanted where choices are checked.
-  const int rounds = a.k + (sizeof(F) == 4 && !ranked_by_logit ? 1 : 0);
-  int mine = -1;
-  for (int j = 0; j < rounds; ++j) {
-    Key best = key[0];
-#pragma unroll
-    for (int i = 1; i < V; ++i) best = key[i] > best ? key[i] : best;
-    const Key top = wave_max(best);
-    if (top == 0) break;
-    const int from = __builtin_ctzll(__ballot(best == top));
-    int slot = 0;
-#pragma unroll
-    for (int i = V - 1; i > 0; --i) slot = key[i] == top ? i : slot;
-    if (key[0] == top) slot = 0;
-    const int chosen = from * V + __builtin_amdgcn_readlane(slot, from);
-    if (lane == j) mine = chosen;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (lane * V + i == chosen) key[i] = 0;
-  }
-  *id = mine;
-  return close;
+  return mine;
 }
 
-template <int DT, int V>
+// ---- the choice in FP32 ----------------------------------------------------------
+// Over the L lanes of a token, in all of them.
+template <int L>
+__device__ inline uint32_t part_max(uint32_t v) {
+  if constexpr (L == 16) return max_of_16_lanes(v);
+  else return wave_max(v);
+}
+template <int L>
+__device__ inline float part_sum(float v) {
+  if constexpr (L == 64) return wave_sum(v);
+  v = dpp_add<0xB1>(v);
+  v = dpp_add<0x4E>(v);
+  v = dpp_add<0x141>(v);
+  return dpp_add<0x140>(v);
+}
+// NaN left aside; -inf of nothing.
+template <int L>
+__device__ inline float part_max(float v) {
+  return KeyOf<float>::value(part_max<L>(KeyOf<float>::of(v == v ? v : kNegInf)));
+}
+// Whether it is so in any of the token's lanes.
+template <int L>
+__device__ inline bool part_any(bool v, int lane) {
+  const uint64_t b = __ballot(v);
+  if constexpr (L == 64) return b != 0;
+  return ((b >> (lane & 48)) & 0xffffu) != 0;
+}
+// e^v for v <= 0 by the hardware's power of two: off by |v| 2^-24 and two units.
+__device__ inline float fast_exp(float v) { return __builtin_amdgcn_exp2f(v * 0x1.715476p+0f); }
+__device__ inline float fast_sigmoid(float v) { return __builtin_amdgcn_rcpf(1.0f + fast_exp(-v)); }
+
+template <int N>
+__device__ inline float tree_sum(const float *v) {
+  if constexpr (N == 1) return v[0];
+  else return tree_sum<N / 2>(v) + tree_sum<N / 2>(v + N / 2);
+}
+
+template <int CTRL>
+__device__ inline float dpp_move(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false));
+}
+// A group's two best from those of two of its parts.
+struct Best {
+  float first, second;
+};
+__device__ inline Best merge(Best a, float first, float second) {
+  return {__builtin_fmaxf(a.first, first),
+          __builtin_fmaxf(__builtin_fminf(a.first, first), __builtin_fmaxf(a.second, second))};
+}
+
+constexpr int kMaxGroups = 64;
+template <int L, int V>
+union TopkShared {
+  double exact[L * V];  // of one token
+  struct {
+    float value[64 / L][L * V];
+    float group[64 / L][kMaxGroups], error[64 / L][kMaxGroups];
+  } fast;
+};
+
+template <int DT, int L, int V>
 __global__ void __launch_bounds__(kWaves * 64)
 topk_kernel(const typename Element<DT>::type *__restrict__ logits, const float *__restrict__ bias, int *__restrict__ ids,
             float *__restrict__ weights, int64_t T, TopkArgs a) {
-  __shared__ double buffers[kWaves][64 * V];
+  constexpr int kTokens = 64 / L;  // of a wave
+  constexpr int kIndexBits = __builtin_ctz(L * V);
+  __shared__ TopkShared<L, V> shared[kWaves];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kWaves + wave;
-  if (t >= T) return;
+  const int part = lane / L, sub = lane & (L - 1);
+  const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWaves + wave) * kTokens;
+  if (t0 >= T) return;  // the whole wave
+  const bool there = t0 + part < T;
+  const int64_t t = there ? t0 + part : T - 1;  // lanes without a token do the last one's work
   const typename Element<DT>::type *row = logits + t * a.E;
-  float logit[V];
-  load_logits<DT, V>(row, a.E, lane, logit);
-  int id;
-  bool again = choose<float, V>(logit, bias, a, lane, reinterpret_cast<float *>(buffers[wave]), &id);
+  const bool biased = bias != nullptr;
+  const bool softmax = a.score == GEMVTILE_SCORE_SOFTMAX;
+  const int size = a.E / a.groups;
+  const bool sums = a.groups > 1 && a.group_best == 2 && size > 1;
+  const bool rounded = biased || DT == kF32;  // what the keys hold is not exact
 
+  float logit[V], value[V];
+  load_logits<DT, V>(row, a.E, sub, logit);
   bool nan = false;  // among all logits
 #pragma unroll
   for (int i = 0; i < V; ++i) nan |= logit[i] != logit[i];
-  nan = __ballot(nan) != 0;
+  nan = part_any<L>(nan, lane);
   float top_logit = kNegInf, sum = 1.0f;  // of all experts
-  if (a.score == GEMVTILE_SCORE_SOFTMAX && (!a.norm || bias != nullptr)) {
+  const bool scored = biased || sums;
+  if (softmax && (scored || !a.norm)) {
     float m = kNegInf;
 #pragma unroll
     for (int i = 0; i < V; ++i) m = logit[i] > m ? logit[i] : m;
-    top_logit = wave_max_logit(m);
-    float part = 0.0f;
+    top_logit = part_max<L>(m);
 #pragma unroll
-    for (int i = 0; i < V; ++i) part += logit[i] == kNegInf ? 0.0f : expf(logit[i] - top_logit);
-    sum = wave_sum(part);
+    for (int i = 0; i < V; ++i) value[i] = logit[i] == kNegInf ? 0.0f : fast_exp(logit[i] - top_logit);
+    sum = part_sum<L>(tree_sum<V>(value));
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int i = 0; i < V; ++i) value[i] *= inv;
+  } else if (scored) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) value[i] = fast_sigmoid(logit[i]);
   }
-  if (bias != nullptr) {
-    // Lane j has the j-th choice, lane k the next one.
-    const float l = id >= 0 ? widen_logit<DT>(row[id]) : kNegInf;
-    const float b = id >= 0 ? bias[id] : 0.0f;
-    const bool softmax = a.score == GEMVTILE_SCORE_SOFTMAX;
-    const float score = softmax ? (l == kNegInf ? 0.0f : expf(l - top_logit) / sum) : sigmoid(l);
-    const float choice = score + b;
+  const float wrong = score_error(softmax, 1.0f / sum);
+  float own_bias[V];
+  if (biased) {
+    load_bias<V>(bias, a.E, sub, own_bias);
+#pragma unroll
+    for (int i = 0; i < V; ++i) value[i] += own_bias[i];
+  } else if (!sums) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) value[i] = logit[i];
+  }
+  bool again = nan && (scored || rounded || a.groups > 1);
+
+  // ---- groups: value[] is what they count by
+  uint32_t dropped = 0;  // experts of this lane (as bits) in groups that are not kept
+  if (a.groups > 1) {
+    bool close = false;
+    const int lanes = size / V;  // of a group, if that is a power of two
+    if (lanes * V == size && (lanes & (lanes - 1)) == 0) {
+      Best b = {kNegInf, kNegInf};
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float v = sub * V + i < a.E ? value[i] : kNegInf;
+        b = merge(b, v == v ? v : kNegInf, kNegInf);
+      }
+      if (lanes >= 2) b = merge(b, dpp_move<0xB1>(b.first), dpp_move<0xB1>(b.second));
+      if (lanes >= 4) b = merge(b, dpp_move<0x4E>(b.first), dpp_move<0x4E>(b.second));
+      if (lanes >= 8) b = merge(b, dpp_move<0x141>(b.first), dpp_move<0x141>(b.second));
+      if (lanes >= 16) b = merge(b, dpp_move<0x140>(b.first), dpp_move<0x140>(b.second));
+      if (lanes >= 32) b = merge(b, __shfl_xor(b.first, 16), __shfl_xor(b.second, 16));
+      const int mine = sub / lanes;
+      const bool real = mine < a.groups;
+      const float counts = sums ? b.first + b.second : b.first;
+      again |= part_any<L>(counts != counts, lane);
+      int rank = 0;  // groups ahead of this one
+      for (int o = 0; o < a.groups; ++o) {
+        const float other = __shfl(counts, part * L + o * lanes);
+        rank += other > counts || (other == counts && o < mine) ? 1 : 0;
+      }
+      const bool kept = real && rank < a.top_groups;
+      if (!kept) dropped = ~0u;
+      if (scored && a.top_groups < a.groups) {
+        // The last kept group against the first dropped one, and the largest error of any.
+        const float low = -part_max<L>(kept ? -counts : kNegInf), high = part_max<L>(real && !kept ? counts : kNegInf);
+        const float error = real ? group_error(wrong, b.first, sums ? b.second : 0.0f) : 0.0f;
+        const float most = __builtin_bit_cast(float, part_max<L>(__builtin_bit_cast(uint32_t, error)));
+        close = !(low - high > 2.0f * most);
+        if (__ballot(close) != 0 && !softmax) {
+          // In FP64, by the choices that count alone.  Where others come near them,
+          // the group counts by more than these.
+          const int need = sums ? 2 : 1;
+          const float least = sums ? b.second : b.first;
+          const float edge = least - choice_margin(wrong, least, least, 0.0f);
+          int count = 0;
+          float l1 = 0.0f, b1 = 0.0f, l2 = 0.0f, b2 = 0.0f;
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            if (sub * V + i < a.E && value[i] >= edge) {
+              l2 = l1;
+              b2 = b1;
+              l1 = logit[i];
+              b1 = biased ? own_bias[i] : 0.0f;
+              ++count;
+            }
+          }
+          double exact = count > 0 ? sigmoid(static_cast<double>(l1)) + static_cast<double>(b1) : 0.0;
+          if (count > 1) exact += sigmoid(static_cast<double>(l2)) + static_cast<double>(b2);
+          for (int d = 1; d < lanes; d <<= 1) {
+            exact += __shfl_xor(exact, d);
+            count += __shfl_xor(count, d);
+          }
+          const bool unclear = part_any<L>(real && count != need, lane);
+          rank = 0;
+          for (int o = 0; o < a.groups; ++o) {
+            const double other = __shfl(exact, part * L + o * lanes);
+            rank += other > exact || (other == exact && o < mine) ? 1 : 0;
+          }
+          if (close && !unclear) {
+            dropped = real && rank < a.top_groups ? 0 : ~0u;
+            close = false;
+          }
+        }
+      }
+    } else {
+      auto &s = shared[wave].fast;
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (sub * V + i < a.E) s.value[part][sub * V + i] = value[i];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      for (int o = sub; o < a.groups; o += L) {
+        Best b = {kNegInf, kNegInf};
+        for (int i = 0; i < size; ++i) {
+          const float v = s.value[part][o * size + i];
+          b = merge(b, v == v ? v : kNegInf, kNegInf);
+        }
+        s.group[part][o] = sums ? b.first + b.second : b.first;
+        s.error[part][o] = group_error(wrong, b.first, sums ? b.second : 0.0f);
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      float low = __builtin_inff(), high = kNegInf, most = 0.0f;
+      bool none = false;
+      for (int o = sub; o < a.groups; o += L) {
+        const float counts = s.group[part][o];
+        none |= counts != counts;
+        int rank = 0;
+        for (int p = 0; p < a.groups; ++p) {
+          const float other = s.group[part][p];
+          rank += other > counts || (other == counts && p < o) ? 1 : 0;
+        }
+        const bool kept = rank < a.top_groups;
+        low = kept ? __builtin_fminf(low, counts) : low;
+        high = kept ? high : __builtin_fmaxf(high, counts);
+        const float error = s.error[part][o];
+        most = error > most || error != error ? error : most;
+        s.error[part][o] = kept ? 1.0f : 0.0f;  // only this lane reads the errors of its groups
+      }
+      again |= part_any<L>(none, lane);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int e = sub * V + i;
+        if (e < a.E && s.error[part][e / size] == 0.0f) dropped |= 1u << i;
+      }
+      if (scored && a.top_groups < a.groups) {
+        low = -part_max<L>(-low);
+        high = part_max<L>(high);
+        most = __builtin_bit_cast(float, part_max<L>(__builtin_bit_cast(uint32_t, most)));
+        close = !(low - high > 2.0f * most);
+      }
+    }
+    again |= close;
+  }
+  if (!biased && sums) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) value[i] = logit[i];
+  }
+
+  // ---- keys: 1 + the rounded choice above the inverted number; 0: not to be chosen
+  uint32_t key[V];
+  float step = 0.0f;
+  if (rounded) {
+    // 16 below the largest choice, or less if there is less, in equal steps.
+    constexpr uint32_t kSteps = (1u << (31 - kIndexBits < 23 ? 31 - kIndexBits : 23)) - 4;  // FP32 counts them all
+    float high = kNegInf, low = __builtin_inff();
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const bool in = sub * V + i < a.E && !((dropped >> i) & 1) && value[i] > kNegInf;
+      high = in ? __builtin_fmaxf(high, value[i]) : high;
+      low = in ? __builtin_fminf(low, value[i]) : low;
+    }
+    high = part_max<L>(high);
+    low = -part_max<L>(-low);
+    float range = high - low;
+    range = range < 16.0f ? range : 16.0f;
+    range = range > 1e-30f ? range : 1e-30f;
+    again |= !(__builtin_fabsf(high) < __builtin_inff());
+    const float base = high - range, scale = static_cast<float>(kSteps) / range;
+    step = 2.0f * range / static_cast<float>(kSteps);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float q = __builtin_fminf(__builtin_fmaxf((value[i] - base) * scale, 0.0f), static_cast<float>(kSteps));
+      key[i] = static_cast<uint32_t>(q);
+    }
+  } else {
+    // All bits that differ among 16-bit numbers.
+    constexpr int kShift = DT == kBF16 ? 16 : 13;
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = KeyOf<float>::of(value[i]) >> kShift;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = sub * V + i;
+    key[i] = (key[i] + 1) << kIndexBits | static_cast<uint32_t>(L * V - 1 - e);
+    if (e >= a.E || ((dropped >> i) & 1)) key[i] = 0;
+  }
+
+  // ---- rounds: lane j gets the j-th largest key, two more than are wanted where keys are rounded
+  uint32_t best = key[0];
+#pragma unroll
+  for (int i = 1; i < V; ++i) best = key[i] > best ? key[i] : best;
+  uint32_t mine = 0;
+  const int rounds = a.k + (rounded ? 2 : 0);
+  for (int j = 0; j < rounds; ++j) {
+    const uint32_t top = part_max<L>(best);
+    if (sub == j) mine = top;
+    // The largest key below: keys less top wrap round to the upper half.
+    uint32_t below = key[0] - top;
+#pragma unroll
+    for (int i = 1; i < V; ++i) below = key[i] - top > below ? key[i] - top : below;
+    best = below & 0x80000000u ? below + top : 0;
+  }
+  const auto number = [](uint32_t key) { return key == 0 ? -1 : L * V - 1 - static_cast<int>(key & (L * V - 1)); };
+  int id = number(mine);
+  float l = id >= 0 ? widen_logit<DT>(row[id]) : kNegInf;
+
+  if (rounded) {
+    // Lane j has the j-th choice, lanes k and k + 1 the next ones.
+    const float b = biased && id >= 0 ? bias[id] : 0.0f;
+    float choice = l;
+    if (biased)
+      choice = (softmax ? (l == kNegInf ? 0.0f : fast_exp(l - top_logit) / sum) : fast_sigmoid(l)) + b;
     const float next_choice = __shfl_down(choice, 1), next_l = __shfl_down(l, 1), next_b = __shfl_down(b, 1);
-    const int next_id = __shfl_down(id, 1);
+    const uint32_t next_key = static_cast<uint32_t>(__shfl_down(static_cast<int>(mine), 1));
+    const bool judged = sub < a.k && next_key != 0;
     // Equal logits with equal biases are a tie in any arithmetic.
     const bool tie = l == next_l && b == next_b;
-    const float margin = choice_margin(softmax ? 1.0f / sum : 1.0f, choice, next_choice);
-    again |= __ballot(lane < a.k && next_id >= 0 && !tie && !(choice - next_choice > margin)) != 0;
+    const bool good = tie || (biased ? choice - next_choice > choice_margin(wrong, choice, next_choice, step) : l > next_l);
+    const bool bad = part_any<L>(judged && !good, lane);
+    // Where the last choice and the next one tie, or share a step, or are too near,
+    // others may be as near: not if the one after next is further down.
+    const bool edge = sub == a.k - 1 && judged && (tie || !good || mine >> kIndexBits == next_key >> kIndexBits);
+    bool alone = true;
+    if (__ballot(edge || bad) != 0) {
+      const int from = part * L + a.k - 1;
+      const float last = __shfl(choice, from), after = __shfl(choice, from + 2);
+      const float last_l = __shfl(l, from), last_b = __shfl(b, from);
+      const uint32_t last_key = static_cast<uint32_t>(__shfl(static_cast<int>(mine), from));
+      const uint32_t after_key = static_cast<uint32_t>(__shfl(static_cast<int>(mine), from + 2));
+      alone = after_key == 0 || (biased ? last - after > choice_margin(wrong, last, after, step)
+                                        : last_key >> kIndexBits != after_key >> kIndexBits);
+      const bool asked = __shfl(static_cast<int>(edge), from) != 0 && !alone;
+      // Each other one has to be such a tie, or further down.
+      bool doubt = false;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (key[i] != 0 && key[i] < last_key) {
+          const float other = biased ? value[i] : logit[i];
+          const bool same = logit[i] == last_l && (!biased || own_bias[i] == last_b);
+          doubt |= !same && !(biased ? last - other > choice_margin(wrong, last, other, step) : last_l > other);
+        }
+      }
+      again |= part_any<L>(doubt && asked, lane);
+      again |= bad && (!alone || (biased && softmax));
+      if (__ballot(bad && !again) != 0) {
+        // The k + 2 in FP64: lane j takes the place that its number has among them.
+        const bool in = sub < rounds && id >= 0;
+        double exact = static_cast<double>(l);
+        if (biased) exact = sigmoid(exact) + static_cast<double>(b);
+        int place = 0;
+        for (int o = 0; o < rounds; ++o) {
+          const double other = __shfl(exact, part * L + o);
+          const int other_id = __shfl(id, part * L + o);
+          place += other_id >= 0 && (other > exact || (other == exact && other_id < id)) ? 1 : 0;
+        }
+        const int to = (part * L + (in ? place : sub)) * 4;
+        const int new_id = __builtin_amdgcn_ds_permute(to, id);
+        const float new_l = __builtin_bit_cast(float, __builtin_amdgcn_ds_permute(to, __builtin_bit_cast(int, l)));
+        if (bad) {
+          id = new_id;
+          l = new_l;
+        }
+      }
+    }
   }
-  if (again) choose<double, V>(logit, bias, a, lane, buffers[wave], &id);
+  uint64_t todo = __ballot(again && there);
+  while (todo != 0) {
+    const int p = __builtin_ctzll(todo) / L;
+    todo &= L == 64 ? 0 : ~(uint64_t{0xffff} << (16 * p));
+    const int exact = choose_exactly<DT>(logits + (t0 + p) * a.E, bias, a, shared[wave].exact);
+    const int moved = __shfl(exact, sub);
+    if (part == p) {
+      id = moved;
+      l = id >= 0 ? widen_logit<DT>(row[id]) : kNegInf;
+    }
+  }
 
-  const bool has = lane < a.k;
-  const float own = has ? widen_logit<DT>(row[id]) : kNegInf;
+  const bool has = sub < a.k;
+  const float own = has ? l : kNegInf;
   float w;
   if (a.norm) {
     // exp(own - ref) is the score times a number that all of them share; with a
     // sigmoid's 1 + exp(own) below, ref is 0 once a logit is above.
-    float ref = wave_max_logit(own);
-    if (a.score == GEMVTILE_SCORE_SIGMOID) nan = __ballot(has && own != own) != 0;
-    if (a.score == GEMVTILE_SCORE_SOFTMAX) {
+    float ref = part_max<L>(own);
+    if (!softmax) nan = part_any<L>(has && own != own, lane);
+    if (softmax) {
       w = ref == kNegInf ? 0.0f : expf(own - ref);
     } else {
       ref = ref < 0.0f ? ref : 0.0f;
       w = own > 0.0f ? 1.0f / (1.0f + expf(-own)) : ref == kNegInf ? 0.0f : expf(own - ref) / (1.0f + expf(own));
     }
     if (!has) w = 0.0f;
-    const float total = wave_add(w);
+    const float total = part_sum<L>(w);
     w = nan ? __builtin_nanf("") : total > 0.0f ? w / total : total;
   } else {
-    w = a.score == GEMVTILE_SCORE_SOFTMAX ? (own == kNegInf && !nan ? 0.0f : expf(own - top_logit) / sum) : sigmoid(own);
+    w = softmax ? (own == kNegInf && !nan ? 0.0f : expf(own - top_logit) / sum) : sigmoid(own);
   }
-  if (has) {
-    ids[t * a.k + lane] = id;
-    weights[t * a.k + lane] = a.scale * w;
+  if (has && there) {
+    ids[t * a.k + sub] = id;
+    weights[t * a.k + sub] = a.scale * w;
   }
 }
 
@@ -474,11 +800,15 @@ __device__ inline SortRun sort_run(int64_t begin, int64_t end, int part, int par
 }
 
 __device__ inline void count_run(const int *ids, SortRun r, int E, uint32_t *count, int lane) {
+#pragma unroll 4
   for (int64_t i = r.begin + lane; i < r.end; i += 64) {
     const int e = ids[i];
     if (e >= 0 && e < E) atomicAdd(&count[e], 1u);  // a count: its order does not matter
   }
 }
+
+// Threads that share an expert's column of `hist`.
+__device__ inline int column_parts(int E) { return E <= 64 ? 8 : E <= 128 ? 4 : E <= 256 ? 2 : 1; }
 
 // hist [blocks, E]: each workgroup's slots by expert.
 __global__ void __launch_bounds__(kSortThreads)
@@ -498,31 +828,42 @@ sort_place_kernel(const int *__restrict__ ids, const int *__restrict__ hist, int
                   int64_t n, int E, int bits) {
   __shared__ uint32_t count[kSortWaves][kSortExperts];  // first a wave's slots by expert, then its next row of each
   __shared__ uint32_t wave_total[kSortWaves];
+  __shared__ uint32_t ahead[kSortExperts], all_of[kSortExperts];  // an expert's slots in earlier workgroups, and in all
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   for (int e = lane; e < E; e += 64) count[wave][e] = 0;
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
+  for (int e = threadIdx.x; e < E; e += kSortThreads) ahead[e] = all_of[e] = 0;
+  __syncthreads();
+  if (hist != nullptr) {
+    const int parts = column_parts(E), blocks = static_cast<int>(gridDim.x), mine = static_cast<int>(blockIdx.x);
+    for (int c = threadIdx.x; c < E * parts; c += kSortThreads) {
+      const int part = c / E, e = c - part * E;
+      const int past = blocks * (part + 1) / parts;
+      uint32_t before = 0, total = 0;
+#pragma unroll 16
+      for (int b = blocks * part / parts; b < past; ++b) {
+        const uint32_t v = static_cast<uint32_t>(hist[static_cast<int64_t>(b) * E + e]);
+        before += b < mine ? v : 0u;
+        total += v;
+      }
+      atomicAdd(&ahead[e], before);  // counts: their order does not matter
+      atomicAdd(&all_of[e], total);
+    }
+  }
   const SortRun all = sort_run(0, n, blockIdx.x, gridDim.x);
   const SortRun mine = sort_run(all.begin, all.end, wave, kSortWaves);
   count_run(ids, mine, E, count[wave], lane);
   __syncthreads();
-  // Thread i has experts 2 i and 2 i + 1: slots ahead in earlier workgroups, and in all.
+  // Thread i has experts 2 i and 2 i + 1.
   uint32_t before[2] = {0, 0}, total[2] = {0, 0};
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     const int e = 2 * static_cast<int>(threadIdx.x) + s;
     if (e < E) {
+      before[s] = ahead[e];
+      total[s] = all_of[e];
       if (hist == nullptr) {
         for (int w = 0; w < kSortWaves; ++w) total[s] += count[w][e];
-      } else {
-        const int blocks = static_cast<int>(gridDim.x);
-#pragma unroll 8
-        for (int b = 0; b < blocks; ++b) {
-          const uint32_t c = static_cast<uint32_t>(hist[static_cast<int64_t>(b) * E + e]);
-          before[s] += b < static_cast<int>(blockIdx.x) ? c : 0u;
-          total[s] += c;
-        }
       }
     }
   }
@@ -556,10 +897,12 @@ sort_place_kernel(const int *__restrict__ ids, const int *__restrict__ hist, int
   }
   __syncthreads();
   volatile uint32_t *next_row = count[wave];
+  int coming = mine.begin + lane < mine.end ? ids[mine.begin + lane] : -1;
   for (int64_t base = mine.begin; base < mine.end; base += 64) {
     const int64_t i = base + lane;
     const bool in = i < mine.end;
-    const int e = in ? ids[i] : -1;
+    const int e = coming;
+    coming = i + 64 < mine.end ? ids[i + 64] : -1;
     const bool valid = e >= 0 && e < E;
     uint64_t same = __ballot(valid);
     for (int b = 0; b < bits; ++b) {
@@ -579,21 +922,29 @@ sort_place_kernel(const int *__restrict__ ids, const int *__restrict__ hist, int
   }
 }
 
-template <int DT, int V>
+template <int DT, int L, int V>
 hipError_t launch_topk_v(const void *logits, const float *bias, int *ids, float *weights, int64_t T, const TopkArgs &a,
                          hipStream_t stream) {
-  hipLaunchKernelGGL((topk_kernel<DT, V>), dim3(static_cast<unsigned>((T + kWaves - 1) / kWaves)), dim3(kWaves * 64), 0, stream,
-                     static_cast<const typename Element<DT>::type *>(logits), bias, ids, weights, T, a);
+  const int64_t tokens = kWaves * (64 / L);
+  hipLaunchKernelGGL((topk_kernel<DT, L, V>), dim3(static_cast<unsigned>((T + tokens - 1) / tokens)), dim3(kWaves * 64), 0,
+                     stream, static_cast<const typename Element<DT>::type *>(logits), bias, ids, weights, T, a);
   return hipGetLastError();
 }
+// 16 lanes hold the k choices and two more.
 template <int DT>
 hipError_t launch_topk_dt(const void *logits, const float *bias, int *ids, float *weights, int64_t T, const TopkArgs &a,
                           hipStream_t stream) {
-  if (a.E <= 64) return launch_topk_v<DT, 1>(logits, bias, ids, weights, T, a, stream);
-  if (a.E <= 128) return launch_topk_v<DT, 2>(logits, bias, ids, weights, T, a, stream);
-  if (a.E <= 256) return launch_topk_v<DT, 4>(logits, bias, ids, weights, T, a, stream);
-  if (a.E <= 512) return launch_topk_v<DT, 8>(logits, bias, ids, weights, T, a, stream);
-  return launch_topk_v<DT, 16>(logits, bias, ids, weights, T, a, stream);
+  if (a.k <= 14) {
+    if (a.E <= 16) return launch_topk_v<DT, 16, 1>(logits, bias, ids, weights, T, a, stream);
+    if (a.E <= 32) return launch_topk_v<DT, 16, 2>(logits, bias, ids, weights, T, a, stream);
+    if (a.E <= 64) return launch_topk_v<DT, 16, 4>(logits, bias, ids, weights, T, a, stream);
+    if (a.E <= 128) return launch_topk_v<DT, 16, 8>(logits, bias, ids, weights, T, a, stream);
+    if (a.E <= 256) return launch_topk_v<DT, 16, 16>(logits, bias, ids, weights, T, a, stream);
+  }
+  if (a.E <= 64) return launch_topk_v<DT, 64, 1>(logits, bias, ids, weights, T, a, stream);
+  if (a.E <= 256) return launch_topk_v<DT, 64, 4>(logits, bias, ids, weights, T, a, stream);
+  if (a.E <= 512) return launch_topk_v<DT, 64, 8>(logits, bias, ids, weights, T, a, stream);
+  return launch_topk_v<DT, 64, 16>(logits, bias, ids, weights, T, a, stream);
 }
 template <int DT, int V>
 hipError_t launch_topk_grad_v(const void *logits, const int *ids, const float *dweights, void *dlogits, int64_t T,
