@@ -14,7 +14,7 @@ constexpr int64_t kMaxFp4N = int64_t{1} << 25;
 constexpr int64_t kMaxFp4M = int64_t{1} << 19;
 constexpr int64_t kMaxFp4K = 4194272;
 constexpr int64_t kMaxFp4Elements = (int64_t{1} << 36) - 4096;
-constexpr int64_t kMaxNormC = 65536;
+constexpr int64_t kMaxNormC = 32768;
 constexpr int64_t kMaxTopkT = (int64_t{1} << 26) - 64;
 constexpr int64_t kMaxExperts = 1024, kMaxChoices = 32, kMaxExpertGroups = 64;
 constexpr int64_t kMaxTokens = (int64_t{1} << 24) - 1;

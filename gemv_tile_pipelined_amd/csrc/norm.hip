@@ -8,10 +8,14 @@
 //   dx = r (weight dy) - h r^3 mean_c(weight dy h) + dh
 //   dweight[c] = sum_t dy h r
 //
-// Statistics, y and both gradients are in FP32 until the one rounding of what is
-// written.  A workgroup holds a row in registers between the sum of squares and
-// the output, so each input is read once and each output written once: bound by
-// memory.  16 lanes hold a block of 128 columns, 8 each, so a block's largest
+// A workgroup holds a row in registers between the sum of squares and the output,
+// so each input is read once and each output written once: bound by memory.  The
+// sum of squares and r are in FP64, which costs nothing here (8192 x 4096 with the
+// residual, 8 bits out, takes 46 us either way) and makes the e4m3 numbers those
+// nearest to y / scale but for one in some 10^7: weight h is exact in FP32, r /
+// scale has 48 bits, and the product is rounded to odd before the conversion, so
+// that only real ties tie.  y in 16 bits and both gradients are FP32 until their one
+// rounding.  16 lanes hold a block of 128 columns, 8 each, so a block's largest
 // number is found within a lane row.
 #include "fp8_common.hpp"
 #include "kernels.hpp"
@@ -21,7 +25,6 @@ namespace gt {
 
 namespace {
 
-constexpr float kE4m3Max = 448.0f;
 constexpr float kMinScale = 0x1p-80f;
 
 // Sum over the workgroup, in every lane; waves are added in order.  `slots` is
@@ -38,6 +41,41 @@ __device__ inline float group_sum(float v, float *slots) {
   return sum;
 }
 
+// The same in FP64.
+template <int THREADS>
+__device__ inline double group_sum(double v, double *slots) {
+  v = wave_sum_last(v);
+  if ((threadIdx.x & 63) == 63) slots[threadIdx.x >> 6] = v;
+  __syncthreads();
+  double sum = slots[0];
+#pragma unroll
+  for (int w = 1; w < THREADS / 64; ++w) sum += slots[w];
+  return sum;
+}
+
+// 1 / sqrt(v): the instruction's approximation and two Newton steps; 0, infinity
+// and NaN as they come.
+__device__ inline double inverse_root(double v) {
+  double r = __builtin_amdgcn_rsq(v);
+  if (v > 0 && v < __builtin_inf()) {
+    r = r * (1.5 - 0.5 * v * r * r);
+    r = r * (1.5 - 0.5 * v * r * r);
+  }
+  return r;
+}
+
+// p (high + low) rounded to odd: the rounded product, one bit lower where it is
+// above the real one, with its last bit set unless it is that.
+__device__ inline float product_to_odd(float p, float high, float low) {
+  const float q = p * high;
+  const float rest = __builtin_fmaf(p, low, __builtin_fmaf(p, high, -q));
+  const float r = q < 0.0f ? -rest : rest;  // towards larger magnitudes
+  uint32_t b = __builtin_bit_cast(uint32_t, q);
+  b -= r < 0.0f ? 1u : 0u;
+  b |= r != 0.0f ? 1u : 0u;
+  return __builtin_bit_cast(float, b);
+}
+
 // h may be x or residual: a row's vectors are all read by the threads that write
 // them, before they do.
 template <int DT, int THREADS, int NV, bool FP8>
@@ -45,8 +83,9 @@ __global__ void __launch_bounds__(THREADS)
 rmsnorm_kernel(const uint16_t *x, const uint16_t *residual, const uint16_t *__restrict__ weight, uint16_t *h,
                uint16_t *__restrict__ y, uint8_t *__restrict__ q, float *__restrict__ scale, float *__restrict__ rstd, int T,
                int C, float eps) {
-  __shared__ float slots[2][THREADS / 64];
+  __shared__ double slots[2][THREADS / 64];
   const int vecs = C / 8, blocks = (C + kScaleBlock - 1) / kScaleBlock;
+  const double inv_c = 1.0 / static_cast<double>(C);
   uint4_v wv[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -83,16 +122,17 @@ rmsnorm_kernel(const uint16_t *x, const uint16_t *residual, const uint16_t *__re
         if (v < vecs) hr[v] = hv[i];
       }
     }
-    float sum = 0.0f;
+    double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float a[8];
       widen8<DT>(hv[i], a);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(a[j], a[j], sum);
+      for (int j = 0; j < 8; ++j) sum = __builtin_fma(static_cast<double>(a[j]), static_cast<double>(a[j]), sum);
     }
     sum = group_sum<THREADS>(sum, slots[turn]);
-    const float r = 1.0f / __builtin_sqrtf(sum / static_cast<float>(C) + eps);
+    const double rd = inverse_root(sum * inv_c + static_cast<double>(eps));
+    const float r = static_cast<float>(rd);
     if (rstd != nullptr && threadIdx.x == 0) rstd[row] = r;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -100,32 +140,38 @@ rmsnorm_kernel(const uint16_t *x, const uint16_t *residual, const uint16_t *__re
       float a[8], w[8];
       widen8<DT>(hv[i], a);
       widen8<DT>(wv[i], w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        a[j] = a[j] * r * w[j];
-        // y is an FP32 number in every variant: not a product that v_fma_mix*
-        // rounds to half precision with it.
-        asm volatile("" : "+v"(a[j]));
-      }
-      if (y != nullptr && v < vecs) reinterpret_cast<uint4_v *>(y + row * C)[v] = round8<DT>(a);
-      if constexpr (FP8) {
-        uint32_t top = 0;
+      if (y != nullptr) {
+        float out[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const uint32_t bits = __builtin_bit_cast(uint32_t, a[j]) & 0x7fffffffu;
-          // columns behind the row: 0 * r is NaN where r is infinite
-          top = v < vecs && bits > top ? bits : top;
+          out[j] = a[j] * r * w[j];
+          // y is an FP32 number in every variant: not a product that v_fma_mix*
+          // rounds to half precision with it.
+          asm volatile("" : "+v"(out[j]));
         }
-        const float amax = __builtin_bit_cast(float, max_of_16_lanes(top));
-        float s = amax / kE4m3Max;
+        if (v < vecs) reinterpret_cast<uint4_v *>(y + row * C)[v] = round8<DT>(out);
+      }
+      if constexpr (FP8) {
+        uint32_t top = 0;  // of |weight h|, as bits: NaN above infinity above the rest
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          a[j] *= w[j];
+          const uint32_t bits = __builtin_bit_cast(uint32_t, a[j]) & 0x7fffffffu;
+          top = bits > top ? bits : top;
+        }
+        const double amax = static_cast<double>(__builtin_bit_cast(float, max_of_16_lanes(top)));
+        float s = static_cast<float>(amax * rd * (1.0 / 448.0));
         s = s < kMinScale ? kMinScale : s;  // a NaN stays
-        const float inv = 1.0f / s;
-        int lo = __builtin_amdgcn_cvt_pk_fp8_f32(a[0] * inv, a[1] * inv, 0, false);
-        lo = __builtin_amdgcn_cvt_pk_fp8_f32(a[2] * inv, a[3] * inv, lo, true);
-        int hi = __builtin_amdgcn_cvt_pk_fp8_f32(a[4] * inv, a[5] * inv, 0, false);
-        hi = __builtin_amdgcn_cvt_pk_fp8_f32(a[6] * inv, a[7] * inv, hi, true);
+        const double t = rd / static_cast<double>(s);
+        const float high = static_cast<float>(t), low = static_cast<float>(t - static_cast<double>(high));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a[j] = product_to_odd(a[j], high, low);
+        int q0 = __builtin_amdgcn_cvt_pk_fp8_f32(a[0], a[1], 0, false);
+        q0 = __builtin_amdgcn_cvt_pk_fp8_f32(a[2], a[3], q0, true);
+        int q1 = __builtin_amdgcn_cvt_pk_fp8_f32(a[4], a[5], 0, false);
+        q1 = __builtin_amdgcn_cvt_pk_fp8_f32(a[6], a[7], q1, true);
         if (v < vecs) {
-          reinterpret_cast<uint2_v *>(q + row * C)[v] = uint2_v{static_cast<uint32_t>(lo), static_cast<uint32_t>(hi)};
+          reinterpret_cast<uint2_v *>(q + row * C)[v] = uint2_v{static_cast<uint32_t>(q0), static_cast<uint32_t>(q1)};
           if ((threadIdx.x & 15) == 0) scale[row * blocks + v / 16] = s;
         }
       }
@@ -205,8 +251,9 @@ rmsnorm_grad_kernel(const uint16_t *__restrict__ dy, const uint16_t *__restrict_
 }
 
 // dweight[c] = the sum of `parts` rows of partial [parts, C]: 32 columns to a
-// workgroup, 8 threads to a column, each a run of rows.
-constexpr int kReduceCols = 32, kReduceRuns = 8;
+// workgroup, 32 threads to a column, each a run of rows whose loads are in flight
+// together (8 threads to a column: 4.4 us for 512 x 2048).
+constexpr int kReduceCols = 32, kReduceRuns = 32;
 __global__ void __launch_bounds__(kReduceCols *kReduceRuns)
 rmsnorm_reduce_kernel(const float *__restrict__ partial, float *__restrict__ dweight, int parts, int C) {
   __shared__ float sums[kReduceRuns][kReduceCols];
@@ -215,7 +262,7 @@ rmsnorm_reduce_kernel(const float *__restrict__ partial, float *__restrict__ dwe
   float sum = 0.0f;
   if (col < C) {
     const int end = (run + 1) * parts / kReduceRuns;
-#pragma unroll 8
+#pragma unroll 16
     for (int p = run * parts / kReduceRuns; p < end; ++p) sum += partial[static_cast<int64_t>(p) * C + col];
   }
   sums[run][threadIdx.x & (kReduceCols - 1)] = sum;
@@ -227,7 +274,10 @@ rmsnorm_reduce_kernel(const float *__restrict__ partial, float *__restrict__ dwe
   }
 }
 
-constexpr int kNormGrid = 2048;  // workgroups of the norm at most; each then takes several rows
+// Workgroups of the norm at most; each then takes several rows.  8192 x 4096: 46.5 us
+// with 256 threads, with 2048 workgroups and with one for each row; with 512 threads
+// 48.3 and 46.3 to 48.
+constexpr int kNormGrid = 16384;
 
 template <int DT, int THREADS, int NV>
 hipError_t launch_norm(const NormArgs &a, hipStream_t stream) {
@@ -246,10 +296,10 @@ hipError_t launch_norm_dt(const NormArgs &a, hipStream_t stream) {
   if (vecs <= 64) return launch_norm<DT, 64, 1>(a, stream);
   if (vecs <= 128) return launch_norm<DT, 128, 1>(a, stream);
   if (vecs <= 256) return launch_norm<DT, 256, 1>(a, stream);
-  if (vecs <= 512) return launch_norm<DT, 512, 1>(a, stream);
+  if (vecs <= 512) return launch_norm<DT, 256, 2>(a, stream);
   if (vecs <= 1024) return launch_norm<DT, 512, 2>(a, stream);
   if (vecs <= 2048) return launch_norm<DT, 512, 4>(a, stream);
-  return launch_norm<DT, 1024, 8>(a, stream);
+  return launch_norm<DT, 1024, 4>(a, stream);
 }
 
 template <int DT, int THREADS, int NV>
@@ -277,7 +327,7 @@ hipError_t launch_grad_dt(const NormGradArgs &a, hipStream_t stream) {
   if (vecs <= 512) return launch_grad<DT, 512, 1>(a, stream);
   if (vecs <= 1024) return launch_grad<DT, 512, 2>(a, stream);
   if (vecs <= 2048) return launch_grad<DT, 512, 4>(a, stream);
-  return launch_grad<DT, 1024, 8>(a, stream);
+  return launch_grad<DT, 1024, 4>(a, stream);
 }
 
 }  // namespace

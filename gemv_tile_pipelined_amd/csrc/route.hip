@@ -83,7 +83,6 @@ __device__ inline uint64_t wave_max(uint64_t v) {  // the upper halves, then the
   const uint32_t high = static_cast<uint32_t>(v >> 32), top = wave_max(high);
   return static_cast<uint64_t>(top) << 32 | wave_max(high == top ? static_cast<uint32_t>(v) : 0u);
 }
-__device__ inline float wave_add(float v) { return wave_sum(v); }
 __device__ inline double wave_add(double v) {
 #pragma unroll
   for (int lane = 1; lane < 64; lane <<= 1) v += __shfl_xor(v, lane);
@@ -152,15 +151,13 @@ __device__ inline void load_bias(const float *bias, int E, int lane, float *out)
   }
 }
 
-template <typename F>
-__device__ inline F exp_of(F v) {
-  if constexpr (sizeof(F) == 8) return ::exp(v);
-  else return ::expf(v);
+__device__ inline float sigmoid(float v) {
+  const float e = expf(v < 0 ? v : -v);
+  return (v < 0 ? e : 1.0f) / (1.0f + e);
 }
-template <typename F>
-__device__ inline F sigmoid(F v) {
-  const F e = exp_of(v < 0 ? v : -v);
-  return (v < 0 ? e : 1) / (1 + e);
+__device__ inline double sigmoid(double v) {
+  const double e = exp(v < 0 ? v : -v);
+  return (v < 0 ? e : 1.0) / (1.0 + e);
 }
 
 struct TopkArgs {
@@ -684,49 +681,49 @@ topk_kernel(const typename Element<DT>::type *__restrict__ logits, const float *
 //   sigmoid               dlogit_j = g_j c_j (1 - c_j)
 //   sigmoid, normalised   the same with (g_j - sum_i g_i w_i) / sum_i c_i for g_j, w = c / sum c
 // and 0 for experts not chosen.  Ids outside 0 .. E - 1 are left out.
-template <int DT, int V>
+template <int DT, int L, int V>
 __global__ void __launch_bounds__(kWaves * 64)
 topk_grad_kernel(const typename Element<DT>::type *__restrict__ logits, const int *__restrict__ ids,
                  const float *__restrict__ dweights, typename Element<DT>::type *__restrict__ dlogits, int64_t T, TopkArgs a) {
   typedef typename Element<DT>::type E_t;
+  constexpr int kTokens = 64 / L;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kWaves + wave;
-  if (t >= T) return;
+  const int part = lane / L, sub = lane & (L - 1);
+  const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWaves + wave) * kTokens;
+  if (t0 >= T) return;  // the whole wave
+  const bool there = t0 + part < T;
+  const int64_t t = there ? t0 + part : T - 1;
+  const bool softmax = a.score == GEMVTILE_SCORE_SOFTMAX;
+  const bool dense = softmax && !a.norm;
   const E_t *row = logits + t * a.E;
-  int id = lane < a.k ? ids[t * a.k + lane] : -1;
+  int id = sub < a.k ? ids[t * a.k + sub] : -1;
+  float g = sub < a.k ? a.scale * dweights[t * a.k + sub] : 0.0f;
+  float p[V];  // the logits, then their scores
+  if (dense) load_logits<DT, V>(row, a.E, sub, p);
   const bool has = id >= 0 && id < a.E;
   if (!has) id = -1;
-  const float g = has ? a.scale * dweights[t * a.k + lane] : 0.0f;
+  if (!has) g = 0.0f;
   const float own = has ? widen_logit<DT>(row[id]) : kNegInf;
-  const bool dense = a.score == GEMVTILE_SCORE_SOFTMAX && !a.norm;
-  float p[V];
   float value, dot = 0.0f;  // of the chosen expert; what every expert's score is multiplied with
   if (dense) {
-    float logit[V];
-    load_logits<DT, V>(row, a.E, lane, logit);
     float m = kNegInf;
 #pragma unroll
-    for (int i = 0; i < V; ++i) m = logit[i] > m ? logit[i] : m;
-    m = wave_max_logit(m);
-    float sum = 0.0f;
+    for (int i = 0; i < V; ++i) m = p[i] > m ? p[i] : m;
+    m = part_max<L>(m);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      p[i] = logit[i] == kNegInf ? 0.0f : expf(logit[i] - m);
-      sum += p[i];
-    }
-    sum = wave_add(sum);
+    for (int i = 0; i < V; ++i) p[i] = p[i] == kNegInf ? 0.0f : expf(p[i] - m);
+    const float sum = part_sum<L>(tree_sum<V>(p));
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
     for (int i = 0; i < V; ++i) p[i] *= inv;
     const float pj = own == kNegInf ? 0.0f : expf(own - m) * inv;
-    dot = wave_add(has ? g * pj : 0.0f);
+    dot = part_sum<L>(has ? g * pj : 0.0f);
     value = g;
   } else {
     float u, slope;  // score over what all share, and d score / d logit over the same
-    const float top = wave_max_logit(own);
-    float ref = top;
-    if (a.score == GEMVTILE_SCORE_SOFTMAX) {
+    float ref = part_max<L>(own);
+    if (softmax) {
       u = ref == kNegInf ? 0.0f : expf(own - ref);
       slope = u;
     } else {
@@ -737,9 +734,9 @@ topk_grad_kernel(const typename Element<DT>::type *__restrict__ logits, const in
     }
     if (!has) u = slope = 0.0f;
     if (a.norm) {
-      const float total = wave_add(u);
+      const float total = part_sum<L>(u);
       const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-      const float mean = wave_add(has ? g * u : 0.0f) * inv;
+      const float mean = part_sum<L>(has ? g * u : 0.0f) * inv;
       value = (g - mean) * (slope * inv);
     } else {
       value = g * slope;
@@ -750,18 +747,18 @@ topk_grad_kernel(const typename Element<DT>::type *__restrict__ logits, const in
 #pragma unroll
   for (int i = 0; i < V; ++i) out[i] = 0.0f;
   for (int j = 0; j < a.k; ++j) {
-    const int e = __builtin_amdgcn_readlane(id, j);
-    const float v = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, value), j));
+    const int e = __shfl(id, part * L + j);
+    const float v = __shfl(value, part * L + j);
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (lane * V + i == e) out[i] += v;
+    for (int i = 0; i < V; ++i) out[i] = sub * V + i == e ? out[i] + v : out[i];
   }
   if (dense) {
 #pragma unroll
     for (int i = 0; i < V; ++i) out[i] = p[i] * (out[i] - dot);
   }
+  if (!there) return;
   E_t *dst = dlogits + t * a.E;
-  const int e0 = lane * V;
+  const int e0 = sub * V;
   if (a.E % V == 0) {
     if (e0 < a.E) {
       E_t v[V];
@@ -946,22 +943,27 @@ hipError_t launch_topk_dt(const void *logits, const float *bias, int *ids, float
   if (a.E <= 512) return launch_topk_v<DT, 64, 8>(logits, bias, ids, weights, T, a, stream);
   return launch_topk_v<DT, 64, 16>(logits, bias, ids, weights, T, a, stream);
 }
-template <int DT, int V>
+template <int DT, int L, int V>
 hipError_t launch_topk_grad_v(const void *logits, const int *ids, const float *dweights, void *dlogits, int64_t T,
                               const TopkArgs &a, hipStream_t stream) {
   typedef typename Element<DT>::type E_t;
-  hipLaunchKernelGGL((topk_grad_kernel<DT, V>), dim3(static_cast<unsigned>((T + kWaves - 1) / kWaves)), dim3(kWaves * 64), 0,
+  const int64_t tokens = kWaves * (64 / L);
+  hipLaunchKernelGGL((topk_grad_kernel<DT, L, V>), dim3(static_cast<unsigned>((T + tokens - 1) / tokens)), dim3(kWaves * 64), 0,
                      stream, static_cast<const E_t *>(logits), ids, dweights, static_cast<E_t *>(dlogits), T, a);
   return hipGetLastError();
 }
 template <int DT>
 hipError_t launch_topk_grad_dt(const void *logits, const int *ids, const float *dweights, void *dlogits, int64_t T,
                                const TopkArgs &a, hipStream_t stream) {
-  if (a.E <= 64) return launch_topk_grad_v<DT, 1>(logits, ids, dweights, dlogits, T, a, stream);
-  if (a.E <= 128) return launch_topk_grad_v<DT, 2>(logits, ids, dweights, dlogits, T, a, stream);
-  if (a.E <= 256) return launch_topk_grad_v<DT, 4>(logits, ids, dweights, dlogits, T, a, stream);
-  if (a.E <= 512) return launch_topk_grad_v<DT, 8>(logits, ids, dweights, dlogits, T, a, stream);
-  return launch_topk_grad_v<DT, 16>(logits, ids, dweights, dlogits, T, a, stream);
+  if (a.k <= 16) {
+    if (a.E <= 32) return launch_topk_grad_v<DT, 16, 2>(logits, ids, dweights, dlogits, T, a, stream);
+    if (a.E <= 64) return launch_topk_grad_v<DT, 16, 4>(logits, ids, dweights, dlogits, T, a, stream);
+    if (a.E <= 128) return launch_topk_grad_v<DT, 16, 8>(logits, ids, dweights, dlogits, T, a, stream);
+    if (a.E <= 256) return launch_topk_grad_v<DT, 16, 16>(logits, ids, dweights, dlogits, T, a, stream);
+  }
+  if (a.E <= 64) return launch_topk_grad_v<DT, 64, 1>(logits, ids, dweights, dlogits, T, a, stream);
+  if (a.E <= 256) return launch_topk_grad_v<DT, 64, 4>(logits, ids, dweights, dlogits, T, a, stream);
+  return launch_topk_grad_v<DT, 64, 16>(logits, ids, dweights, dlogits, T, a, stream);
 }
 
 }  // namespace

@@ -130,7 +130,7 @@ combine_grad_kernel(const uint4_v *__restrict__ dY, const uint4_v *__restrict__ 
           dot[j] = __builtin_fmaf(g[i], a[i], dot[j]);
           o[i] = f[j] * g[i];
         }
-        dD[static_cast<int64_t>(r[j]) * vecs + v] = round8<DT>(o);
+        __builtin_nontemporal_store(round8<DT>(o), dD + static_cast<int64_t>(r[j]) * vecs + v);
       }
     }
 #pragma unroll

@@ -43,6 +43,22 @@ __device__ inline float wave_sum(float v) {
   v = dpp_add<0x143, 0xC>(v);
   return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
+template <int CTRL, int ROW_MASK = 0xF>
+__device__ inline double dpp_add(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const int low = __builtin_amdgcn_update_dpp(0, static_cast<int>(b), CTRL, ROW_MASK, 0xF, false);
+  const int high = __builtin_amdgcn_update_dpp(0, static_cast<int>(b >> 32), CTRL, ROW_MASK, 0xF, false);
+  return v + __builtin_bit_cast(double, static_cast<uint64_t>(static_cast<uint32_t>(high)) << 32 | static_cast<uint32_t>(low));
+}
+// In lane 63 only.
+__device__ inline double wave_sum_last(double v) {
+  v = dpp_add<0xB1>(v);
+  v = dpp_add<0x4E>(v);
+  v = dpp_add<0x141>(v);
+  v = dpp_add<0x140>(v);
+  v = dpp_add<0x142, 0xA>(v);
+  return dpp_add<0x143, 0xC>(v);
+}
 __device__ inline uint32_t wave_max(uint32_t v) {
   v = max_of_16_lanes(v);
   v = dpp_max<0x142, 0xA>(v);

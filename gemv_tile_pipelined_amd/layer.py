@@ -17,13 +17,26 @@ from __future__ import annotations
 
 import torch
 from torch import Tensor
+from torch._C import _cuda_getCurrentRawStream as _raw_stream
+from torch._C import _cuda_getDevice as _current_device
 
-from . import LAYER_CALLS, load_library
-from .blocks import FP8, _blocks, _first, _output, _run, _shaped
+from . import LAYER_CALLS, _check, load_library
+from .blocks import FP8, _blocks, _first, _output, _shaped
 
 __all__ = list(LAYER_CALLS) + ["alloc_rmsnorm_grad_workspace", "alloc_route_sort_workspace"]
 
 SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _run(dev, stream, call, *args):
+    s = _raw_stream(dev) if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
+    if _current_device() == dev:
+        status = call(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            status = call(*args, s)
+    if status:
+        _check(status)
 
 
 def _score(score: str) -> int:
@@ -130,7 +143,7 @@ def _rmsnorm(x, weight, residual, eps, h, y, rstd, stream, dtype, call):
 
 def rmsnorm_f16(x, weight, residual=None, eps=1e-6, h=None, y=None, rstd=None, stream=None):
     """(y, h): h = x + residual rounded to fp16 (x itself without a residual), y = h / sqrt(mean(h²) + eps) · weight.
-    x, residual, h, y [T,C], weight [C] fp16; C % 8 == 0, C <= 65536.  h may be x or residual; rstd [T] FP32 takes
+    x, residual, h, y [T,C], weight [C] fp16; C % 8 == 0, C <= 32768.  h may be x or residual; rstd [T] FP32 takes
     1 / sqrt(mean(h²) + eps) for rmsnorm_grad_f16.  Enqueued on `stream`, not synchronised."""
     return _rmsnorm(x, weight, residual, eps, h, y, rstd, stream, torch.float16, load_library().rmsnorm_f16)
 

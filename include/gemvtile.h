@@ -687,19 +687,19 @@ int gemv_fp4_bf16(const void *x, const void *W, const void *scale_W, void *y, in
  *
  *   h = x + residual, rounded once     (residual and h both NULL: h is x)
  *   r = 1 / sqrt(sum_c h^2 / C + eps)
- *   y = h * r * weight                 in FP32
+ *   y = h * r * weight
  *
  * rmsnorm_* rounds y to 16 bits.  rmsnorm_fp8_* gives q [T,C] e4m3 and scale
  * [T, ceil(C/128)] FP32 with one scale for each 128 columns of a row, as
- * quantize_fp8_rows_* does, of y in FP32 (not rounded to 16 bits first): scale =
- * max(amax / 448, 2^-80), q = e4m3(y / scale); y itself too if it is not NULL.
- * What a block with an infinity or a NaN becomes is as there.
+ * quantize_fp8_rows_* does, of y before any rounding: scale = max(amax / 448,
+ * 2^-80), q = e4m3(y / scale); y itself in 16 bits too if it is not NULL.  What a
+ * block with an infinity or a NaN becomes is as there.
  *   x, residual, weight [C], h, y, q  16-byte aligned; h may be x or residual
  *            (the stream is then updated in place), other outputs overlap nothing
  *   scale, rstd                       4-byte aligned; rstd [T] takes r for the
  *            gradient, or NULL
- *   T, C     >= 0; T <= 2^31 - 512, C <= 65536, C % 8 == 0 (16 for rmsnorm_fp8_*)
- *   eps      >= 0.  The sum of squares has to be finite in FP32.
+ *   T, C     >= 0; T <= 2^31 - 512, C <= 32768, C % 8 == 0 (16 for rmsnorm_fp8_*)
+ *   eps      >= 0; the sum of squares and r are computed in FP64
  * T == 0 or C == 0 touches nothing.
  *
  * rmsnorm_grad_f16, _bf16 -- the gradients, given dy, h, weight and rstd, and dh, the

@@ -11,7 +11,7 @@ EPS = 1e-5
 
 # rows, columns: every launch shape, ragged ends of it, more rows than workgroups
 SHAPES = [(1, 16), (3, 144), (5, 512), (2, 528), (4, 1024), (3, 1040), (7, 2048), (2, 2064), (3, 4096), (1, 4112), (2, 8192), (2, 8208),
-          (1, 16384), (2, 16400), (1, 65536), (2100, 48), (5000, 128), (4100, 272)]
+          (1, 16384), (2, 16400), (1, 32768), (2100, 48), (17000, 128), (4100, 272)]
 
 
 @pytest.fixture(scope="module")
