@@ -103,13 +103,13 @@ __device__ inline float4_t spread_rows(float v) {
 // x on their way, and waits for its own loads only.  Loads outside the matrices
 // (rows past the last, the end of a ragged K, chunks past the last) go to an offset
 // that buffer loads answer with zeros, so the number in flight is always the same.
-// The scales of the workgroup's rows are in LDS too, 16384 columns at a time.  The
-// waves' sums meet in LDS and are added in wave order.
+// The scales of the workgroup's rows are in LDS too, 16384 columns at a time (8192
+// where there are more than 32 rows).  The waves' sums meet in LDS and are added in
+// wave order.
 //
 // Places in LDS, in 16-byte pieces.  W: piece g of row n at 4 n + (g ^ (n >> 2)), so
 // that the 16 rows' pieces g are spread over all banks.  x: piece p (of 16) of row m
 // at 16 m + (p ^ (m & 15)), likewise.
-constexpr int kSegmentChunks = 128;
 template <int DT, int XQ, int NT, int WAVES, int DEPTH>
 __global__ void __launch_bounds__(WAVES * 64)
 gemv_fp4_kernel(const uint16_t *__restrict__ x, const uint8_t *__restrict__ W, const uint8_t *__restrict__ sW,
@@ -118,10 +118,11 @@ gemv_fp4_kernel(const uint16_t *__restrict__ x, const uint8_t *__restrict__ W, c
   constexpr int kChains = NT * MT == 1 ? 2 : 1;  // of MFMAs that wait for one another
   constexpr int kSums = NT * MT * 256;
   constexpr int kLoads = NT + XQ;  // of a chunk, 1 KiB each
-  constexpr int kScaleBytes = NT * 16 * kSegmentChunks * 4;
+  constexpr int kSegment = NT <= 2 ? 128 : 64;    // chunks whose scales are in LDS
+  constexpr int kScaleRow = kSegment * 4 + 16;  // bytes for a row's scales and their place within 16
   static_assert(kSums * 4 <= DEPTH * kLoads * 1024, "the sums fit where the ring was");
   __shared__ __attribute__((aligned(16))) char ring[WAVES * DEPTH * kLoads * 1024];
-  __shared__ __attribute__((aligned(16))) uint8_t scales[kScaleBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t scales[NT * 16 * kScaleRow];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, i16 = lane & 15;
@@ -219,29 +220,33 @@ gemv_fp4_kernel(const uint16_t *__restrict__ x, const uint8_t *__restrict__ W, c
 #pragma unroll
   for (int d = 0; d < DEPTH; ++d) issue(wave + d * WAVES, d);
   int chunk = wave, stage = 0;
-  for (int first = 0; first < chunks; first += kSegmentChunks) {
-    // The scales of the segment: the workgroup's rows one after another.
-    const int b0 = first * 4, nb = row_blocks - b0 < kSegmentChunks * 4 ? row_blocks - b0 : kSegmentChunks * 4;
+  for (int first = 0; first < chunks; first += kSegment) {
+    // The scales of the segment.  A row's keep their place within 16 bytes, so that
+    // whole pieces are moved wherever it begins.
+    const int b0 = first * 4, nb = row_blocks - b0 < kSegment * 4 ? row_blocks - b0 : kSegment * 4;
     const uint8_t *src = sW + static_cast<int64_t>(n0) * row_blocks + b0;
     if (first > 0) __syncthreads();
-    const int bytes = rows * nb;
-    if (nb == row_blocks && (reinterpret_cast<uintptr_t>(src) & 15) == 0) {
-      // all of K: the rows' scales follow one another in memory too
-      for (int i = threadIdx.x * 16; i < bytes; i += WAVES * 64 * 16) {
-        if (i + 16 <= bytes) {
-          *reinterpret_cast<uint4_v *>(scales + i) = *reinterpret_cast<const uint4_v *>(src + i);
-        } else {
-          for (int j = i; j < bytes; ++j) scales[j] = src[j];
-        }
-      }
-    } else {
-      for (int i = threadIdx.x; i < bytes; i += WAVES * 64) {
-        const int r = i / nb;
-        scales[i] = src[static_cast<int64_t>(r) * row_blocks + (i - r * nb)];
+    const int pieces = (nb + 30) / 16;
+    for (int i = threadIdx.x; i < rows * pieces; i += WAVES * 64) {
+      const int r = i / pieces, at = (i - r * pieces) * 16;
+      const uint8_t *row = src + static_cast<int64_t>(r) * row_blocks;
+      const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15);
+      uint8_t *to = scales + r * kScaleRow;
+      if (at >= skew && at + 16 <= skew + nb) {
+        *reinterpret_cast<uint4_v *>(to + at) = *reinterpret_cast<const uint4_v *>(row + (at - skew));
+      } else {
+        for (int j = at < skew ? skew : at; j < skew + nb && j < at + 16; ++j) to[j] = row[j - skew];
       }
     }
     __syncthreads();
-    const int past = first + kSegmentChunks < chunks ? first + kSegmentChunks : chunks;
+    const uint8_t *mine_s[NT];  // this lane's rows, by block
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int r = t * 16 + i16;
+      const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(src + static_cast<int64_t>(r) * row_blocks) & 15);
+      mine_s[t] = scales + r * kScaleRow + skew - b0;
+    }
+    const int past = first + kSegment < chunks ? first + kSegment : chunks;
     for (; chunk < past; chunk += WAVES) {
       // Lanes behind the last row or the end of K: zeros of W, any scale but NaN.
       const int block = chunk * 4 + g;
@@ -250,7 +255,7 @@ gemv_fp4_kernel(const uint16_t *__restrict__ x, const uint8_t *__restrict__ W, c
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const int r = t * 16 + i16;
-        s[t] = r < rows && block < row_blocks ? scales[r * nb + block - b0] : 127u;
+        s[t] = r < rows && block < row_blocks ? mine_s[t][block] : 127u;
         fits &= scale_fits<DT>(s[t]);
       }
       wait_vmcnt<(DEPTH - 1) * kLoads>();
@@ -350,43 +355,48 @@ hipError_t launch_gemv(const void *x, const void *W, const void *sW, void *y, in
   return hipGetLastError();
 }
 
-// Rows of W for a workgroup: 16 as long as that leaves compute units idle or gives
-// each only one or two workgroups, more beyond, as every workgroup reads all of x
-// (figures: us, 16 / 32 / 64 rows).
-//   up to 4 rows of x   4096x14336 8.3 / 11.4, 8192x4096 5.9 / 6.0, 14336x4096 10.3 / 8.4, 28672x8192 28.7 / 27.1
-//   up to 16            4096x4096 5.3 / 5.8 / 7.5, 8192x8192 15.0 / 12.8 / 15.8, 28672x4096 28.3 / 20.7 / 19.4
-//   up to 32            4096x14336 20.4 / 23.4 / 32.6, 8195x4128 16.2 / 11.8 / 11.2, 28672x4096 46.3 / 31.8 / 24.7
-//   up to 64            4096x4096 10.6 / 13.0 / 19.1, 8192x8192 35.6 / 26.0 / 35.7, 28672x4096 70.6 / 55.3 / 41.6
-// The ring is as deep as the LDS holds with one or two workgroups to a CU; with few
-// rows of x two stages do unless a wave has more than four chunks (4096x14336 9.5 us
-// with two, 8.3 with three; 4096x4096 4.2 and 4.5).
+// Blocks of 16 rows of W for a workgroup: every workgroup reads all of x, at the 25
+// bytes a cycle that a CU gets from its L2, so as many as it takes for one round of
+// the compute units, up to 4 (us with 1 / 2 / 3 / 4 blocks):
+//   12 rows of x  5000x4096 6.6 / 5.9 / - / -, 8195x4128 10.1 / 8.4 / 7.9 / 8.9, 28672x4096 - / 19.6 / 19.3 / 19.0
+//   27            8192x8192 22.1 / 15.4 / 17.5 / 21.0, 8195x4128 15.5 / 11.4 / 10.0 / 11.2, 28672x4096 - / 26.7 / 28.3 / 24.3
+//   64            4096x14336 34.7 / 47.9 / - / -, 8192x8192 35.7 / 26.3 / 30.7 / 36.9, 28672x4096 - / 56.3 / 52.2 / 43.6
+// With up to 8 rows of x, which take little LDS and time, several workgroups share a
+// CU: no more than 3, and 2 where that does not make one round (1 row: 8195x4128 7.7 /
+// 7.5 / 6.9 / 7.7, 14336x4096 10.2 / 8.3 / - / 9.7, 28672x4096 17.8 / 14.8 / 15.9 / 17.3).
+// Waves and depth are what the LDS holds; 8 waves of one stage are ahead of 4 of two
+// except with the most registers.  One row's ring has a third stage where a wave has
+// more than four chunks (4096x14336 9.5 us with two, 8.3 with three; 4096x4096 4.2 and
+// 4.5).
+template <int DT, int XQ, int W1, int D1, int W2, int W3, int W4, int D>
+hipError_t launch_blocks(int blocks, const void *x, const void *W, const void *sW, void *y, int M, int N, int K,
+                         hipStream_t stream) {
+  if (blocks <= 1) return launch_gemv<DT, XQ, 1, W1, D1>(x, W, sW, y, M, N, K, stream);
+  if (blocks == 2) return launch_gemv<DT, XQ, 2, W2, D>(x, W, sW, y, M, N, K, stream);
+  if constexpr (XQ <= 2) {
+    return launch_gemv<DT, XQ, 3, W3, D>(x, W, sW, y, M, N, K, stream);
+  } else {
+    if (blocks == 3) return launch_gemv<DT, XQ, 3, W3, D>(x, W, sW, y, M, N, K, stream);
+    return launch_gemv<DT, XQ, 4, W4, D>(x, W, sW, y, M, N, K, stream);
+  }
+}
+
 template <int DT>
 hipError_t launch_gemv_dt(const void *x, const void *W, const void *sW, void *y, int M, int N, int K, int cus,
                           hipStream_t stream) {
   const int tiles = (N + 15) / 16;
-  const bool deep = K > 4 * 8 * kFp4Chunk;
-  if (M <= 8) {
-    if (M <= 4) {
-      if (tiles > 2 * cus) return launch_gemv<DT, 1, 2, 8, 2>(x, W, sW, y, M, N, K, stream);
-      if (deep) return launch_gemv<DT, 1, 1, 8, 3>(x, W, sW, y, M, N, K, stream);
-      return launch_gemv<DT, 1, 1, 8, 2>(x, W, sW, y, M, N, K, stream);
-    }
-    if (tiles > 2 * cus) return launch_gemv<DT, 2, 2, 8, 2>(x, W, sW, y, M, N, K, stream);
-    return launch_gemv<DT, 2, 1, 8, 2>(x, W, sW, y, M, N, K, stream);
+  const int round = (tiles + cus - 1) / cus;  // blocks for one round of the compute units
+  const int few = round <= 3 ? round : 2;
+  if (M <= 4) {
+    if (few == 1 && K > 4 * 8 * kFp4Chunk) return launch_gemv<DT, 1, 1, 8, 3>(x, W, sW, y, M, N, K, stream);
+    return launch_blocks<DT, 1, 8, 2, 8, 8, 8, 2>(few, x, W, sW, y, M, N, K, stream);
   }
-  if (M <= 16) {
-    if (tiles <= cus) return launch_gemv<DT, 4, 1, 8, 2>(x, W, sW, y, M, N, K, stream);
-    if (tiles < 4 * cus) return launch_gemv<DT, 4, 2, 8, 1>(x, W, sW, y, M, N, K, stream);
-    return launch_gemv<DT, 4, 4, 8, 1>(x, W, sW, y, M, N, K, stream);
-  }
-  if (M <= 32) {
-    if (tiles <= cus) return launch_gemv<DT, 8, 1, 8, 1>(x, W, sW, y, M, N, K, stream);
-    if (tiles < 2 * cus) return launch_gemv<DT, 8, 2, 4, 1>(x, W, sW, y, M, N, K, stream);
-    return launch_gemv<DT, 8, 4, 8, 1>(x, W, sW, y, M, N, K, stream);
-  }
-  if (tiles <= cus) return launch_gemv<DT, 16, 1, 8, 1>(x, W, sW, y, M, N, K, stream);
-  if (tiles < 4 * cus) return launch_gemv<DT, 16, 2, 4, 1>(x, W, sW, y, M, N, K, stream);
-  return launch_gemv<DT, 16, 4, 4, 1>(x, W, sW, y, M, N, K, stream);
+  if (M <= 8) return launch_blocks<DT, 2, 8, 2, 8, 8, 8, 2>(few, x, W, sW, y, M, N, K, stream);
+  if (M <= 16) return launch_blocks<DT, 4, 8, 2, 8, 8, 8, 1>(round, x, W, sW, y, M, N, K, stream);
+  if (M <= 24) return launch_blocks<DT, 6, 8, 1, 8, 8, 8, 1>(round, x, W, sW, y, M, N, K, stream);
+  if (M <= 32) return launch_blocks<DT, 8, 8, 1, 8, 8, 8, 1>(round, x, W, sW, y, M, N, K, stream);
+  if (M <= 48) return launch_blocks<DT, 12, 8, 1, 8, 8, 4, 1>(round, x, W, sW, y, M, N, K, stream);
+  return launch_blocks<DT, 16, 8, 1, 4, 4, 4, 1>(round, x, W, sW, y, M, N, K, stream);
 }
 
 }  // namespace

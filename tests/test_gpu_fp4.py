@@ -85,9 +85,9 @@ def _weights(r, N, K, low=110, high=130):
 SHAPES = [(1, 1, 32), (1, 16, 128), (1, 17, 160), (2, 15, 64), (3, 33, 96), (4, 300, 1024), (5, 40, 4128), (15, 31, 224), (16, 100, 512),
           (17, 47, 2080), (27, 515, 1056), (32, 64, 256), (33, 65, 1056), (48, 70, 320), (64, 130, 2080), (65, 50, 256), (200, 33, 160),
           (1, 1000, 14336), (1, 5000, 96), (1, 9000, 544), (7, 8200, 288), (40, 4200, 160),
-          # each number of rows of a workgroup, and scales past one segment of 16384 columns
-          (12, 4100, 160), (16, 16400, 96), (20, 4128, 224), (32, 8208, 64), (64, 16390, 96), (2, 20, 16416), (1, 35, 33024),
-          (13, 33, 20000), (70, 18, 16512)]
+          # each number of rows of x and of W that a workgroup has, and scales past one segment of 8192 or 16384 columns
+          *((M, N, 160) for M in (1, 5, 9, 20, 32, 40, 64) for N in (4100, 8200, 12290)), (3, 16400, 64), (12, 16400, 64),
+          (2, 20, 16416), (1, 35, 33024), (13, 33, 20000), (70, 18, 16512), (18, 8210, 8224)]
 
 
 @FMT
