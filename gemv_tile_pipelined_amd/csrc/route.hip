@@ -170,7 +170,7 @@ struct TopkArgs {
 // holds E numbers of the wave's own.  Few tokens come here, so the code is never in
 // the instruction cache and its length is what it costs: loops, nothing unrolled.
 template <int DT>
-__device__ __attribute__((noinline)) int choose_exactly(const typename Element<DT>::type *row, const float *bias, TopkArgs a,
+__device__ __attribute__((always_inline)) inline int choose_exactly(const typename Element<DT>::type *row, const float *bias, TopkArgs a,
                                                         double *buf) {
   typedef KeyOf<double> Keys;
   const int lane = threadIdx.x & 63;
