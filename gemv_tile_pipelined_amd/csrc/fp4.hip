@@ -162,18 +162,20 @@ gemv_fp4_kernel(const uint16_t *__restrict__ x, const uint8_t *__restrict__ W, c
 #pragma unroll
       for (int r = 0; r < kChains; ++r) acc[a][b][r] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-  // Where this lane reads: W's piece g of row i16, x's pieces of row i16 (of one
-  // that is there where a block has fewer: what it gives is not stored).
+  // Where this lane reads: W's piece g of row i16 of a block, x's pieces of row i16
+  // (of the last one that has a place where there are fewer: what it gives is not
+  // stored).
   const uint32_t wread = (4 * i16 + (g ^ (i16 >> 2))) * 16;
-  const uint32_t xrow = XQ >= 4 ? i16 : i16 & (XQ * 4 - 1);
   auto read = [&](const char *stage, uint4_v (&w)[NT], uint4_v (&xv)[MT][4]) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) w[t] = *reinterpret_cast<const uint4_v *>(stage + t * 1024 + wread);
 #pragma unroll
-    for (int u = 0; u < MT; ++u)
+    for (int u = 0; u < MT; ++u) {
+      const int row = u * 16 + i16 < XQ * 4 ? u * 16 + i16 : XQ * 4 - 1;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        xv[u][i] = *reinterpret_cast<const uint4_v *>(stage + NT * 1024 + (u * 256 + xrow * 16 + ((4 * g + i) ^ xrow)) * 16);
+        xv[u][i] = *reinterpret_cast<const uint4_v *>(stage + NT * 1024 + (row * 16 + ((4 * g + i) ^ (row & 15))) * 16);
+    }
   };
   auto multiply = [&](const uint4_v (&w)[NT], const uint4_v (&xv)[MT][4], const uint32_t (&s)[NT]) {
 #pragma unroll
@@ -355,48 +357,80 @@ hipError_t launch_gemv(const void *x, const void *W, const void *sW, void *y, in
   return hipGetLastError();
 }
 
-// Blocks of 16 rows of W for a workgroup: every workgroup reads all of x, at the 25
-// bytes a cycle that a CU gets from its L2, so as many as it takes for one round of
-// the compute units, up to 4 (us with 1 / 2 / 3 / 4 blocks):
-//   12 rows of x  5000x4096 6.6 / 5.9 / - / -, 8195x4128 10.1 / 8.4 / 7.9 / 8.9, 28672x4096 - / 19.6 / 19.3 / 19.0
-//   27            8192x8192 22.1 / 15.4 / 17.5 / 21.0, 8195x4128 15.5 / 11.4 / 10.0 / 11.2, 28672x4096 - / 26.7 / 28.3 / 24.3
-//   64            4096x14336 34.7 / 47.9 / - / -, 8192x8192 35.7 / 26.3 / 30.7 / 36.9, 28672x4096 - / 56.3 / 52.2 / 43.6
-// With up to 8 rows of x, which take little LDS and time, several workgroups share a
-// CU: no more than 3, and 2 where that does not make one round (1 row: 8195x4128 7.7 /
-// 7.5 / 6.9 / 7.7, 14336x4096 10.2 / 8.3 / - / 9.7, 28672x4096 17.8 / 14.8 / 15.9 / 17.3).
-// Waves and depth are what the LDS holds; 8 waves of one stage are ahead of 4 of two
-// except with the most registers.  One row's ring has a third stage where a wave has
-// more than four chunks (4096x14336 9.5 us with two, 8.3 with three; 4096x4096 4.2 and
-// 4.5).
-template <int DT, int XQ, int W1, int D1, int W2, int W3, int W4, int D>
-hipError_t launch_blocks(int blocks, const void *x, const void *W, const void *sW, void *y, int M, int N, int K,
-                         hipStream_t stream) {
-  if (blocks <= 1) return launch_gemv<DT, XQ, 1, W1, D1>(x, W, sW, y, M, N, K, stream);
-  if (blocks == 2) return launch_gemv<DT, XQ, 2, W2, D>(x, W, sW, y, M, N, K, stream);
-  if constexpr (XQ <= 2) {
-    return launch_gemv<DT, XQ, 3, W3, D>(x, W, sW, y, M, N, K, stream);
-  } else {
-    if (blocks == 3) return launch_gemv<DT, XQ, 3, W3, D>(x, W, sW, y, M, N, K, stream);
-    return launch_gemv<DT, XQ, 4, W4, D>(x, W, sW, y, M, N, K, stream);
+// Rows of x (4 XQ) and of W (16 NT) for a workgroup.  A CU gets 25 bytes a cycle from
+// its L2, and a workgroup needs 2 bytes of each of its rows of x and 1/2 of each of W
+// for a column, whose unpacking takes about as long again: of the pairs, the one with
+// the least rounds * (2 rows of x + 16 NT), of equal ones that with more rows of x.
+// Fewer rows of x than there are make several workgroups read the same W, from L2 or
+// beyond.  us with what is chosen / with all rows of x and the W of one round:
+//   27 rows of x  1024x4096 4.4 / 6.0, 4096x14336 16.5 / 21.6, 8195x4128 10.6 / 10.6, 8192x8192 15.3 / 15.3
+//   64            1024x4096 5.1 / 9.5, 4096x14336 22.9 / 34.7, 8195x4128 20.4 / 21.2, 8192x8192 20.3 / 26.7
+// Eight waves and the depth that the LDS holds are ahead of fewer waves and more depth.
+struct GemvShape {
+  int xq, nt;
+};
+GemvShape gemv_shape(int64_t M, int64_t tiles, int64_t cus) {
+  GemvShape best = {2, 1};
+  int64_t least = INT64_MAX;
+  for (const int xq : {2, 4, 6, 8, 12}) {
+    for (int nt = 1; nt <= (xq == 2 ? 2 : 4); ++nt) {
+      const int64_t groups = (tiles + nt - 1) / nt * ((M + 4 * xq - 1) / (4 * xq));
+      const int64_t cost = (groups + cus - 1) / cus * (2 * (M < 4 * xq ? M : 4 * xq) + 16 * nt);
+      if (cost < least || (cost == least && xq > best.xq)) {
+        least = cost;
+        best = {xq, nt};
+      }
+    }
+    if (4 * xq >= M) break;
   }
+  return best;
 }
 
 template <int DT>
 hipError_t launch_gemv_dt(const void *x, const void *W, const void *sW, void *y, int M, int N, int K, int cus,
                           hipStream_t stream) {
   const int tiles = (N + 15) / 16;
-  const int round = (tiles + cus - 1) / cus;  // blocks for one round of the compute units
-  const int few = round <= 3 ? round : 2;
-  if (M <= 4) {
-    if (few == 1 && K > 4 * 8 * kFp4Chunk) return launch_gemv<DT, 1, 1, 8, 3>(x, W, sW, y, M, N, K, stream);
-    return launch_blocks<DT, 1, 8, 2, 8, 8, 8, 2>(few, x, W, sW, y, M, N, K, stream);
+  if (M <= 8) {
+    // Several workgroups of few rows of x share a CU: no more than 3 blocks of W, and 2
+    // where that does not make one round (1 row: 8195x4128 7.7 us with 1, 7.5 with 2, 6.9
+    // with 3; 14336x4096 10.2, 8.3, - and 9.7 with 4; 28672x4096 17.8, 14.8, 15.9, 17.3).
+    const int round = (tiles + cus - 1) / cus;
+    const int nt = round <= 3 ? round : 2;
+    if (M <= 4) {
+      // A third stage where a wave has more than four chunks (4096x14336 9.5 us with two,
+      // 8.3 with three; 4096x4096 4.2 and 4.5).
+      if (nt == 1 && K > 4 * 8 * kFp4Chunk) return launch_gemv<DT, 1, 1, 8, 3>(x, W, sW, y, M, N, K, stream);
+      if (nt == 1) return launch_gemv<DT, 1, 1, 8, 2>(x, W, sW, y, M, N, K, stream);
+      if (nt == 2) return launch_gemv<DT, 1, 2, 8, 2>(x, W, sW, y, M, N, K, stream);
+      return launch_gemv<DT, 1, 3, 8, 2>(x, W, sW, y, M, N, K, stream);
+    }
+    if (nt == 1) return launch_gemv<DT, 2, 1, 8, 2>(x, W, sW, y, M, N, K, stream);
+    // One stage lets three workgroups share a CU (6 rows: 14336x4096 11.1 us with two, 9.0
+    // with one; 8192x8192, one round, 10.8 and 11.9).
+    if (nt == 2 && round > 2) return launch_gemv<DT, 2, 2, 8, 1>(x, W, sW, y, M, N, K, stream);
+    if (nt == 2) return launch_gemv<DT, 2, 2, 8, 2>(x, W, sW, y, M, N, K, stream);
+    return launch_gemv<DT, 2, 3, 8, 1>(x, W, sW, y, M, N, K, stream);
   }
-  if (M <= 8) return launch_blocks<DT, 2, 8, 2, 8, 8, 8, 2>(few, x, W, sW, y, M, N, K, stream);
-  if (M <= 16) return launch_blocks<DT, 4, 8, 2, 8, 8, 8, 1>(round, x, W, sW, y, M, N, K, stream);
-  if (M <= 24) return launch_blocks<DT, 6, 8, 1, 8, 8, 8, 1>(round, x, W, sW, y, M, N, K, stream);
-  if (M <= 32) return launch_blocks<DT, 8, 8, 1, 8, 8, 8, 1>(round, x, W, sW, y, M, N, K, stream);
-  if (M <= 48) return launch_blocks<DT, 12, 8, 1, 8, 8, 4, 1>(round, x, W, sW, y, M, N, K, stream);
-  return launch_blocks<DT, 16, 8, 1, 4, 4, 4, 1>(round, x, W, sW, y, M, N, K, stream);
+  const GemvShape s = gemv_shape(M, tiles, cus);
+  switch (s.xq * 8 + s.nt) {
+    case 2 * 8 + 1: return launch_gemv<DT, 2, 1, 8, 2>(x, W, sW, y, M, N, K, stream);
+    case 2 * 8 + 2: return launch_gemv<DT, 2, 2, 8, 2>(x, W, sW, y, M, N, K, stream);
+    case 4 * 8 + 1: return launch_gemv<DT, 4, 1, 8, 2>(x, W, sW, y, M, N, K, stream);
+    case 4 * 8 + 2: return launch_gemv<DT, 4, 2, 8, 2>(x, W, sW, y, M, N, K, stream);
+    case 4 * 8 + 3: return launch_gemv<DT, 4, 3, 8, 1>(x, W, sW, y, M, N, K, stream);
+    case 4 * 8 + 4: return launch_gemv<DT, 4, 4, 8, 1>(x, W, sW, y, M, N, K, stream);
+    case 6 * 8 + 1: return launch_gemv<DT, 6, 1, 8, 2>(x, W, sW, y, M, N, K, stream);
+    case 6 * 8 + 2: return launch_gemv<DT, 6, 2, 8, 1>(x, W, sW, y, M, N, K, stream);
+    case 6 * 8 + 3: return launch_gemv<DT, 6, 3, 8, 1>(x, W, sW, y, M, N, K, stream);
+    case 6 * 8 + 4: return launch_gemv<DT, 6, 4, 8, 1>(x, W, sW, y, M, N, K, stream);
+    case 8 * 8 + 1: return launch_gemv<DT, 8, 1, 8, 1>(x, W, sW, y, M, N, K, stream);
+    case 8 * 8 + 2: return launch_gemv<DT, 8, 2, 8, 1>(x, W, sW, y, M, N, K, stream);
+    case 8 * 8 + 3: return launch_gemv<DT, 8, 3, 8, 1>(x, W, sW, y, M, N, K, stream);
+    case 8 * 8 + 4: return launch_gemv<DT, 8, 4, 8, 1>(x, W, sW, y, M, N, K, stream);
+    case 12 * 8 + 2: return launch_gemv<DT, 12, 2, 8, 1>(x, W, sW, y, M, N, K, stream);
+    case 12 * 8 + 3: return launch_gemv<DT, 12, 3, 8, 1>(x, W, sW, y, M, N, K, stream);
+    default: return launch_gemv<DT, 12, 4, 4, 1>(x, W, sW, y, M, N, K, stream);
+  }
 }
 
 }  // namespace

@@ -87,6 +87,7 @@ SHAPES = [(1, 1, 32), (1, 16, 128), (1, 17, 160), (2, 15, 64), (3, 33, 96), (4, 
           (1, 1000, 14336), (1, 5000, 96), (1, 9000, 544), (7, 8200, 288), (40, 4200, 160),
           # each number of rows of x and of W that a workgroup has, and scales past one segment of 8192 or 16384 columns
           *((M, N, 160) for M in (1, 5, 9, 20, 32, 40, 64) for N in (4100, 8200, 12290)), (3, 16400, 64), (12, 16400, 64),
+          (17, 2080, 96), (9, 2080, 96), (17, 2752, 64), (81, 1360, 96), (25, 6160, 64), (33, 6160, 64), (73, 3090, 64),
           (2, 20, 16416), (1, 35, 33024), (13, 33, 20000), (70, 18, 16512), (18, 8210, 8224)]
 
 
