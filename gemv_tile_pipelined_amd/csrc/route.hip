@@ -134,7 +134,7 @@ __device__ inline void load_logits(const typename Element<DT>::type *row, int E,
   }
 }
 
-// The lane's V biases, 0 behind the last expert.
+// The lane's V biases, -inf behind the last expert.
 template <int V>
 __device__ inline void load_bias(const float *bias, int E, int lane, float *out) {
   const int e0 = lane * V;
@@ -143,11 +143,11 @@ __device__ inline void load_bias(const float *bias, int E, int lane, float *out)
       __builtin_memcpy(out, __builtin_assume_aligned(bias + e0, V % 4 == 0 ? 16 : 4), V * sizeof(float));
     } else {
 #pragma unroll
-      for (int i = 0; i < V; ++i) out[i] = 0.0f;
+      for (int i = 0; i < V; ++i) out[i] = kNegInf;
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) out[i] = e0 + i < E ? bias[e0 + i] : 0.0f;
+    for (int i = 0; i < V; ++i) out[i] = e0 + i < E ? bias[e0 + i] : kNegInf;
   }
 }
 
@@ -325,6 +325,9 @@ __device__ inline Best merge(Best a, float first, float second) {
   return {__builtin_fmaxf(a.first, first),
           __builtin_fmaxf(__builtin_fminf(a.first, first), __builtin_fmaxf(a.second, second))};
 }
+__device__ inline Best merge(Best a, float v) {
+  return {__builtin_fmaxf(a.first, v), __builtin_amdgcn_fmed3f(a.first, a.second, v)};
+}
 
 constexpr int kMaxGroups = 64;
 template <int L, int V>
@@ -400,10 +403,7 @@ topk_kernel(const typename Element<DT>::type *__restrict__ logits, const float *
     if (lanes * V == size && (lanes & (lanes - 1)) == 0) {
       Best b = {kNegInf, kNegInf};
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float v = sub * V + i < a.E ? value[i] : kNegInf;
-        b = merge(b, v == v ? v : kNegInf, kNegInf);
-      }
+      for (int i = 0; i < V; ++i) b = merge(b, value[i]);  // with a NaN the token is done again
       if (lanes >= 2) b = merge(b, dpp_move<0xB1>(b.first), dpp_move<0xB1>(b.second));
       if (lanes >= 4) b = merge(b, dpp_move<0x4E>(b.first), dpp_move<0x4E>(b.second));
       if (lanes >= 8) b = merge(b, dpp_move<0x141>(b.first), dpp_move<0x141>(b.second));
@@ -471,10 +471,7 @@ topk_kernel(const typename Element<DT>::type *__restrict__ logits, const float *
       __builtin_amdgcn_wave_barrier();
       for (int o = sub; o < a.groups; o += L) {
         Best b = {kNegInf, kNegInf};
-        for (int i = 0; i < size; ++i) {
-          const float v = s.value[part][o * size + i];
-          b = merge(b, v == v ? v : kNegInf, kNegInf);
-        }
+        for (int i = 0; i < size; ++i) b = merge(b, s.value[part][o * size + i]);
         s.group[part][o] = sums ? b.first + b.second : b.first;
         s.error[part][o] = group_error(wrong, b.first, sums ? b.second : 0.0f);
       }
@@ -523,39 +520,35 @@ topk_kernel(const typename Element<DT>::type *__restrict__ logits, const float *
   uint32_t key[V];
   float step = 0.0f;
   if (rounded) {
-    // 16 below the largest choice, or less if there is less, in equal steps.
+    // Equal steps over 2 below the largest choice (16 of logits); further down all are
+    // alike, and settled as whatever is too near is.
     constexpr uint32_t kSteps = (1u << (31 - kIndexBits < 23 ? 31 - kIndexBits : 23)) - 4;  // FP32 counts them all
-    float high = kNegInf, low = __builtin_inff();
+    float high = kNegInf;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const bool in = sub * V + i < a.E && !((dropped >> i) & 1) && value[i] > kNegInf;
-      high = in ? __builtin_fmaxf(high, value[i]) : high;
-      low = in ? __builtin_fminf(low, value[i]) : low;
-    }
+    for (int i = 0; i < V; ++i) high = __builtin_fmaxf(high, value[i]);
     high = part_max<L>(high);
-    low = -part_max<L>(-low);
-    float range = high - low;
-    range = range < 16.0f ? range : 16.0f;
-    range = range > 1e-30f ? range : 1e-30f;
     again |= !(__builtin_fabsf(high) < __builtin_inff());
-    const float base = high - range, scale = static_cast<float>(kSteps) / range;
+    const float range = biased ? 2.0f : 16.0f, scale = static_cast<float>(kSteps) / range;
+    const float base = 1.0f - (high - range) * scale;
     step = 2.0f * range / static_cast<float>(kSteps);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float q = __builtin_fminf(__builtin_fmaxf((value[i] - base) * scale, 0.0f), static_cast<float>(kSteps));
-      key[i] = static_cast<uint32_t>(q);
-    }
+    for (int i = 0; i < V; ++i)
+      key[i] = static_cast<uint32_t>(
+          __builtin_amdgcn_fmed3f(__builtin_fmaf(value[i], scale, base), 1.0f, static_cast<float>(kSteps + 1)));
   } else {
     // All bits that differ among 16-bit numbers.
     constexpr int kShift = DT == kBF16 ? 16 : 13;
 #pragma unroll
-    for (int i = 0; i < V; ++i) key[i] = KeyOf<float>::of(value[i]) >> kShift;
+    for (int i = 0; i < V; ++i) key[i] = (KeyOf<float>::of(value[i]) >> kShift) + 1;
   }
+  {
+    // Bits of the lane's experts that can be chosen.
+    const int count = a.E - sub * V < 0 ? 0 : a.E - sub * V < V ? a.E - sub * V : V;
+    const uint32_t open = ((1u << count) - 1u) & ~dropped;
+    const uint32_t number = static_cast<uint32_t>(L * V - V - sub * V);
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = sub * V + i;
-    key[i] = (key[i] + 1) << kIndexBits | static_cast<uint32_t>(L * V - 1 - e);
-    if (e >= a.E || ((dropped >> i) & 1)) key[i] = 0;
+    for (int i = 0; i < V; ++i)
+      key[i] = (key[i] << kIndexBits | (number + (V - 1 - i))) & static_cast<uint32_t>(static_cast<int>(open << (31 - i)) >> 31);
   }
 
   // ---- rounds: lane j gets the j-th largest key, two more than are wanted where keys are rounded
@@ -984,10 +977,14 @@ hipError_t launch_route_topk_grad(int dtype, const void *logits, const int *ids,
   return launch_topk_grad_dt<kF32>(logits, ids, dweights, dlogits, r.T, a, stream);
 }
 
+// One workgroup (and launch) for as many slots as it sorts sooner than two launches do
+// (E = 256, us with one / two: 1024 slots 4.6 / 6.7, 4096 8.9 / 7.7), then 512 slots to a
+// workgroup, up to 128 of them, as each reads all the others' counts (131072 slots: 10.4
+// us with 64, 9.9 with 128, 11.2 with 256).
 int route_sort_blocks(int64_t slots) {
-  if (slots <= 4096) return 1;
-  const int64_t b = (slots + 2047) / 2048;
-  return static_cast<int>(b < 64 ? b : 64);
+  if (slots <= 2048) return 1;
+  const int64_t b = (slots + 511) / 512;
+  return static_cast<int>(b < 128 ? b : 128);
 }
 
 hipError_t launch_route_sort(const int *ids, int *offsets, int *pos, int *hist, int64_t slots, int E, hipStream_t stream) {

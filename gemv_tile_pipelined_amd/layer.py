@@ -294,7 +294,7 @@ def alloc_route_sort_workspace(T, E, k, device):
 def route_sort(ids, E, offsets=None, pos=None, workspace=None, stream=None):
     """(offsets, pos): the slots of ids [T,k] int32 sorted by expert, in their order within one.  offsets [E+1] int32 as
     gemm_grouped_* take it, pos [T,k] int32 the row of each slot; -1 for a slot whose id is outside 0 .. E - 1.
-    `workspace`: a device tensor (alloc_route_sort_workspace makes one) owned by the caller, needed above 4096 slots;
+    `workspace`: a device tensor (alloc_route_sort_workspace makes one) owned by the caller, needed above 2048 slots;
     without one the call then raises GemvTileError."""
     dev = _first(ids, "ids", torch.int32, 2)
     T, k = ids.shape

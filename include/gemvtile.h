@@ -752,9 +752,9 @@ enum gemvtile_score {
  *                    scores if norm is 1
  *
  * Ids are those of choices computed in 64 bits, whatever the logits' type.  A logit
- * of -inf is an expert with score 0, chosen after all others; where every score
- * that is divided by is 0 (all logits -inf) the weights are 0.  A NaN choice ranks
- * below all others.  With softmax a NaN or +inf among a token's logits makes its
+ * of -inf is an expert with score 0, chosen after all others unless a bias lifts it (a
+ * bias of -inf does not); where every score that is divided by is 0 (all logits -inf)
+ * the weights are 0.  A NaN choice ranks below all others.  With softmax a NaN or +inf among a token's logits makes its
  * weights NaN (and with a bias, or sums of two, every choice: ids are the lowest
  * then); with a sigmoid a NaN does so where it is chosen.  Ids are always k
  * different numbers of 0 .. E - 1.
@@ -789,7 +789,7 @@ int route_topk_grad_f32(const void *logits, const int32_t *ids, const float *dwe
  * whose id is outside 0 .. E - 1 has no row (pos -1; so a card that holds some of the
  * experts sorts the slots of those).
  *   ids, offsets, pos  4-byte aligned, not overlapping
- *   workspace  gemvtile_route_sort_workspace(T, k, E) bytes (0 for up to 4096 slots;
+ *   workspace  gemvtile_route_sort_workspace(T, k, E) bytes (0 for up to 2048 slots;
  *            it may then be NULL), 16-byte aligned, owned by the caller; as for
  *            rmsnorm_grad_*
  *   T >= 0, k >= 1, 1 <= E <= 1024, T * k <= 2^31 - 512.  T == 0: offsets are zeros.

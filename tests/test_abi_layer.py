@@ -129,7 +129,7 @@ def test_route_topk_grad(lib, fmt):
 def test_route_sort(lib):
     f = lib.route_sort
     space = lib.gemvtile_route_sort_workspace
-    assert space(512, 8, 64) == 0 and space(513, 8, 64) == 4 * 3 * 64 and space(1 << 20, 8, 256) == 4 * 64 * 256
+    assert space(256, 8, 64) == 0 and space(257, 8, 64) == 4 * 5 * 64 and space(1 << 20, 8, 256) == 4 * 128 * 256
     assert space(-1, 8, 64) == space(8, 0, 64) == space(8, 8, 0) == space(1 << 31, 8, 64) == 0
     for sizes in ((-1, 2, 4), (4, 0, 4), (4, 2, 0)):
         assert f(P, P, P, *sizes, None, 0, None) == INVALID

@@ -178,7 +178,7 @@ def _sort(env, ids, E, **kw):
     np.testing.assert_array_equal(host(pos), want_pos)
 
 
-@pytest.mark.parametrize("T,k,E", [(1, 1, 1), (1, 8, 64), (27, 8, 64), (63, 1, 3), (65, 3, 1000), (511, 8, 256), (512, 8, 1024), (513, 8, 1024),
+@pytest.mark.parametrize("T,k,E", [(1, 1, 1), (1, 8, 64), (27, 8, 64), (63, 1, 3), (65, 3, 1000), (255, 8, 256), (256, 8, 1024), (257, 8, 1024), (513, 8, 1024),
                                    (4097, 1, 17), (9000, 8, 256), (16384, 8, 256), (40000, 6, 1024), (300000, 1, 2)])
 def test_sort(env, T, k, E):
     r = np.random.default_rng(T + E)
@@ -222,7 +222,7 @@ def test_refusals(env):
         env.gt.route_topk_f32(t.zeros(2, 1100, device="cuda"), 2)
     with pytest.raises(TypeError):
         env.gt.route_topk_f16(l, 2)
-    ids = t.zeros(5000, 2, dtype=t.int32, device="cuda")
+    ids = t.zeros(1025, 2, dtype=t.int32, device="cuda")
     with pytest.raises(env.gt.GemvTileError, match="INVALID"):
         env.gt.route_sort(ids, 4)
     with pytest.raises(ValueError):
