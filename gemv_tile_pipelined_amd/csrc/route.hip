@@ -518,7 +518,7 @@ topk_kernel(const typename Element<DT>::type *__restrict__ logits, const float *
 
   // ---- keys: 1 + the rounded choice above the inverted number; 0: not to be chosen
   uint32_t key[V];
-  float step = 0.0f;
+  float step = 0.0f, lowest = kNegInf;  // the keys' step; what the lowest of them reach up to
   if (rounded) {
     // Equal steps over 2 below the largest choice (16 of logits); further down all are
     // alike, and settled as whatever is too near is.
@@ -531,6 +531,7 @@ topk_kernel(const typename Element<DT>::type *__restrict__ logits, const float *
     const float range = biased ? 2.0f : 16.0f, scale = static_cast<float>(kSteps) / range;
     const float base = 1.0f - (high - range) * scale;
     step = 2.0f * range / static_cast<float>(kSteps);
+    lowest = high - range + step;
 #pragma unroll
     for (int i = 0; i < V; ++i)
       key[i] = static_cast<uint32_t>(
@@ -576,7 +577,10 @@ topk_kernel(const typename Element<DT>::type *__restrict__ logits, const float *
     float choice = l;
     if (biased)
       choice = (softmax ? (l == kNegInf ? 0.0f : fast_exp(l - top_logit) / sum) : fast_sigmoid(l)) + b;
-    const float next_choice = __shfl_down(choice, 1), next_l = __shfl_down(l, 1), next_b = __shfl_down(b, 1);
+    // What the numbers with this key or a lower one reach up to: the lowest key stands for
+    // all further down.
+    const float reach = mine >> kIndexBits <= 1 ? __builtin_fmaxf(choice, lowest) : choice;
+    const float next_choice = __shfl_down(reach, 1), next_l = __shfl_down(l, 1), next_b = __shfl_down(b, 1);
     const uint32_t next_key = static_cast<uint32_t>(__shfl_down(static_cast<int>(mine), 1));
     const bool judged = sub < a.k && next_key != 0;
     // Equal logits with equal biases are a tie in any arithmetic.
@@ -589,12 +593,12 @@ topk_kernel(const typename Element<DT>::type *__restrict__ logits, const float *
     bool alone = true;
     if (__ballot(edge || bad) != 0) {
       const int from = part * L + a.k - 1;
-      const float last = __shfl(choice, from), after = __shfl(choice, from + 2);
+      const float last = __shfl(choice, from), after = __shfl(reach, from + 2);
       const float last_l = __shfl(l, from), last_b = __shfl(b, from);
       const uint32_t last_key = static_cast<uint32_t>(__shfl(static_cast<int>(mine), from));
       const uint32_t after_key = static_cast<uint32_t>(__shfl(static_cast<int>(mine), from + 2));
-      alone = after_key == 0 || (biased ? last - after > choice_margin(wrong, last, after, step)
-                                        : last_key >> kIndexBits != after_key >> kIndexBits);
+      alone = after_key == 0 || (last_key >> kIndexBits != after_key >> kIndexBits &&
+                                 (!biased || last - after > choice_margin(wrong, last, after, step)));
       const bool asked = __shfl(static_cast<int>(edge), from) != 0 && !alone;
       // Each other one has to be such a tie, or further down.
       bool doubt = false;

@@ -76,6 +76,29 @@ def test_choices_closer_than_fp32_tells(env, score):
     _check(env, logits, "f32", 8, bias + 1000.0, 8, 3, 1, score)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_choices_far_apart(env, score):
+    """Biases that spread the choices over many times the scores' range: clusters a few units of FP32 wide, whole units
+    below the largest choice and beside numbers far below them, with and without a large offset."""
+    r = np.random.default_rng(9)
+    T, E = 400, 128
+    for offset in (0.0, 37.0, -900.0):
+        for down in (1.0, 2.0, 2.0 + 2.0**-20, 5.0, 16.0):
+            logits = np.where(r.random((T, E)) < 0.5, 0.0, r.integers(-20, 21, (T, E)) * 2.0**-22).astype(np.float32).astype(np.float64)
+            bias = offset - down + r.integers(-6, 7, E) * 2.0**-22
+            bias[r.permutation(E)[:4]] = offset
+            bias[r.permutation(E)[:60]] -= 50.0
+            bias = bias.astype(np.float32).astype(np.float64)
+            for k in (3, 6, 12, 20):
+                _check(env, logits, "f32", k, bias, 1, 1, 1, score)
+            _check(env, logits, "f32", 6, bias, 8, 3, 2, score)
+            _check(env, logits, "bf16", 6, bias, 4, 2, 1, score)
+    logits = r.standard_normal((T, E)) * 30
+    logits[:, ::3] = np.round(logits[:, ::3])
+    _check(env, logits, "f32", 14, None, 1, 1, 1, score)
+    _check(env, logits, "f32", 30, None, 8, 4, 1, score)
+
+
 @FMT
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_masked_experts(env, score, fmt):
