@@ -362,10 +362,6 @@ topk_kernel(const typename Element<DT>::type *__restrict__ logits, const float *
 
   float logit[V], value[V];
   load_logits<DT, V>(row, a.E, sub, logit);
-  bool nan = false;  // among all logits
-#pragma unroll
-  for (int i = 0; i < V; ++i) nan |= logit[i] != logit[i];
-  nan = part_any<L>(nan, lane);
   float top_logit = kNegInf, sum = 1.0f;  // of all experts
   const bool scored = biased || sums;
   if (softmax && (scored || !a.norm)) {
@@ -393,7 +389,18 @@ topk_kernel(const typename Element<DT>::type *__restrict__ logits, const float *
 #pragma unroll
     for (int i = 0; i < V; ++i) value[i] = logit[i];
   }
+  // A choice that is NaN (its logit or its bias is, or the softmax) is left to FP64.
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < V; ++i) nan |= biased ? value[i] != value[i] : logit[i] != logit[i];
+  nan = part_any<L>(nan, lane);
   bool again = nan && (scored || rounded || a.groups > 1);
+  if (biased && nan) {  // all lanes of the token; from here on it is about the logits
+    nan = false;
+#pragma unroll
+    for (int i = 0; i < V; ++i) nan |= logit[i] != logit[i];
+    nan = part_any<L>(nan, lane);
+  }
 
   // ---- groups: value[] is what they count by
   uint32_t dropped = 0;  // experts of this lane (as bits) in groups that are not kept

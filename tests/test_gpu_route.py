@@ -154,6 +154,27 @@ def test_not_finite(env, fmt):
 
 @FMT
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_nan_bias(env, score, fmt):
+    """An expert whose bias is NaN ranks below all others, far ones and those with a bias of -inf too, in the choice and in
+    its group; its weight is that of its score."""
+    r = np.random.default_rng(10)
+    for E, groups, top in ((4, 1, 1), (48, 6, 2), (60, 5, 4), (600, 4, 1)):
+        logits = r.standard_normal((9, E))
+        for others in (0.1, -200.0, -INF):
+            bias = np.full(E, others)
+            bias[r.permutation(E)[: E // 4]] = 0.2
+            bias[r.permutation(E)[: E // 2]] = np.nan
+            bias[0] = np.nan
+            for k in (3, min(E // groups * top, 13)):
+                _check(env, logits, fmt, k, bias, 1, 1, 1, score)
+                if groups > 1:
+                    _check(env, logits, fmt, k, bias, groups, top, 1, score)
+                    _check(env, logits, fmt, k, bias, groups, top, 2, score)
+    _check(env, logits, fmt, 5, np.full(E, np.nan), 4, 2, 2, score)
+
+
+@FMT
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (5, 7, 3), (9, 64, 8), (4, 100, 6), (130, 128, 6), (3, 255, 8), (6, 512, 32), (3, 1000, 9), (2, 1024, 8)])
 def test_gradient(env, T, E, k, score, fmt):
     r = np.random.default_rng(T + E)
