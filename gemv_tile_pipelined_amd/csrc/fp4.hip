@@ -373,7 +373,7 @@ GemvShape gemv_shape(int64_t M, int64_t tiles, int64_t cus) {
   GemvShape best = {2, 1};
   int64_t least = INT64_MAX;
   for (const int xq : {2, 4, 6, 8, 12}) {
-    for (int nt = 1; nt <= (xq == 2 ? 2 : 4); ++nt) {
+    for (int nt = xq == 12 ? 2 : 1; nt <= (xq == 2 ? 2 : 4); ++nt) {
       const int64_t groups = (tiles + nt - 1) / nt * ((M + 4 * xq - 1) / (4 * xq));
       const int64_t cost = (groups + cus - 1) / cus * (2 * (M < 4 * xq ? M : 4 * xq) + 16 * nt);
       if (cost < least || (cost == least && xq > best.xq)) {

@@ -108,7 +108,7 @@ def _gemv_fp4(x, W, scale_W, y, stream, dtype, call):
 
 def gemv_fp4_f16(x, W, scale_W, y=None, stream=None):
     """y = x · (W scaled)ᵀ for one row x [K] or a decode batch x [M,K], fp16, rounded once: W [N,K/2] and scale_W
-    [N,K/32] uint8 as quantize_fp4_f16 gives them, y [N] or [M,N].  W is read once for up to 64 rows."""
+    [N,K/32] uint8 as quantize_fp4_f16 gives them, y [N] or [M,N].  Up to 48 rows share a read of W."""
     return _gemv_fp4(x, W, scale_W, y, stream, torch.float16, load_library().gemv_fp4_f16)
 
 

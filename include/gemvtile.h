@@ -666,8 +666,8 @@ int64_t gemvtile_group_unit(const int32_t *offsets, int64_t E, int64_t T, int64_
  *   y[m,n] = sum_b 2^(scale_W[n,b] - 127) * sum_{k in block b} x[m,k] * W[n,k]
  *
  * Products are exact; a block's are added in FP32, then scaled and added in FP32.
- * Meant for decode batches: W is read once for up to 64 rows, and again for each
- * 64 more.
+ * Meant for decode batches: up to 48 rows share what a workgroup reads of W, fewer
+ * where more workgroups make up for reading it again.
  *   x        [M,K] fp16 / bf16, 16-byte aligned
  *   W        [N,K/2] bytes, 16-byte aligned;  scale_W  [N,K/32] bytes
  *   y        [M,N] fp16 / bf16, 2-byte aligned
@@ -754,10 +754,10 @@ enum gemvtile_score {
  * Ids are those of choices computed in 64 bits, whatever the logits' type.  A logit
  * of -inf is an expert with score 0, chosen after all others unless a bias lifts it (a
  * bias of -inf does not); where every score that is divided by is 0 (all logits -inf)
- * the weights are 0.  A NaN choice ranks below all others.  With softmax a NaN or +inf among a token's logits makes its
- * weights NaN (and with a bias, or sums of two, every choice: ids are the lowest
- * then); with a sigmoid a NaN does so where it is chosen.  Ids are always k
- * different numbers of 0 .. E - 1.
+ * the weights are 0.  A NaN choice (of the logit or the bias) ranks below all others.
+ * With softmax a NaN or +inf among a token's logits makes its weights NaN (and with a
+ * bias, or sums of two, every choice: ids are the lowest then); with a sigmoid a NaN
+ * logit does so where it is chosen.  Ids are always k different numbers of 0 .. E - 1.
  *
  *   logits   [T,E] fp16 / bf16 / FP32, 16-byte aligned
  *   bias     [E] FP32 or NULL; ids, weights 4-byte aligned
