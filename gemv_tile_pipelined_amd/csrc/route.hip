@@ -787,6 +787,7 @@ topk_grad_kernel(const typename Element<DT>::type *__restrict__ logits, const in
 constexpr int kSortWaves = 8;
 constexpr int kSortThreads = kSortWaves * 64;
 constexpr int kSortExperts = 1024;
+constexpr int kSortLoads = 16;  // rows of counts that a thread reads together
 
 struct SortRun {
   int64_t begin, end;
@@ -800,11 +801,19 @@ __device__ inline SortRun sort_run(int64_t begin, int64_t end, int part, int par
   return {b, e};
 }
 
+// Four steps' numbers are on their way together, also where there are fewer.
 __device__ inline void count_run(const int *ids, SortRun r, int E, uint32_t *count, int lane) {
-#pragma unroll 4
-  for (int64_t i = r.begin + lane; i < r.end; i += 64) {
-    const int e = ids[i];
-    if (e >= 0 && e < E) atomicAdd(&count[e], 1u);  // a count: its order does not matter
+  for (int64_t base = r.begin; base < r.end; base += 256) {
+    int e[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int64_t i = base + s * 64 + lane;
+      e[s] = ids[i < r.end ? i : r.end - 1];
+      if (i >= r.end) e[s] = -1;
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+      if (e[s] >= 0 && e[s] < E) atomicAdd(&count[e[s]], 1u);  // a count: its order does not matter
   }
 }
 
@@ -841,11 +850,26 @@ sort_place_kernel(const int *__restrict__ ids, const int *__restrict__ hist, int
       const int part = c / E, e = c - part * E;
       const int past = blocks * (part + 1) / parts;
       uint32_t before = 0, total = 0;
-#pragma unroll 16
-      for (int b = blocks * part / parts; b < past; ++b) {
-        const uint32_t v = static_cast<uint32_t>(hist[static_cast<int64_t>(b) * E + e]);
-        before += b < mine ? v : 0u;
-        total += v;
+      int b = blocks * part / parts;
+      for (; b + kSortLoads <= past; b += kSortLoads) {
+#pragma unroll
+        for (int i = 0; i < kSortLoads; ++i) {
+          const uint32_t v = static_cast<uint32_t>(hist[static_cast<int64_t>(b + i) * E + e]);
+          before += b + i < mine ? v : 0u;
+          total += v;
+        }
+      }
+      if (b < past) {  // fewer rows, on their way together as well
+        uint32_t v[kSortLoads];
+#pragma unroll
+        for (int i = 0; i < kSortLoads; ++i)
+          v[i] = static_cast<uint32_t>(hist[static_cast<int64_t>(b + i < past ? b + i : past - 1) * E + e]);
+#pragma unroll
+        for (int i = 0; i < kSortLoads; ++i) {
+          if (b + i >= past) v[i] = 0;
+          before += b + i < mine ? v[i] : 0u;
+          total += v[i];
+        }
       }
       atomicAdd(&ahead[e], before);  // counts: their order does not matter
       atomicAdd(&all_of[e], total);
