@@ -16,6 +16,10 @@
 // and a maximum over the lanes through DPP; nothing is marked as taken, and the
 // key says whose it is.
 //
+// Bound by vector instructions, 276 a token of 256 experts (16384 tokens, 8 of 256 of
+// bf16 logits: 6.7 us, with a sigmoid and a bias 10.7, in 4 of 8 groups 12.1; with a
+// wave a token, as at 16 of 256, 13.2, 19.3 and 22.1).
+//
 // Ids are those of exact arithmetic.  16-bit logits fit a key as they are.  Scores,
 // and logits of 32 bits, are rounded; each decision (a choice against the next, the
 // last kept group against the first dropped) is checked afterwards against the
@@ -684,7 +688,9 @@ topk_kernel(const typename Element<DT>::type *__restrict__ logits, const float *
 //   softmax, normalised   dlogit_j = w_j (g_j - sum_i g_i w_i), w the softmax of the chosen logits
 //   sigmoid               dlogit_j = g_j c_j (1 - c_j)
 //   sigmoid, normalised   the same with (g_j - sum_i g_i w_i) / sum_i c_i for g_j, w = c / sum c
-// and 0 for experts not chosen.  Ids outside 0 .. E - 1 are left out.
+// and 0 for experts not chosen.  Ids outside 0 .. E - 1 are left out.  Rows are written
+// whole, by the lanes that have the experts: 8200 tokens, 6 of 128, in 4.5 us, of which
+// bytes are 0.9 and the rest a launch and a chain of loads, reductions and stores.
 template <int DT, int L, int V>
 __global__ void __launch_bounds__(kWaves * 64)
 topk_grad_kernel(const typename Element<DT>::type *__restrict__ logits, const int *__restrict__ ids,
@@ -1015,7 +1021,7 @@ hipError_t launch_route_topk_grad(int dtype, const void *logits, const int *ids,
 // One workgroup (and launch) for as many slots as it sorts sooner than two launches do
 // (E = 256, us with one / two: 1024 slots 4.6 / 6.7, 4096 8.9 / 7.7), then 512 slots to a
 // workgroup, up to 128 of them, as each reads all the others' counts (131072 slots: 10.4
-// us with 64, 9.9 with 128, 11.2 with 256).
+// us with 64, 9.7 with 128, 11.2 with 256).
 int route_sort_blocks(int64_t slots) {
   if (slots <= 2048) return 1;
   const int64_t b = (slots + 511) / 512;

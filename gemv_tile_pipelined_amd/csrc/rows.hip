@@ -7,7 +7,9 @@
 // Slots whose pos is outside 0 .. rows - 1 are left out.  All three walk over the
 // tokens, so a token's own row is read or written once however many experts it
 // has, and pos is all that they need.  Sums are in FP32, in the order of j.  Bound
-// by memory.
+// by memory: 4100 x 8 rows of 4096 bytes are gathered in 30 us (4.9 TB/s), the
+// gradient of a combine of 4096 x 8 rows of 2048 takes 58 us (4.9 TB/s; a large copy
+// reaches 5.3); 27 x 8 rows are combined in 3.8 us, a launch and its latency.
 #include "device_common.hpp"
 #include "kernels.hpp"
 #include "wave_ops.hpp"
