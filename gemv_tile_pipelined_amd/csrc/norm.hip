@@ -253,7 +253,7 @@ rmsnorm_grad_kernel(const uint16_t *__restrict__ dy, const uint16_t *__restrict_
 
 // dweight[c] = the sum of `parts` rows of partial [parts, C]: 32 columns to a
 // workgroup, 32 threads to a column, each a run of rows whose loads are in flight
-// together (8 threads to a column: 4.4 us for 512 x 2048, now 2.6).
+// together (8 threads to a column: 8191 x 2048 in 31.2 us in all, not 29.7).
 constexpr int kReduceCols = 32, kReduceRuns = 32;
 __global__ void __launch_bounds__(kReduceCols *kReduceRuns)
 rmsnorm_reduce_kernel(const float *__restrict__ partial, float *__restrict__ dweight, int parts, int C) {
