@@ -8,15 +8,16 @@
 //   dx = r (weight dy) - h r^3 mean_c(weight dy h) + dh
 //   dweight[c] = sum_t dy h r
 //
-// A workgroup holds a row in registers between the sum of squares and the output,
-// so each input is read once and each output written once: bound by memory.  The
-// sum of squares and r are in FP64, which costs nothing here (8192 x 4096 with the
-// residual, 8 bits out, takes 46 us either way) and makes the e4m3 numbers those
-// nearest to y / scale but for one in some 10^7: weight h is exact in FP32, r /
-// scale has 48 bits, and the product is rounded to odd before the conversion, so
-// that only real ties tie.  y in 16 bits and both gradients are FP32 until their one
-// rounding.  16 lanes hold a block of 128 columns, 8 each, so a block's largest
-// number is found within a lane row.
+// A row is held in registers between the sum of squares and the output, so each input
+// is read once and each output written once: bound by memory.  Rows of up to 1536
+// columns are a wave's or less, several to a workgroup, and need no barrier; longer
+// ones are a workgroup's.  The sum of squares and r are in FP64, which costs nothing
+// here (8192 x 4096 with the residual, 8 bits out, takes 46 us either way) and makes the
+// e4m3 numbers those nearest to y / scale but for one in some 10^7: weight h is exact in
+// FP32, r / scale has 48 bits, and the product is rounded to odd before the conversion,
+// so that only real ties tie.  y in 16 bits and both gradients are FP32 until their one
+// rounding.  16 lanes hold a block of 128 columns, 8 each, so a block's largest number
+// is found within a lane row.
 #include "fp8_common.hpp"
 #include "kernels.hpp"
 #include "wave_ops.hpp"
@@ -27,29 +28,57 @@ namespace {
 
 constexpr float kMinScale = 0x1p-80f;
 
-// Sum over the workgroup, in every lane; waves are added in order.  `slots` is
-// one of two buffers that the caller uses in turn, so that one barrier is enough.
-template <int THREADS>
-__device__ inline float group_sum(float v, float *slots) {
+// Which of a workgroup's ROWS rows this thread is at; the same for a whole wave if the
+// row has one.
+template <int LANES, int ROWS>
+__device__ inline int row_group() {
+  if constexpr (ROWS == 1) return 0;
+  const int group = static_cast<int>(threadIdx.x) / LANES;
+  if constexpr (LANES < 64) return group;
+  return __builtin_amdgcn_readfirstlane(group);
+}
+
+// Sum over the LANES threads of a row, in every one of them: within a wave, or over
+// the waves of a workgroup (LANES > 64, one row a workgroup), added in order.  `slots`
+// is one of two buffers that the caller uses in turn, so that one barrier is enough.
+template <int LANES>
+__device__ inline float row_sum(float v, float *slots) {
+  if constexpr (LANES <= 32) {
+    v = dpp_add<0xB1>(v);
+    v = dpp_add<0x4E>(v);
+    v = dpp_add<0x141>(v);
+    if constexpr (LANES >= 16) v = dpp_add<0x140>(v);
+    if constexpr (LANES == 32) v += __shfl_xor(v, 16);
+    return v;
+  }
   v = wave_sum(v);
-  if constexpr (THREADS == 64) return v;
+  if constexpr (LANES == 64) return v;
   if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = v;
   __syncthreads();
   float sum = slots[0];
 #pragma unroll
-  for (int w = 1; w < THREADS / 64; ++w) sum += slots[w];
+  for (int w = 1; w < LANES / 64; ++w) sum += slots[w];
   return sum;
 }
 
 // The same in FP64.
-template <int THREADS>
-__device__ inline double group_sum(double v, double *slots) {
+template <int LANES>
+__device__ inline double row_sum(double v, double *slots) {
+  if constexpr (LANES <= 32) {
+    v = dpp_add<0xB1>(v);
+    v = dpp_add<0x4E>(v);
+    v = dpp_add<0x141>(v);
+    if constexpr (LANES >= 16) v = dpp_add<0x140>(v);
+    if constexpr (LANES == 32) v += __shfl_xor(v, 16);
+    return v;
+  }
   v = wave_sum_last(v);
+  if constexpr (LANES == 64) return __shfl(v, 63);
   if ((threadIdx.x & 63) == 63) slots[threadIdx.x >> 6] = v;
   __syncthreads();
   double sum = slots[0];
 #pragma unroll
-  for (int w = 1; w < THREADS / 64; ++w) sum += slots[w];
+  for (int w = 1; w < LANES / 64; ++w) sum += slots[w];
   return sum;
 }
 
@@ -78,27 +107,29 @@ __device__ inline float product_to_odd(float p, float high, float low) {
 
 // h may be x or residual: a row's vectors are all read by the threads that write
 // them, before they do.
-template <int DT, int THREADS, int NV, bool FP8>
-__global__ void __launch_bounds__(THREADS)
+template <int DT, int LANES, int NV, int ROWS, bool FP8>
+__global__ void __launch_bounds__(LANES *ROWS)
 rmsnorm_kernel(const uint16_t *x, const uint16_t *residual, const uint16_t *__restrict__ weight, uint16_t *h,
                uint16_t *__restrict__ y, uint8_t *__restrict__ q, float *__restrict__ scale, float *__restrict__ rstd, int T,
                int C, float eps) {
-  __shared__ double slots[2][THREADS / 64];
+  __shared__ double slots[2][(LANES + 63) / 64];
+  const int group = row_group<LANES, ROWS>(), sub = static_cast<int>(threadIdx.x) - group * LANES;
   const int vecs = C / 8, blocks = (C + kScaleBlock - 1) / kScaleBlock;
   const double inv_c = 1.0 / static_cast<double>(C);
   uint4_v wv[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int v = i * THREADS + threadIdx.x;
+    const int v = i * LANES + sub;
     wv[i] = v < vecs ? reinterpret_cast<const uint4_v *>(weight)[v] : uint4_v{0, 0, 0, 0};
   }
   int turn = 0;
-  for (int64_t row = blockIdx.x; row < T; row += gridDim.x, turn ^= 1) {
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + group; row < T;
+       row += static_cast<int64_t>(gridDim.x) * ROWS, turn ^= 1) {
     const uint4_v *xr = reinterpret_cast<const uint4_v *>(x + row * C);
     uint4_v hv[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int v = i * THREADS + threadIdx.x;
+      const int v = i * LANES + sub;
       hv[i] = v < vecs ? xr[v] : uint4_v{0, 0, 0, 0};
     }
     if (residual != nullptr) {
@@ -107,12 +138,12 @@ rmsnorm_kernel(const uint16_t *x, const uint16_t *residual, const uint16_t *__re
       uint4_v rv[NV];
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int v = i * THREADS + threadIdx.x;
+        const int v = i * LANES + sub;
         rv[i] = v < vecs ? rr[v] : uint4_v{0, 0, 0, 0};
       }
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int v = i * THREADS + threadIdx.x;
+        const int v = i * LANES + sub;
         float a[8], b[8];
         widen8<DT>(hv[i], a);
         widen8<DT>(rv[i], b);
@@ -130,13 +161,13 @@ rmsnorm_kernel(const uint16_t *x, const uint16_t *residual, const uint16_t *__re
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum = __builtin_fma(static_cast<double>(a[j]), static_cast<double>(a[j]), sum);
     }
-    sum = group_sum<THREADS>(sum, slots[turn]);
+    sum = row_sum<LANES>(sum, slots[turn]);
     const double rd = inverse_root(sum * inv_c + static_cast<double>(eps));
     const float r = static_cast<float>(rd);
-    if (rstd != nullptr && threadIdx.x == 0) rstd[row] = r;
+    if (rstd != nullptr && sub == 0) rstd[row] = r;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int v = i * THREADS + threadIdx.x;
+      const int v = i * LANES + sub;
       float a[8], w[8];
       widen8<DT>(hv[i], a);
       widen8<DT>(wv[i], w);
@@ -159,7 +190,7 @@ rmsnorm_kernel(const uint16_t *x, const uint16_t *residual, const uint16_t *__re
           const uint32_t bits = __builtin_bit_cast(uint32_t, a[j]) & 0x7fffffffu;
           top = bits > top ? bits : top;
         }
-        const double amax = static_cast<double>(__builtin_bit_cast(float, max_of_16_lanes(top)));
+        const double amax = static_cast<double>(__builtin_bit_cast(float, LANES == 8 ? max_of_8_lanes(top) : max_of_16_lanes(top)));
         float s = static_cast<float>(amax * rd * (1.0 / 448.0));
         s = s < kMinScale ? kMinScale : s;  // a NaN stays
         const double t = rd / static_cast<double>(s);
@@ -172,45 +203,74 @@ rmsnorm_kernel(const uint16_t *x, const uint16_t *residual, const uint16_t *__re
         q1 = __builtin_amdgcn_cvt_pk_fp8_f32(a[6], a[7], q1, true);
         if (v < vecs) {
           reinterpret_cast<uint2_v *>(q + row * C)[v] = uint2_v{static_cast<uint32_t>(q0), static_cast<uint32_t>(q1)};
-          if ((threadIdx.x & 15) == 0) scale[row * blocks + v / 16] = s;
+          if ((sub & 15) == 0) scale[row * blocks + v / 16] = s;
         }
       }
     }
   }
 }
 
-// Rows of a workgroup follow one another by the grid; a thread keeps its
-// columns' share of dweight in registers over them and leaves it in `partial`
-// [gridDim.x, C].  8191 x 2048 with dh: 29.7 us with the sum of the partial rows, of
-// which 25.3 are its bytes at a large copy's rate.
-template <int DT, int THREADS, int NV>
-__global__ void __launch_bounds__(THREADS)
+// Rows of a workgroup follow one another by the grid; a thread keeps its columns'
+// share of dweight in registers over them (in LDS, in places of its own, where the
+// registers do not hold it) and leaves it in `partial` [gridDim.x, C].  AHEAD: the next
+// row is on its way while this one is worked on, for rows of which a CU has only one.
+// 8191 x 2048 with dh: 29.7 us with the sum of the partial rows, of which 25.3 are its
+// bytes at a large copy's rate.
+template <int DT, int LANES, int NV, int ROWS, bool AHEAD>
+__global__ void __launch_bounds__(LANES *ROWS)
 rmsnorm_grad_kernel(const uint16_t *__restrict__ dy, const uint16_t *__restrict__ dh, const uint16_t *__restrict__ h,
                     const uint16_t *__restrict__ weight, const float *__restrict__ rstd, uint16_t *__restrict__ dx,
                     float *__restrict__ partial, int T, int C) {
-  __shared__ float slots[2][THREADS / 64];
+  __shared__ float slots[2][(LANES + 63) / 64];
+  const int group = row_group<LANES, ROWS>(), sub = static_cast<int>(threadIdx.x) - group * LANES;
   const int vecs = C / 8;
   const float inv_c = 1.0f / static_cast<float>(C);
-  uint4_v wv[NV];
-  float dw[NV][8];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int v = i * THREADS + threadIdx.x;
-    wv[i] = v < vecs ? reinterpret_cast<const uint4_v *>(weight)[v] : uint4_v{0, 0, 0, 0};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
-  }
-  int turn = 0;
-  for (int64_t row = blockIdx.x; row < T; row += gridDim.x, turn ^= 1) {
-    const float r = rstd[row];
-    uint4_v dv[NV], hv[NV], ev[NV];
+  constexpr bool kFar = LANES * NV > 2048;  // dw is in LDS, and dh is read late
+  __shared__ float4_t far[kFar ? 2 * LANES * NV : 1];
+  uint4_v wv[NV], dv[NV], hv[NV], ev[NV];
+  float dw[NV][8], r = 0.0f;
+  const auto load = [&](const uint4_v *src, uint4_v (&to)[NV]) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int v = i * THREADS + threadIdx.x;
-      const bool in = v < vecs;
-      dv[i] = in ? reinterpret_cast<const uint4_v *>(dy + row * C)[v] : uint4_v{0, 0, 0, 0};
-      hv[i] = in ? reinterpret_cast<const uint4_v *>(h + row * C)[v] : uint4_v{0, 0, 0, 0};
-      ev[i] = in && dh != nullptr ? reinterpret_cast<const uint4_v *>(dh + row * C)[v] : uint4_v{0, 0, 0, 0};
+      const int v = i * LANES + sub;
+      to[i] = src != nullptr && v < vecs ? src[v] : uint4_v{0, 0, 0, 0};
+    }
+  };
+  const auto row_of = [&](const uint16_t *p, int64_t row) {
+    return p != nullptr ? reinterpret_cast<const uint4_v *>(p + row * C) : nullptr;
+  };
+  const auto load_row = [&](int64_t row, uint4_v (&d)[NV], uint4_v (&hh)[NV], uint4_v (&e)[NV], float &rr) {
+    rr = rstd[row];
+    load(row_of(dy, row), d);
+    load(row_of(h, row), hh);
+    if constexpr (!kFar) load(row_of(dh, row), e);
+  };
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
+  if constexpr (kFar) {
+#pragma unroll
+    for (int i = 0; i < 2 * NV; ++i) far[i * LANES + sub] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  load(reinterpret_cast<const uint4_v *>(weight), wv);
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * ROWS + group, step = static_cast<int64_t>(gridDim.x) * ROWS;
+  uint4_v dn[NV], hn[NV], en[NV];
+  float rn = 0.0f;
+  if (AHEAD && first < T) load_row(first, dn, hn, en, rn);
+  int turn = 0;
+  for (int64_t row = first; row < T; row += step, turn ^= 1) {
+    if constexpr (AHEAD) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        dv[i] = dn[i];
+        hv[i] = hn[i];
+        ev[i] = en[i];
+      }
+      r = rn;
+      if (row + step < T) load_row(row + step, dn, hn, en, rn);
+    } else {
+      load_row(row, dv, hv, ev, r);
     }
     float dot = 0.0f;
 #pragma unroll
@@ -219,17 +279,29 @@ rmsnorm_grad_kernel(const uint16_t *__restrict__ dy, const uint16_t *__restrict_
       widen8<DT>(dv[i], a);
       widen8<DT>(hv[i], b);
       widen8<DT>(wv[i], w);
+      float4_t lo, hi;
+      if constexpr (kFar) {
+        lo = far[2 * i * LANES + sub];
+        hi = far[(2 * i + 1) * LANES + sub];
+      }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float n = b[j] * r;
-        dw[i][j] = __builtin_fmaf(a[j], n, dw[i][j]);
+        if constexpr (!kFar) dw[i][j] = __builtin_fmaf(a[j], n, dw[i][j]);
+        else if (j < 4) lo[j] = __builtin_fmaf(a[j], n, lo[j]);
+        else hi[j - 4] = __builtin_fmaf(a[j], n, hi[j - 4]);
         dot = __builtin_fmaf(a[j] * w[j], n, dot);
       }
+      if constexpr (kFar) {
+        far[2 * i * LANES + sub] = lo;
+        far[(2 * i + 1) * LANES + sub] = hi;
+      }
     }
-    dot = group_sum<THREADS>(dot, slots[turn]) * inv_c;
+    dot = row_sum<LANES>(dot, slots[turn]) * inv_c;
+    if constexpr (kFar) load(row_of(dh, row), ev);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int v = i * THREADS + threadIdx.x;
+      const int v = i * LANES + sub;
       float a[8], b[8], w[8], e[8];
       widen8<DT>(dv[i], a);
       widen8<DT>(hv[i], b);
@@ -240,13 +312,31 @@ rmsnorm_grad_kernel(const uint16_t *__restrict__ dy, const uint16_t *__restrict_
       if (v < vecs) reinterpret_cast<uint4_v *>(dx + row * C)[v] = round8<DT>(a);
     }
   }
+  if constexpr (ROWS > 1) {
+    // The shares of the rows that went side by side, in their order.
+    __shared__ __attribute__((aligned(16))) float sums[ROWS][LANES * NV * 8];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int v = i * THREADS + threadIdx.x;
-    if (v < vecs) {
-      float4_t *out = reinterpret_cast<float4_t *>(partial + static_cast<int64_t>(blockIdx.x) * C + 8 * v);
-      out[0] = float4_t{dw[i][0], dw[i][1], dw[i][2], dw[i][3]};
-      out[1] = float4_t{dw[i][4], dw[i][5], dw[i][6], dw[i][7]};
+    for (int i = 0; i < NV; ++i) {
+      float4_t *to = reinterpret_cast<float4_t *>(&sums[group][(i * LANES + sub) * 8]);
+      to[0] = float4_t{dw[i][0], dw[i][1], dw[i][2], dw[i][3]};
+      to[1] = float4_t{dw[i][4], dw[i][5], dw[i][6], dw[i][7]};
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < C; c += LANES * ROWS) {
+      float sum = sums[0][c];
+#pragma unroll
+      for (int r = 1; r < ROWS; ++r) sum += sums[r][c];
+      partial[static_cast<int64_t>(blockIdx.x) * C + c] = sum;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = i * LANES + sub;
+      if (v < vecs) {
+        float4_t *out = reinterpret_cast<float4_t *>(partial + static_cast<int64_t>(blockIdx.x) * C + 8 * v);
+        out[0] = kFar ? far[2 * i * LANES + sub] : float4_t{dw[i][0], dw[i][1], dw[i][2], dw[i][3]};
+        out[1] = kFar ? far[(2 * i + 1) * LANES + sub] : float4_t{dw[i][4], dw[i][5], dw[i][6], dw[i][7]};
+      }
     }
   }
 }
@@ -279,35 +369,49 @@ rmsnorm_reduce_kernel(const float *__restrict__ partial, float *__restrict__ dwe
 // with 256 threads, with 2048 workgroups and with one for each row; with 512 threads
 // 48.3 and 46.3 to 48.
 constexpr int kNormGrid = 16384;
+// Workgroups of the gradient at most, each with a row of partial sums; half as many for
+// long rows, whose partial sums are bytes that count.
+constexpr int kNormParts = 512, kLongRowParts = 256;
 
-template <int DT, int THREADS, int NV>
+template <int DT, int LANES, int NV, int ROWS = 1>
 hipError_t launch_norm(const NormArgs &a, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(a.T < kNormGrid ? a.T : kNormGrid));
-  const auto kernel = a.q != nullptr ? rmsnorm_kernel<DT, THREADS, NV, true> : rmsnorm_kernel<DT, THREADS, NV, false>;
-  hipLaunchKernelGGL(kernel, grid, dim3(THREADS), 0, stream, static_cast<const uint16_t *>(a.x),
+  const int blocks = (a.T + ROWS - 1) / ROWS;
+  const dim3 grid(static_cast<unsigned>(blocks < kNormGrid ? blocks : kNormGrid));
+  const auto kernel = a.q != nullptr ? rmsnorm_kernel<DT, LANES, NV, ROWS, true> : rmsnorm_kernel<DT, LANES, NV, ROWS, false>;
+  hipLaunchKernelGGL(kernel, grid, dim3(LANES * ROWS), 0, stream, static_cast<const uint16_t *>(a.x),
                      static_cast<const uint16_t *>(a.residual), static_cast<const uint16_t *>(a.weight),
                      static_cast<uint16_t *>(a.h), static_cast<uint16_t *>(a.y), static_cast<uint8_t *>(a.q), a.scale, a.rstd,
                      a.T, a.C, a.eps);
   return hipGetLastError();
 }
 
+// LANES, NV, ROWS for a row's pieces of 8 columns.  2^25 numbers, us without a residual /
+// with it / with 8 bits out (bytes at a large copy's rate: 25.3, 50.6, 44.3): C = 64 27 / 48 /
+// 46 (a wave a row 95 / 147 / 207), 128 27 / 48 / 45 (54 / 85 / 110), 256 27 / 48 / 46 (33 / 55 /
+// 62), 1024 25 / 48 / 45 (two waves a row 26 / 51 / 47), 1536 25 / 48 / 46 (four 30 / 49 / 49), 2048
+// 27 / 47 / 46 (a wave a row 25 / 47 / 47), 20480 29 / 57 / 61 (four pieces a thread 30 / 59 / 64).
 template <int DT>
 hipError_t launch_norm_dt(const NormArgs &a, hipStream_t stream) {
   const int vecs = a.C / 8;
-  if (vecs <= 64) return launch_norm<DT, 64, 1>(a, stream);
-  if (vecs <= 128) return launch_norm<DT, 128, 1>(a, stream);
+  if (vecs <= 8) return launch_norm<DT, 8, 1, 32>(a, stream);
+  if (vecs <= 16) return launch_norm<DT, 16, 1, 16>(a, stream);
+  if (vecs <= 32) return launch_norm<DT, 32, 1, 8>(a, stream);
+  if (vecs <= 64) return launch_norm<DT, 64, 1, 4>(a, stream);
+  if (vecs <= 128) return launch_norm<DT, 64, 2, 4>(a, stream);
+  if (vecs <= 192) return launch_norm<DT, 64, 3, 4>(a, stream);
   if (vecs <= 256) return launch_norm<DT, 256, 1>(a, stream);
   if (vecs <= 512) return launch_norm<DT, 256, 2>(a, stream);
   if (vecs <= 1024) return launch_norm<DT, 512, 2>(a, stream);
   if (vecs <= 2048) return launch_norm<DT, 512, 4>(a, stream);
+  if (vecs <= 3 * 1024) return launch_norm<DT, 1024, 3>(a, stream);
   return launch_norm<DT, 1024, 4>(a, stream);
 }
 
-template <int DT, int THREADS, int NV>
+template <int DT, int LANES, int NV, int ROWS = 1, int PARTS = kNormParts, bool AHEAD = false>
 hipError_t launch_grad(const NormGradArgs &a, hipStream_t stream) {
-  const int parts = rmsnorm_grad_parts(a.T);
+  const int parts = (a.T + ROWS - 1) / ROWS < PARTS ? (a.T + ROWS - 1) / ROWS : PARTS;
   if (parts > 0) {  // without rows dweight is a sum of nothing
-    hipLaunchKernelGGL((rmsnorm_grad_kernel<DT, THREADS, NV>), dim3(parts), dim3(THREADS), 0, stream,
+    hipLaunchKernelGGL((rmsnorm_grad_kernel<DT, LANES, NV, ROWS, AHEAD>), dim3(parts), dim3(LANES * ROWS), 0, stream,
                        static_cast<const uint16_t *>(a.dy), static_cast<const uint16_t *>(a.dh),
                        static_cast<const uint16_t *>(a.h), static_cast<const uint16_t *>(a.weight), a.rstd,
                        static_cast<uint16_t *>(a.dx), a.workspace, a.T, a.C);
@@ -319,16 +423,26 @@ hipError_t launch_grad(const NormGradArgs &a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// As above.  2^25 numbers with dh, us (bytes 50.6): C = 64 51 (a wave a row, one to a
+// workgroup: 778), 128 52 (389), 512 51 (120), 1024 53 (two waves a row 76), 1536 54 (four 60),
+// 2048 53 (a wave a row 54), 5120 55 (512 threads and workgroups, not AHEAD 56), 8192 55 (57),
+// 12288 58 (63), 16384 60 (67; AHEAD does not fit the registers: 118), 20480 62 (1024 threads of
+// 4 pieces, dw in registers that it does not have, 277; 512 of 6 67), 32768 74 (220; 1024 of 4 80).
 template <int DT>
 hipError_t launch_grad_dt(const NormGradArgs &a, hipStream_t stream) {
   const int vecs = a.C / 8;
-  if (vecs <= 64) return launch_grad<DT, 64, 1>(a, stream);
-  if (vecs <= 128) return launch_grad<DT, 128, 1>(a, stream);
+  if (vecs <= 8) return launch_grad<DT, 8, 1, 32>(a, stream);
+  if (vecs <= 16) return launch_grad<DT, 16, 1, 16>(a, stream);
+  if (vecs <= 32) return launch_grad<DT, 32, 1, 8>(a, stream);
+  if (vecs <= 64) return launch_grad<DT, 64, 1, 4>(a, stream);
+  if (vecs <= 128) return launch_grad<DT, 64, 2, 4>(a, stream);
+  if (vecs <= 192) return launch_grad<DT, 64, 3, 4>(a, stream);
   if (vecs <= 256) return launch_grad<DT, 256, 1>(a, stream);
   if (vecs <= 512) return launch_grad<DT, 512, 1>(a, stream);
-  if (vecs <= 1024) return launch_grad<DT, 512, 2>(a, stream);
-  if (vecs <= 2048) return launch_grad<DT, 512, 4>(a, stream);
-  return launch_grad<DT, 1024, 4>(a, stream);
+  if (vecs <= 1024) return launch_grad<DT, 1024, 1, 1, kLongRowParts, true>(a, stream);
+  if (vecs <= 2048) return launch_grad<DT, 1024, 2, 1, kLongRowParts>(a, stream);
+  if (vecs <= 3 * 1024) return launch_grad<DT, 1024, 3, 1, kLongRowParts>(a, stream);
+  return launch_grad<DT, 512, 8, 1, kLongRowParts>(a, stream);
 }
 
 }  // namespace
@@ -337,7 +451,7 @@ hipError_t launch_rmsnorm(int dtype, const NormArgs &a, hipStream_t stream) {
   return dtype == kBF16 ? launch_norm_dt<kBF16>(a, stream) : launch_norm_dt<kF16>(a, stream);
 }
 
-int rmsnorm_grad_parts(int64_t T) { return static_cast<int>(T < 512 ? T : 512); }
+int rmsnorm_grad_parts(int64_t T) { return static_cast<int>(T < kNormParts ? T : kNormParts); }
 
 hipError_t launch_rmsnorm_grad(int dtype, const NormGradArgs &a, hipStream_t stream) {
   return dtype == kBF16 ? launch_grad_dt<kBF16>(a, stream) : launch_grad_dt<kF16>(a, stream);

@@ -22,14 +22,14 @@ __device__ inline uint32_t dpp_max(uint32_t v) {
   return o > v ? o : v;
 }
 
-// Maximum over each lane row of 16: pairs, quads, the mirrored half row, the
-// mirrored row.
-__device__ inline uint32_t max_of_16_lanes(uint32_t v) {
+// Maximum over 8 lanes and over each lane row of 16: pairs, quads, the mirrored half
+// row, the mirrored row.
+__device__ inline uint32_t max_of_8_lanes(uint32_t v) {
   v = dpp_max<0xB1>(v);
   v = dpp_max<0x4E>(v);
-  v = dpp_max<0x141>(v);
-  return dpp_max<0x140>(v);
+  return dpp_max<0x141>(v);
 }
+__device__ inline uint32_t max_of_16_lanes(uint32_t v) { return dpp_max<0x140>(max_of_8_lanes(v)); }
 
 // Sum and maximum over the 64 lanes, in every lane: as above within lane rows,
 // then row_bcast:15 adds row 0 into 1 and 2 into 3, row_bcast:31 lane 31 into the

@@ -709,7 +709,7 @@ int gemv_fp4_bf16(const void *x, const void *W, const void *scale_W, void *y, in
  *                the gradient of x and of residual alike
  *   dweight[c] = sum_t dy h r                                        FP32
  *
- * The rows' shares of dweight are added in FP32, in an order that T alone decides.
+ * The rows' shares of dweight are added in FP32, in an order that T and C alone decide.
  *   dy, dh, h, weight, dx  16-byte aligned; rstd, dweight 4-byte aligned; dx
  *            overlaps nothing
  *   workspace  gemvtile_rmsnorm_grad_workspace(T, C) bytes of device memory, owned

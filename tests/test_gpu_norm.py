@@ -120,6 +120,52 @@ def test_gradient(env, T, C, with_dh, fmt):
     assert env.torch.equal(again[0], dx) and env.torch.equal(again[1], dw)
 
 
+# rows of every launch shape, several to a wave or a workgroup, and more of them than workgroups take at once
+MANY = [(20000, 64), (33, 56), (20, 136), (70, 256), (5000, 512), (9, 528), (2600, 1024), (2100, 1536), (530, 2048), (600, 5120), (300, 8192),
+        (270, 16384), (3, 16392), (259, 20480), (2, 24576), (258, 24584), (257, 32768)]
+
+
+@pytest.mark.parametrize("T,C", MANY)
+def test_many_rows(env, T, C):
+    x, res, w = _inputs(env, T, C, "bf16")
+    rstd = env.torch.empty(T, device="cuda")
+    y, h = env.gt.rmsnorm_bf16(x, w, res, EPS, rstd=rstd)
+    want_h, want_r, want_y = ref.rmsnorm(host(x), host(res), host(w), EPS, "bf16")
+    np.testing.assert_array_equal(host(h), want_h)
+    near(host(rstd), want_r, ref.NORM_ERROR * want_r)
+    near(host(y), want_y, ref.rounded(want_y, ref.NORM_ERROR * np.abs(want_y), "bf16"))
+    if C % 16 == 0:
+        q, scale, _ = env.gt.rmsnorm_fp8_bf16(x, w, res, EPS)
+        _check_fp8(q.float().cpu().double().numpy(), host(scale), want_y)
+    dx, dw = env.gt.rmsnorm_grad_bf16(res, h, w, rstd, x, workspace=env.gt.alloc_rmsnorm_grad_workspace(h).fill_(255))
+    (want, slack), (want_w, slack_w) = ref.rmsnorm_grad(host(res), host(x), host(h), host(w), host(rstd))
+    near(host(dx), want, ref.rounded(want, slack, "bf16"))
+    near(host(dw), want_w, slack_w + 2.0**-149)
+
+
+@pytest.mark.parametrize("C", [8, 64, 128, 256, 512, 1024, 1536])
+def test_rows_of_a_wave_apart(env, C):
+    """A NaN in a row changes neither output nor gradient of those beside it in a wave or a workgroup."""
+    t = env.torch
+    x, res, w = _inputs(env, 70, C, "f16")
+    rstd = t.empty(70, device="cuda")
+    y, h = env.gt.rmsnorm_f16(x, w, res, EPS, rstd=rstd)
+    space = env.gt.alloc_rmsnorm_grad_workspace(h)
+    dx, _ = env.gt.rmsnorm_grad_f16(res, h, w, rstd, x, workspace=space)
+    bad = [0, 5, 33, 69]
+    keep = [i for i in range(70) if i not in bad]
+    h2, rstd2 = h.clone(), rstd.clone()
+    h2[bad, -1], rstd2[bad] = float("nan"), float("nan")
+    y2, _ = env.gt.rmsnorm_f16(h2, w, None, EPS)
+    dx2, _ = env.gt.rmsnorm_grad_f16(res, h2, w, rstd2, x, workspace=space)
+    assert t.equal(y2[keep], y[keep]) and t.equal(dx2[keep], dx[keep])
+    assert t.isnan(y2[bad]).all() and t.isnan(dx2[bad]).all()
+    if C % 16 == 0:
+        q, s, _ = env.gt.rmsnorm_fp8_f16(h, w, None, EPS)
+        q2, s2, _ = env.gt.rmsnorm_fp8_f16(h2, w, None, EPS)
+        assert t.equal(q2.view(t.uint8)[keep], q.view(t.uint8)[keep]) and t.equal(s2[keep], s[keep]) and t.isnan(s2[bad]).all()
+
+
 def test_gradient_of_no_rows(env):
     t = env.torch
     e = t.empty(0, 64, device="cuda").half()
