@@ -43,16 +43,8 @@ __device__ inline int row_group() {
 // is one of two buffers that the caller uses in turn, so that one barrier is enough.
 template <int LANES>
 __device__ inline float row_sum(float v, float *slots) {
-  if constexpr (LANES <= 32) {
-    v = dpp_add<0xB1>(v);
-    v = dpp_add<0x4E>(v);
-    v = dpp_add<0x141>(v);
-    if constexpr (LANES >= 16) v = dpp_add<0x140>(v);
-    if constexpr (LANES == 32) v += __shfl_xor(v, 16);
-    return v;
-  }
+  if constexpr (LANES <= 64) return lanes_sum<LANES>(v);
   v = wave_sum(v);
-  if constexpr (LANES == 64) return v;
   if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = v;
   __syncthreads();
   float sum = slots[0];
@@ -64,16 +56,8 @@ __device__ inline float row_sum(float v, float *slots) {
 // The same in FP64.
 template <int LANES>
 __device__ inline double row_sum(double v, double *slots) {
-  if constexpr (LANES <= 32) {
-    v = dpp_add<0xB1>(v);
-    v = dpp_add<0x4E>(v);
-    v = dpp_add<0x141>(v);
-    if constexpr (LANES >= 16) v = dpp_add<0x140>(v);
-    if constexpr (LANES == 32) v += __shfl_xor(v, 16);
-    return v;
-  }
+  if constexpr (LANES <= 64) return lanes_sum<LANES>(v);
   v = wave_sum_last(v);
-  if constexpr (LANES == 64) return __shfl(v, 63);
   if ((threadIdx.x & 63) == 63) slots[threadIdx.x >> 6] = v;
   __syncthreads();
   double sum = slots[0];

@@ -287,14 +287,6 @@ __device__ inline uint32_t part_max(uint32_t v) {
   if constexpr (L == 16) return max_of_16_lanes(v);
   else return wave_max(v);
 }
-template <int L>
-__device__ inline float part_sum(float v) {
-  if constexpr (L == 64) return wave_sum(v);
-  v = dpp_add<0xB1>(v);
-  v = dpp_add<0x4E>(v);
-  v = dpp_add<0x141>(v);
-  return dpp_add<0x140>(v);
-}
 // NaN left aside; -inf of nothing.
 template <int L>
 __device__ inline float part_max(float v) {
@@ -375,7 +367,7 @@ topk_kernel(const typename Element<DT>::type *__restrict__ logits, const float *
     top_logit = part_max<L>(m);
 #pragma unroll
     for (int i = 0; i < V; ++i) value[i] = logit[i] == kNegInf ? 0.0f : fast_exp(logit[i] - top_logit);
-    sum = part_sum<L>(tree_sum<V>(value));
+    sum = lanes_sum<L>(tree_sum<V>(value));
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
     for (int i = 0; i < V; ++i) value[i] *= inv;
@@ -671,7 +663,7 @@ topk_kernel(const typename Element<DT>::type *__restrict__ logits, const float *
       w = own > 0.0f ? 1.0f / (1.0f + expf(-own)) : ref == kNegInf ? 0.0f : expf(own - ref) / (1.0f + expf(own));
     }
     if (!has) w = 0.0f;
-    const float total = part_sum<L>(w);
+    const float total = lanes_sum<L>(w);
     w = nan ? __builtin_nanf("") : total > 0.0f ? w / total : total;
   } else {
     w = softmax ? (own == kNegInf && !nan ? 0.0f : expf(own - top_logit) / sum) : sigmoid(own);
@@ -723,12 +715,12 @@ topk_grad_kernel(const typename Element<DT>::type *__restrict__ logits, const in
     m = part_max<L>(m);
 #pragma unroll
     for (int i = 0; i < V; ++i) p[i] = p[i] == kNegInf ? 0.0f : expf(p[i] - m);
-    const float sum = part_sum<L>(tree_sum<V>(p));
+    const float sum = lanes_sum<L>(tree_sum<V>(p));
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
     for (int i = 0; i < V; ++i) p[i] *= inv;
     const float pj = own == kNegInf ? 0.0f : expf(own - m) * inv;
-    dot = part_sum<L>(has ? g * pj : 0.0f);
+    dot = lanes_sum<L>(has ? g * pj : 0.0f);
     value = g;
   } else {
     float u, slope;  // score over what all share, and d score / d logit over the same
@@ -744,9 +736,9 @@ topk_grad_kernel(const typename Element<DT>::type *__restrict__ logits, const in
     }
     if (!has) u = slope = 0.0f;
     if (a.norm) {
-      const float total = part_sum<L>(u);
+      const float total = lanes_sum<L>(u);
       const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-      const float mean = part_sum<L>(has ? g * u : 0.0f) * inv;
+      const float mean = lanes_sum<L>(has ? g * u : 0.0f) * inv;
       value = (g - mean) * (slope * inv);
     } else {
       value = g * slope;

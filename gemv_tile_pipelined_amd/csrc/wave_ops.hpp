@@ -59,6 +59,27 @@ __device__ inline double wave_sum_last(double v) {
   v = dpp_add<0x142, 0xA>(v);
   return dpp_add<0x143, 0xC>(v);
 }
+// Sums over each LANES lanes that follow one another (8 to 64), in every one of them.
+template <int LANES>
+__device__ inline float lanes_sum(float v) {
+  if constexpr (LANES == 64) return wave_sum(v);
+  v = dpp_add<0xB1>(v);
+  v = dpp_add<0x4E>(v);
+  v = dpp_add<0x141>(v);
+  if constexpr (LANES >= 16) v = dpp_add<0x140>(v);
+  if constexpr (LANES == 32) v += __shfl_xor(v, 16);
+  return v;
+}
+template <int LANES>
+__device__ inline double lanes_sum(double v) {
+  if constexpr (LANES == 64) return __shfl(wave_sum_last(v), 63);
+  v = dpp_add<0xB1>(v);
+  v = dpp_add<0x4E>(v);
+  v = dpp_add<0x141>(v);
+  if constexpr (LANES >= 16) v = dpp_add<0x140>(v);
+  if constexpr (LANES == 32) v += __shfl_xor(v, 16);
+  return v;
+}
 __device__ inline uint32_t wave_max(uint32_t v) {
   v = max_of_16_lanes(v);
   v = dpp_max<0x142, 0xA>(v);

@@ -91,6 +91,23 @@ def test_combine_gradient(env, T, k, K, fmt):
     near(host(got_w), want_w, tol_w)
 
 
+@pytest.mark.parametrize("T,k,K", [(900, 9, 256), (333, 4, 512), (50, 2, 520), (1001, 3, 128), (67, 5, 56)])
+def test_tokens_of_a_wave_apart(env, T, k, K):
+    """The gradients of tokens that share a wave or a workgroup, a NaN in some of them."""
+    test_combine_gradient(env, T, k, K, "bf16")
+    t = env.torch
+    r = np.random.default_rng(T)
+    pos = env.whole(_pos(r, T, k, T * k, 0.0))
+    D, dY, w = env.device(r.standard_normal((T * k, K)), "f16"), env.device(r.standard_normal((T, K)), "f16"), env.device(r.random((T, k)))
+    dD, dw = env.gt.route_combine_grad_f16(dY, D, pos, w)
+    bad = [0, 3, 33, T - 1]
+    keep = [i for i in range(T) if i not in bad]
+    dY[bad, 1] = float("nan")
+    dD2, dw2 = env.gt.route_combine_grad_f16(dY, D, pos, w)
+    at = pos[keep].flatten().long()
+    assert t.equal(dD2[at], dD[at]) and t.equal(dw2[keep], dw[keep]) and t.isnan(dw2[bad]).all()
+
+
 def test_nothing(env):
     t = env.torch
     pos = t.zeros(3, 2, dtype=t.int32, device="cuda")
