@@ -744,15 +744,25 @@ topk_grad_kernel(const typename Element<DT>::type *__restrict__ logits, const in
       value = g * slope;
     }
   }
-  // To the lanes that have the experts.
+  // To the lanes that have the experts, through LDS: pieces of W experts, those of
+  // neighbouring lanes beside one another.
+  constexpr int W = V < 4 ? V : 4;
+  typedef float Piece __attribute__((ext_vector_type(W)));
+  __shared__ __attribute__((aligned(16))) float spread[kWaves][64 / L][L * V];
+  float *const mine = spread[wave][part];
+#pragma unroll
+  for (int i = 0; i < V; i += W) *reinterpret_cast<Piece *>(mine + i * L + sub * W) = Piece(0.0f);
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  if (has) atomicAdd(mine + id % V / W * W * L + id / V * W + id % W, value);  // ids are different
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
   float out[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) out[i] = 0.0f;
-  for (int j = 0; j < a.k; ++j) {
-    const int e = __shfl(id, part * L + j);
-    const float v = __shfl(value, part * L + j);
+  for (int i = 0; i < V; i += W) {
+    const Piece v = *reinterpret_cast<const Piece *>(mine + i * L + sub * W);
 #pragma unroll
-    for (int i = 0; i < V; ++i) out[i] = sub * V + i == e ? out[i] + v : out[i];
+    for (int j = 0; j < W; ++j) out[i + j] = v[j];
   }
   if (dense) {
 #pragma unroll
@@ -989,6 +999,7 @@ hipError_t launch_topk_grad_dt(const void *logits, const int *ids, const float *
   }
   if (a.E <= 64) return launch_topk_grad_v<DT, 64, 1>(logits, ids, dweights, dlogits, T, a, stream);
   if (a.E <= 256) return launch_topk_grad_v<DT, 64, 4>(logits, ids, dweights, dlogits, T, a, stream);
+  if (a.E <= 512) return launch_topk_grad_v<DT, 64, 8>(logits, ids, dweights, dlogits, T, a, stream);
   return launch_topk_grad_v<DT, 64, 16>(logits, ids, dweights, dlogits, T, a, stream);
 }
 
