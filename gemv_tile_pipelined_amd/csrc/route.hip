@@ -16,7 +16,7 @@
 // and a maximum over the lanes through DPP; nothing is marked as taken, and the
 // key says whose it is.
 //
-// Bound by vector instructions, 276 a token of 256 experts (16384 tokens, 8 of 256 of
+// Bound by vector instructions, 280 a token of 256 experts (16384 tokens, 8 of 256 of
 // bf16 logits: 6.7 us, with a sigmoid and a bias 10.7, in 4 of 8 groups 12.1; with a
 // wave a token, as at 16 of 256, 13.2, 19.3 and 22.1).
 //
@@ -681,8 +681,10 @@ topk_kernel(const typename Element<DT>::type *__restrict__ logits, const float *
 //   sigmoid               dlogit_j = g_j c_j (1 - c_j)
 //   sigmoid, normalised   the same with (g_j - sum_i g_i w_i) / sum_i c_i for g_j, w = c / sum c
 // and 0 for experts not chosen.  Ids outside 0 .. E - 1 are left out.  Rows are written
-// whole, by the lanes that have the experts: 8200 tokens, 6 of 128, in 4.5 us, of which
-// bytes are 0.9 and the rest a launch and a chain of loads, reductions and stores.
+// whole, by the lanes that have the experts: 8200 tokens, 6 of 128, in 3.9 us, of which
+// bytes are 0.9 and the rest a launch and a chain of loads, reductions and stores
+// (16384 tokens, 8 of 256 4.6 us, of 512 6.3; without LDS, each lane comparing its
+// experts with each of the k, 6.0 and 10.8).
 template <int DT, int L, int V>
 __global__ void __launch_bounds__(kWaves * 64)
 topk_grad_kernel(const typename Element<DT>::type *__restrict__ logits, const int *__restrict__ ids,
