@@ -317,7 +317,8 @@ rmsnorm_grad_kernel(const uint16_t *__restrict__ dy, const uint16_t *__restrict_
     for (int i = 0; i < NV; ++i) {
       const int v = i * LANES + sub;
       if (v < vecs) {
-        float4_t *out = reinterpret_cast<float4_t *>(partial + static_cast<int64_t>(blockIdx.x) * C + 8 * v);
+        typedef float float4_u __attribute__((ext_vector_type(4), aligned(4)));  // dweight itself is 4-byte aligned
+        float4_u *out = reinterpret_cast<float4_u *>(partial + static_cast<int64_t>(blockIdx.x) * C + 8 * v);
         out[0] = kFar ? far[2 * i * LANES + sub] : float4_t{dw[i][0], dw[i][1], dw[i][2], dw[i][3]};
         out[1] = kFar ? far[(2 * i + 1) * LANES + sub] : float4_t{dw[i][4], dw[i][5], dw[i][6], dw[i][7]};
       }
@@ -393,14 +394,18 @@ hipError_t launch_norm_dt(const NormArgs &a, hipStream_t stream) {
 
 template <int DT, int LANES, int NV, int ROWS = 1, int PARTS = kNormParts, bool AHEAD = false>
 hipError_t launch_grad(const NormGradArgs &a, hipStream_t stream) {
-  const int parts = (a.T + ROWS - 1) / ROWS < PARTS ? (a.T + ROWS - 1) / ROWS : PARTS;
+  // Few rows are one workgroup's, whose partial sums are the result: one launch
+  // (us with one / two: 1 x 4096 2.6 / 4.7, 2 x 4096 3.2 / 4.9, 8 x 512 2.9 / 4.4, 64 x 64 3.0 / 4.4,
+  // 2 x 32768 13.1 / 12.3).
+  const int rounds = (a.T + ROWS - 1) / ROWS;
+  const int parts = rounds <= 2 ? (rounds > 0 ? 1 : 0) : rounds < PARTS ? rounds : PARTS;
   if (parts > 0) {  // without rows dweight is a sum of nothing
     hipLaunchKernelGGL((rmsnorm_grad_kernel<DT, LANES, NV, ROWS, AHEAD>), dim3(parts), dim3(LANES * ROWS), 0, stream,
                        static_cast<const uint16_t *>(a.dy), static_cast<const uint16_t *>(a.dh),
                        static_cast<const uint16_t *>(a.h), static_cast<const uint16_t *>(a.weight), a.rstd,
-                       static_cast<uint16_t *>(a.dx), a.workspace, a.T, a.C);
+                       static_cast<uint16_t *>(a.dx), parts == 1 ? a.dweight : a.workspace, a.T, a.C);
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess || parts == 1) return e;
   }
   hipLaunchKernelGGL(rmsnorm_reduce_kernel, dim3((a.C + kReduceCols - 1) / kReduceCols), dim3(kReduceCols * kReduceRuns), 0,
                      stream, a.workspace, a.dweight, parts, a.C);

@@ -166,6 +166,20 @@ def test_rows_of_a_wave_apart(env, C):
         assert t.equal(q2.view(t.uint8)[keep], q.view(t.uint8)[keep]) and t.equal(s2[keep], s[keep]) and t.isnan(s2[bad]).all()
 
 
+@pytest.mark.parametrize("T,C", [(1, 8), (2, 2048), (2, 4112), (1, 24584), (5, 64), (3, 4096)])
+def test_gradient_into_given(env, T, C):
+    """dweight at any 4-byte alignment, and nothing around it."""
+    t = env.torch
+    h, dy, w = _inputs(env, T, C, "bf16")
+    rstd = t.rand(T, device="cuda") + 0.5
+    space = env.gt.alloc_rmsnorm_grad_workspace(h)
+    want = env.gt.rmsnorm_grad_bf16(dy, h, w, rstd, workspace=space)
+    for at in (1, 2, 3):
+        dw = t.full((C + 8,), 7.0, device="cuda")
+        dx, got = env.gt.rmsnorm_grad_bf16(dy, h, w, rstd, dweight=dw[at : at + C], workspace=space)
+        assert t.equal(got, want[1]) and t.equal(dx, want[0]) and (dw[:at] == 7).all() and (dw[at + C :] == 7).all()
+
+
 def test_gradient_of_no_rows(env):
     t = env.torch
     e = t.empty(0, 64, device="cuda").half()
