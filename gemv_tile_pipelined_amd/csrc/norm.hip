@@ -78,9 +78,11 @@ __device__ inline double inverse_root(double v) {
 }
 
 // p (high + low) rounded to odd: the rounded product, one bit lower where it is
-// above the real one, with its last bit set unless it is that.
+// above the real one, with its last bit set unless it is that.  `low` is in the product
+// before it is rounded: p high alone can be more than a unit off, and one bit lower is
+// then still above.
 __device__ inline float product_to_odd(float p, float high, float low) {
-  const float q = p * high;
+  const float q = __builtin_fmaf(p, high, p * low);
   const float rest = __builtin_fmaf(p, low, __builtin_fmaf(p, high, -q));
   const float r = q < 0.0f ? -rest : rest;  // towards larger magnitudes
   uint32_t b = __builtin_bit_cast(uint32_t, q);
