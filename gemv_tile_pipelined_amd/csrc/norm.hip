@@ -77,18 +77,18 @@ __device__ inline double inverse_root(double v) {
   return r;
 }
 
-// p (high + low) rounded to odd: the rounded product, one bit lower where it is
-// above the real one, with its last bit set unless it is that.  `low` is in the product
+// p (high + low), high > 0, rounded to odd: the rounded product, one bit lower where it
+// is above the real one, with its last bit set unless it is that.  `low` is in the product
 // before it is rounded: p high alone can be more than a unit off, and one bit lower is
-// then still above.
+// then still above.  Magnitudes, and p's sign: that of a zero is kept.
 __device__ inline float product_to_odd(float p, float high, float low) {
-  const float q = __builtin_fmaf(p, high, p * low);
-  const float rest = __builtin_fmaf(p, low, __builtin_fmaf(p, high, -q));
-  const float r = q < 0.0f ? -rest : rest;  // towards larger magnitudes
+  const float a = __builtin_fabsf(p);
+  const float q = __builtin_fmaf(a, high, a * low);
+  const float rest = __builtin_fmaf(a, low, __builtin_fmaf(a, high, -q));
   uint32_t b = __builtin_bit_cast(uint32_t, q);
-  b -= r < 0.0f ? 1u : 0u;
-  b |= r != 0.0f ? 1u : 0u;
-  return __builtin_bit_cast(float, b);
+  b -= rest < 0.0f ? 1u : 0u;
+  b |= rest != 0.0f ? 1u : 0u;
+  return __builtin_copysignf(__builtin_bit_cast(float, b), p);
 }
 
 // h may be x or residual: a row's vectors are all read by the threads that write

@@ -69,3 +69,16 @@ def test_numbers_next_to_the_middle(env, T, C, fmt):
     weight = np.repeat(r.integers(128, 256, -(-C // 128)) / 128, 128)[:C]  # eight bits
     near = _check(env, env.device(h, fmt), env.device(weight, fmt), fmt)
     assert near >= 0.9 * T * C
+
+
+@FMT
+@pytest.mark.parametrize("C", [64, 272, 4096])
+def test_signs_of_zeros(env, C, fmt):
+    """Zeros, and numbers too small beside the block's largest, keep their signs."""
+    r = np.random.default_rng(C)
+    h = r.standard_normal((200, C)) * r.choice([0.0, 2.0**-13, 1.0], (200, C))
+    h = h * r.choice([-1, 1], (200, C))
+    _check(env, env.device(h, fmt), env.device(1 + 0.1 * r.standard_normal(C), fmt), fmt)
+    q = env.call("rmsnorm_fp8", fmt)(env.device(h, fmt), env.device(np.ones(C), fmt), None, EPS)[0]
+    signs = q.view(env.torch.uint8).cpu().numpy() >> 7
+    np.testing.assert_array_equal(signs, np.signbit(h))
