@@ -216,9 +216,9 @@ def load_library(path: str = LIBRARY_PATH) -> ctypes.CDLL:
             call = getattr(lib, f"{name}_{fmt}")
             call.argtypes = [*args, vp]
             call.restype = c_int
-    f32 = ctypes.c_float
+    f32, f64 = ctypes.c_float, ctypes.c_double
     for name, args in (("quantize_fp4", [vp] * 3 + [i64] * 2), ("gemv_fp4", [vp] * 4 + [i64] * 3),
-                       ("rmsnorm", [vp] * 6 + [i64] * 2 + [f32]), ("rmsnorm_fp8", [vp] * 8 + [i64] * 2 + [f32]),
+                       ("rmsnorm", [vp] * 6 + [i64] * 2 + [f64]), ("rmsnorm_fp8", [vp] * 8 + [i64] * 2 + [f64]),
                        ("rmsnorm_grad", [vp] * 7 + [i64] * 2 + [vp, i64]),
                        ("route_topk", [vp] * 4 + [i64] * 5 + [c_int] * 3 + [f32]),
                        ("route_topk_grad", [vp] * 4 + [i64] * 3 + [c_int] * 2 + [f32]),

@@ -389,7 +389,7 @@ struct NormArgs {
   void *h, *y, *q;
   float *scale, *rstd;
   int T, C;
-  float eps;
+  double eps;
 };
 hipError_t launch_rmsnorm(int dtype, const NormArgs &a, hipStream_t stream);
 struct NormGradArgs {

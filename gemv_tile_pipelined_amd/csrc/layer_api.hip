@@ -47,8 +47,8 @@ int run_gemv_fp4(int dtype, const void *x, const void *W, const void *sW, void *
 
 // fp8: q and scale wanted, y optional; otherwise y wanted.
 int run_rmsnorm(int dtype, bool fp8, const void *x, const void *residual, const void *weight, void *h, void *y, void *q,
-                float *scale, float *rstd, int64_t T, int64_t C, float eps, void *stream) {
-  if (T < 0 || C < 0 || !(eps >= 0.0f)) return GEMVTILE_ERR_INVALID_ARG;
+                float *scale, float *rstd, int64_t T, int64_t C, double eps, void *stream) {
+  if (T < 0 || C < 0 || !(eps >= 0.0)) return GEMVTILE_ERR_INVALID_ARG;
   if ((residual == nullptr) != (h == nullptr)) {
     if (T > 0 && C > 0) return GEMVTILE_ERR_INVALID_ARG;
   }
@@ -197,11 +197,11 @@ int route_gather_fp8(const void *X, const float *scale, const int32_t *pos, void
     return run_gemv_fp4(dtype, x, W, scale_W, y, M, N, K, stream);                                                            \
   }                                                                                                                           \
   int rmsnorm_##fmt(const void *x, const void *residual, const void *weight, void *h, void *y, float *rstd, int64_t T,        \
-                    int64_t C, float eps, void *stream) {                                                                     \
+                    int64_t C, double eps, void *stream) {                                                                    \
     return run_rmsnorm(dtype, false, x, residual, weight, h, y, nullptr, nullptr, rstd, T, C, eps, stream);                   \
   }                                                                                                                           \
   int rmsnorm_fp8_##fmt(const void *x, const void *residual, const void *weight, void *h, void *y, void *q, float *scale,     \
-                        float *rstd, int64_t T, int64_t C, float eps, void *stream) {                                         \
+                        float *rstd, int64_t T, int64_t C, double eps, void *stream) {                                        \
     return run_rmsnorm(dtype, true, x, residual, weight, h, y, q, scale, rstd, T, C, eps, stream);                            \
   }                                                                                                                           \
   int rmsnorm_grad_##fmt(const void *dy, const void *dh, const void *h, const void *weight, const float *rstd, void *dx,      \

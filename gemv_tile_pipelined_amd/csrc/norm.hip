@@ -97,7 +97,7 @@ template <int DT, int LANES, int NV, int ROWS, bool FP8>
 __global__ void __launch_bounds__(LANES *ROWS)
 rmsnorm_kernel(const uint16_t *x, const uint16_t *residual, const uint16_t *__restrict__ weight, uint16_t *h,
                uint16_t *__restrict__ y, uint8_t *__restrict__ q, float *__restrict__ scale, float *__restrict__ rstd, int T,
-               int C, float eps) {
+               int C, double eps) {
   __shared__ double slots[2][(LANES + 63) / 64];
   const int group = row_group<LANES, ROWS>(), sub = static_cast<int>(threadIdx.x) - group * LANES;
   const int vecs = C / 8, blocks = (C + kScaleBlock - 1) / kScaleBlock;
@@ -148,7 +148,7 @@ rmsnorm_kernel(const uint16_t *x, const uint16_t *residual, const uint16_t *__re
       for (int j = 0; j < 8; ++j) sum = __builtin_fma(static_cast<double>(a[j]), static_cast<double>(a[j]), sum);
     }
     sum = row_sum<LANES>(sum, slots[turn]);
-    const double rd = inverse_root(sum * inv_c + static_cast<double>(eps));
+    const double rd = inverse_root(sum * inv_c + eps);
     const float r = static_cast<float>(rd);
     if (rstd != nullptr && sub == 0) rstd[row] = r;
 #pragma unroll

@@ -699,7 +699,7 @@ int gemv_fp4_bf16(const void *x, const void *W, const void *scale_W, void *y, in
  *   scale, rstd                       4-byte aligned; rstd [T] takes r for the
  *            gradient, or NULL
  *   T, C     >= 0; T <= 2^31 - 512, C <= 32768, C % 8 == 0 (16 for rmsnorm_fp8_*)
- *   eps      >= 0; the sum of squares and r are computed in FP64
+ *   eps      >= 0, in FP64, as the sum of squares and r are
  * T == 0 or C == 0 touches nothing.
  *
  * rmsnorm_grad_f16, _bf16 -- the gradients, given dy, h, weight and rstd, and dh, the
@@ -719,13 +719,13 @@ int gemv_fp4_bf16(const void *x, const void *W, const void *scale_W, void *y, in
  *   T, C     as above, C % 8 == 0.  T == 0 fills dweight with zeros.
  */
 int rmsnorm_f16(const void *x, const void *residual, const void *weight, void *h, void *y, float *rstd, int64_t T,
-                int64_t C, float eps, void *stream);
+                int64_t C, double eps, void *stream);
 int rmsnorm_bf16(const void *x, const void *residual, const void *weight, void *h, void *y, float *rstd, int64_t T,
-                 int64_t C, float eps, void *stream);
+                 int64_t C, double eps, void *stream);
 int rmsnorm_fp8_f16(const void *x, const void *residual, const void *weight, void *h, void *y, void *q, float *scale,
-                    float *rstd, int64_t T, int64_t C, float eps, void *stream);
+                    float *rstd, int64_t T, int64_t C, double eps, void *stream);
 int rmsnorm_fp8_bf16(const void *x, const void *residual, const void *weight, void *h, void *y, void *q, float *scale,
-                     float *rstd, int64_t T, int64_t C, float eps, void *stream);
+                     float *rstd, int64_t T, int64_t C, double eps, void *stream);
 int rmsnorm_grad_f16(const void *dy, const void *dh, const void *h, const void *weight, const float *rstd, void *dx,
                      float *dweight, int64_t T, int64_t C, void *workspace, int64_t workspace_bytes, void *stream);
 int rmsnorm_grad_bf16(const void *dy, const void *dh, const void *h, const void *weight, const float *rstd, void *dx,

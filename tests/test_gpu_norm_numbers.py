@@ -82,3 +82,21 @@ def test_signs_of_zeros(env, C, fmt):
     q = env.call("rmsnorm_fp8", fmt)(env.device(h, fmt), env.device(np.ones(C), fmt), None, EPS)[0]
     signs = q.view(env.torch.uint8).cpu().numpy() >> 7
     np.testing.assert_array_equal(signs, np.signbit(h))
+
+
+@FMT
+@pytest.mark.parametrize("eps", [1e-6, 1e-5, 0.1])
+@pytest.mark.parametrize("size", [0.1, 1.0, 3.0])
+def test_eps_counts(env, size, eps, fmt):
+    """Rows whose mean square is about eps: half of what r is off by comes from eps, whole in 64 bits."""
+    r = np.random.default_rng(7)
+    h = r.standard_normal((2000, 1024)) * size * eps**0.5
+    _check(env, env.device(h, fmt), env.device(1 + 0.1 * r.standard_normal(1024), fmt), fmt, eps)
+
+
+def test_eps_of_no_fp32_number(env):
+    """An eps below FP32's range is not zero: a row of zeros has zeros, not NaN."""
+    t = env.torch
+    x, rstd = t.zeros(3, 256, device="cuda").bfloat16(), t.empty(3, device="cuda")
+    y, _ = env.gt.rmsnorm_bf16(x, t.ones(256, device="cuda").bfloat16(), None, 1e-60, rstd=rstd)
+    assert not y.any() and (np.abs(host(rstd) - 1e30) <= NEAREST * 1e30).all()
