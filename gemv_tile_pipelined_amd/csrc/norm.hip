@@ -91,6 +91,24 @@ __device__ inline float product_to_odd(float p, float high, float low) {
   return __builtin_copysignf(__builtin_bit_cast(float, b), p);
 }
 
+// Rows whose r is outside this are multiplied in FP64: below, it is no normal FP32 number;
+// above, a product weight h that FP32 does not hold exactly (below 2^-134) may stand for
+// more than a zero of e4m3 (2^-90 and less).  So are blocks whose weight h leaves FP32's
+// range, as y need not.
+constexpr double kLeastRoot = 0x1p-126, kMostRoot = 0x1p40;
+// The power of two that brings r to 2^9 .. 2^10, and weight h r 2^-that (at most 2^136)
+// into FP32.
+__device__ inline int root_exponent(double r) {
+  return r == 0.0 ? -300 : r < __builtin_inf() ? __builtin_amdgcn_frexp_exp(r) - 10 : 0;
+}
+
+// A number in FP64, converted where it is needed: the compiler would otherwise keep those
+// of the sum of squares, and of the weight over all rows, in registers for it.
+__device__ inline double afresh(float v) {
+  asm volatile("" : "+v"(v));
+  return static_cast<double>(v);
+}
+
 // h may be x or residual: a row's vectors are all read by the threads that write
 // them, before they do.
 template <int DT, int LANES, int NV, int ROWS, bool FP8>
@@ -151,6 +169,7 @@ rmsnorm_kernel(const uint16_t *x, const uint16_t *residual, const uint16_t *__re
     const double rd = inverse_root(sum * inv_c + eps);
     const float r = static_cast<float>(rd);
     if (rstd != nullptr && sub == 0) rstd[row] = r;
+    const bool far = !(rd >= kLeastRoot && rd <= kMostRoot);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = i * LANES + sub;
@@ -159,9 +178,15 @@ rmsnorm_kernel(const uint16_t *x, const uint16_t *residual, const uint16_t *__re
       widen8<DT>(wv[i], w);
       if (y != nullptr) {
         float out[8];
+        if (__builtin_expect(far, 0)) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) out[j] = static_cast<float>(afresh(a[j]) * rd * afresh(w[j]));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) out[j] = a[j] * r * w[j];
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          out[j] = a[j] * r * w[j];
           // y is an FP32 number in every variant: not a product that v_fma_mix*
           // rounds to half precision with it.
           asm volatile("" : "+v"(out[j]));
@@ -169,17 +194,30 @@ rmsnorm_kernel(const uint16_t *x, const uint16_t *residual, const uint16_t *__re
         if (v < vecs) reinterpret_cast<uint4_v *>(y + row * C)[v] = round8<DT>(out);
       }
       if constexpr (FP8) {
-        uint32_t top = 0;  // of |weight h|, as bits: NaN above infinity above the rest
+        const auto block_max = [&] {  // as bits: NaN above infinity above the rest
+          uint32_t top = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          a[j] *= w[j];
-          const uint32_t bits = __builtin_bit_cast(uint32_t, a[j]) & 0x7fffffffu;
-          top = bits > top ? bits : top;
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t bits = __builtin_bit_cast(uint32_t, a[j]) & 0x7fffffffu;
+            top = bits > top ? bits : top;
+          }
+          return LANES == 8 ? max_of_8_lanes(top) : max_of_16_lanes(top);
+        };
+        double root = rd;  // y is a[] times root
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a[j] *= w[j];
+        uint32_t top = block_max();
+        if (__builtin_expect(far || top >= 0x7f800000u, 0)) {  // a block's lanes alike
+          const int e = root_exponent(rd);
+          root = __builtin_ldexp(rd, -e);
+          widen8<DT>(hv[i], a);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) a[j] = static_cast<float>(__builtin_ldexp(afresh(a[j]) * afresh(w[j]), e));
+          top = block_max();
         }
-        const double amax = static_cast<double>(__builtin_bit_cast(float, LANES == 8 ? max_of_8_lanes(top) : max_of_16_lanes(top)));
-        float s = static_cast<float>(amax * rd * (1.0 / 448.0));
+        float s = static_cast<float>(static_cast<double>(__builtin_bit_cast(float, top)) * root * (1.0 / 448.0));
         s = s < kMinScale ? kMinScale : s;  // a NaN stays
-        const double t = rd / static_cast<double>(s);
+        const double t = root / static_cast<double>(s);
         const float high = static_cast<float>(t), low = static_cast<float>(t - static_cast<double>(high));
 #pragma unroll
         for (int j = 0; j < 8; ++j) a[j] = product_to_odd(a[j], high, low);

@@ -699,7 +699,10 @@ int gemv_fp4_bf16(const void *x, const void *W, const void *scale_W, void *y, in
  *   scale, rstd                       4-byte aligned; rstd [T] takes r for the
  *            gradient, or NULL
  *   T, C     >= 0; T <= 2^31 - 512, C <= 32768, C % 8 == 0 (16 for rmsnorm_fp8_*)
- *   eps      >= 0, in FP64, as the sum of squares and r are
+ *   eps      >= 0, in FP64, as the sum of squares and r are; rstd is r rounded to FP32.
+ *            y in 16 bits is rounded from an FP32 number, made of r and h * r in FP32;
+ *            q is the number nearest to y / scale, whatever the sizes of h, weight and
+ *            r (a row of zeros over an eps of 0 is NaN)
  * T == 0 or C == 0 touches nothing.
  *
  * rmsnorm_grad_f16, _bf16 -- the gradients, given dy, h, weight and rstd, and dh, the
