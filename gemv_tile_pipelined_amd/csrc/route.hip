@@ -397,6 +397,9 @@ topk_kernel(const typename Element<DT>::type *__restrict__ logits, const float *
     for (int i = 0; i < V; ++i) nan |= logit[i] != logit[i];
     nan = part_any<L>(nan, lane);
   }
+  // A softmax beside an infinite logit is NaN, whatever is chosen.  (Where the largest logit
+  // is not known, it is among the chosen ones.)
+  nan |= top_logit == __builtin_inff();
 
   // ---- groups: value[] is what they count by
   uint32_t dropped = 0;  // experts of this lane (as bits) in groups that are not kept

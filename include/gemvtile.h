@@ -758,9 +758,10 @@ enum gemvtile_score {
  * of -inf is an expert with score 0, chosen after all others unless a bias lifts it (a
  * bias of -inf does not); where every score that is divided by is 0 (all logits -inf)
  * the weights are 0.  A NaN choice (of the logit or the bias) ranks below all others.
- * With softmax a NaN or +inf among a token's logits makes its weights NaN (and with a
- * bias, or sums of two, every choice: ids are the lowest then); with a sigmoid a NaN
- * logit does so where it is chosen.  Ids are always k different numbers of 0 .. E - 1.
+ * With softmax a NaN or +inf among a token's logits makes its weights NaN, and with a
+ * bias every choice (ids are the lowest then), with sums of two and no bias those sums
+ * (the lowest groups are kept, and in them the largest logits); with a sigmoid a NaN
+ * logit makes the weights NaN where it is chosen.  Ids are always k different numbers of 0 .. E - 1.
  *
  *   logits   [T,E] fp16 / bf16 / FP32, 16-byte aligned
  *   bias     [E] FP32 or NULL; ids, weights 4-byte aligned
