@@ -8,20 +8,24 @@
 //
 //   y[m,n] = sum_b 2^(s[n,b] - 127) * sum_{k in block b} x[m,k] * W[n,k]
 //
-// The product reads 17 bytes of W for 32 numbers, each once, and is bound by
-// that.  One v_cvt_scalef32_pk_*_fp4 turns a byte into two numbers of x's format
+// The product reads 17 bytes of W for 32 numbers and is bound by that for one token: each
+// is read once by up to 48 rows of x, by fewer where gemv_shape has several workgroups
+// read the same.  One v_cvt_scalef32_pk_*_fp4 turns a byte into two numbers of x's format
 // times the scale, and 16-bit MFMAs (16x16x32) multiply exactly and add in FP32.
 // Lane n + 16 g of a wave holds the whole block g of four that follow one another
 // in row n, and as many of x: an MFMA takes 8 numbers of each of the four blocks.
 //
 // That is exact where scaled numbers are numbers of the 16-bit format: scales of
 // 2^-125 to 2^125 in bf16, 2^-23 to 2^13 in half precision, which weights have.
-// Four blocks with another scale among them (blocks of zeros have the smallest),
-// and those at a ragged end of K, take the exact way for any scale: numbers
+// Four blocks with another scale among them in a workgroup's rows (blocks of zeros have
+// the smallest), and those at a ragged end of K, take the exact way for any scale: numbers
 // converted without it, one MFMA for each block, whose sum is then scaled in FP32.
 // That wants all four lane rows to hold 8 numbers each of one block, which is the
 // transpose of 4 x 4 dwords across lane rows (two v_permlane32_swap and two
-// v_permlane16_swap), of W and of x.
+// v_permlane16_swap), of W and of x.  It costs up to half as much again (1, 27 and 64 rows
+// of 4096x14336, 8195x4128 and 4096x14336: 8.0, 10.9 and 18.0 us without a block of zeros,
+// 8.8, 12.2 and 20.6 with one in 1000, 10.7, 14.1 and 25.9 with one in 100, 11.7, 14.4 and
+// 27.9 with zeros only), and sums come in another order.
 //
 // Loads go straight to LDS.  A wave's 64 x 16 bytes are 16 rows of 64 bytes: where
 // neighbouring lanes load from the rows of an MFMA's operand, 16 different cache

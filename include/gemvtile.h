@@ -665,9 +665,14 @@ int64_t gemvtile_group_unit(const int32_t *offsets, int64_t E, int64_t T, int64_
  *
  *   y[m,n] = sum_b 2^(scale_W[n,b] - 127) * sum_{k in block b} x[m,k] * W[n,k]
  *
- * Products are exact; a block's are added in FP32, then scaled and added in FP32.
+ * Products are exact and added in FP32: scaled before they are added, or, where the
+ * scaled numbers are none of the 16-bit format's (scales outside 2^-125 .. 2^125 in bf16,
+ * 2^-23 .. 2^13 in fp16) and at a ragged end of K, a block's first and then scaled.  Four
+ * blocks of K and up to 64 rows of W go one way together, so the last bits of an output
+ * may depend on the scales of rows beside its own; the same call gives the same bits.
+ * Where the magnitudes |x W|, scaled or not, add up to 2^128, y may be infinite or NaN.
  * Meant for decode batches: up to 48 rows share what a workgroup reads of W, fewer
- * where more workgroups make up for reading it again.
+ * where more workgroups make up for reading it again; more rows read it again.
  *   x        [M,K] fp16 / bf16, 16-byte aligned
  *   W        [N,K/2] bytes, 16-byte aligned;  scale_W  [N,K/32] bytes
  *   y        [M,N] fp16 / bf16, 2-byte aligned
