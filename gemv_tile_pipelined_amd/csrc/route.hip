@@ -759,7 +759,7 @@ topk_grad_kernel(const typename Element<DT>::type *__restrict__ logits, const in
   for (int i = 0; i < V; i += W) *reinterpret_cast<Piece *>(mine + i * L + sub * W) = Piece(0.0f);
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
-  if (has) atomicAdd(mine + id % V / W * W * L + id / V * W + id % W, value);  // ids are different
+  if (has) mine[id % V / W * W * L + id / V * W + id % W] = value;  // ids are different
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
   float out[V];

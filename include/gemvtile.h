@@ -775,8 +775,8 @@ enum gemvtile_score {
  *
  * route_topk_grad_f16, _bf16, _f32 -- dlogits [T,E] (16-byte aligned, the logits'
  * type, written whole, one rounding) for dweights [T,k], with the ids held fixed as
- * the choice among them is not differentiated.  The ids of a token are different;
- * one outside 0 .. E - 1 is left out.
+ * the choice among them is not differentiated.  The ids of a token are different (of
+ * one that is not, one of its places counts); one outside 0 .. E - 1 is left out.
  */
 int route_topk_f16(const void *logits, const float *bias, int32_t *ids, float *weights, int64_t T, int64_t E, int64_t k,
                    int64_t groups, int64_t top_groups, int group_best, int score, int norm, float scale, void *stream);

@@ -58,3 +58,29 @@ def test_a_sigmoid_of_an_infinite_logit(env, fmt):
                 ids, w = env.call("route_topk", fmt)(env.device(l, fmt), 6, bias, groups, top, best, "sigmoid", norm)
                 want_ids, want_w = env.call("route_topk", fmt)(env.device(finite, fmt), 6, bias, groups, top, best, "sigmoid", norm)
                 assert env.torch.equal(ids, want_ids) and env.torch.equal(w, want_w)
+
+
+@FMT
+@pytest.mark.parametrize("T,E,k", [(9, 64, 8), (70, 256, 14), (5, 600, 32)])
+def test_gradient_of_an_id_that_stands_twice(env, T, E, k, fmt):
+    """Ids of a token are different; where one stands more than once in spite of that, one of its places counts for it, the
+    same one in every call, and other experts and tokens are as they are."""
+    t = env.torch
+    r = np.random.default_rng(E)
+    l, g = env.device(r.standard_normal((T, E)), fmt), env.device(r.standard_normal((T, k)))
+    ids, _ = env.call("route_topk", fmt)(l, k, None, 1, 1, 1, "sigmoid", False)
+    grad = env.call("route_topk_grad", fmt)
+    want = grad(l, ids, g, "sigmoid", False)
+    twice = ids.clone()
+    twice[2, 1], twice[2, 2] = ids[2, 0], ids[2, 0]
+    single = []
+    for j in range(3):
+        only = t.full_like(ids, -1)
+        only[2, j] = ids[2, 0]
+        single.append(grad(l, only, g, "sigmoid", False)[2, int(ids[2, 0])].item())
+    got = grad(l, twice, g, "sigmoid", False)
+    for _ in range(20):
+        assert t.equal(grad(l, twice, g, "sigmoid", False), got)
+    assert got[2, int(ids[2, 0])].item() in single and not got[2, ids[2, 1:3].long()].any()
+    got[2, ids[2, :3].long()] = want[2, ids[2, :3].long()]
+    assert t.equal(got, want)
