@@ -38,13 +38,24 @@ namespace {
 constexpr int kWaves = 4;  // of a workgroup
 constexpr float kNegInf = -__builtin_inff();
 
-// What FP32 scores can be off, u = 2^-24.  fast_exp(v) is off by |v| + 2 units.  A
-// sigmoid's share of that is s (1 - s) (|v| + 2) <= 0.6 u, its sum and reciprocal are
-// 3 u more: 4 u.  A softmax is off by e^v (|v| + 2) <= 2.4 u over the sum, the sum of
-// E <= 1024 exponentials, added in a tree of 4 + 6 levels, by 10 u and what they are
-// off, quotient and product by 3: 16 u of the token's largest score.  Adding a bias
-// rounds by u of the choice.  A choice x that is far below in FP32 cannot be ahead of
-// c in truth, however large it is: it would take |x| within 2^-22 of |c|.
+// What FP32 scores can be off, u = 2^-24.  fast_exp(v) of either sign is off by
+// (1.25 |v| + 2) u of itself: the product with log2(e), that number's own rounding, and the
+// instruction's unit in the last place.
+//
+// Sigmoid: s (1 - s) (1.25 |v| + 2) <= 0.7 u, its sum and reciprocal 3 u more: 4 u.
+//
+// Softmax, v = logit - largest, rounded: an exponential is off by (2.25 |v| + 2) u of itself,
+// at most 2.1 u of the largest one.  Their sum over E <= 1024 is off by what they are off in
+// the mean, (2.25 * 4.44 + 2) u (the mean of |v| is largest, 4.44, with one logit on top and
+// 1023 of them 5.44 below), and by 10 u for a tree of 4 + 6 levels: with its reciprocal 23 u.
+// That factor is all scores' alike, so of the difference of two it is 23 u of the difference,
+// which is at most the largest score p; with the exponentials and their products, 3.1 u of p
+// each, two scores' difference is off by at most 30 u of p, two sums of two by 59 u.  Twice
+// score_error, 32 u of p, is in the margin of two choices; twice that, 64 u, in that of two
+// groups.
+//
+// Adding a bias rounds by u of the choice.  A choice x that is far below in FP32 cannot be
+// ahead of c in truth, however large it is: it would take |x| within 2^-22 of |c|.
 __device__ inline float score_error(bool softmax, float top_score) { return softmax ? 0x1p-20f * top_score : 0x1p-22f; }
 // How far apart two choices have to be; `step` is that of the keys.
 __device__ inline float choice_margin(float score_error, float a, float b, float step) {
@@ -299,7 +310,7 @@ __device__ inline bool part_any(bool v, int lane) {
   if constexpr (L == 64) return b != 0;
   return ((b >> (lane & 48)) & 0xffffu) != 0;
 }
-// e^v for v <= 0 by the hardware's power of two: off by |v| 2^-24 and two units.
+// e^v by the hardware's power of two; what it is off stands at score_error.
 __device__ inline float fast_exp(float v) { return __builtin_amdgcn_exp2f(v * 0x1.715476p+0f); }
 __device__ inline float fast_sigmoid(float v) { return __builtin_amdgcn_rcpf(1.0f + fast_exp(-v)); }
 

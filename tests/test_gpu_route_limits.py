@@ -84,3 +84,60 @@ def test_gradient_of_an_id_that_stands_twice(env, T, E, k, fmt):
     assert got[2, int(ids[2, 0])].item() in single and not got[2, ids[2, 1:3].long()].any()
     got[2, ids[2, :3].long()] = want[2, ids[2, :3].long()]
     assert t.equal(got, want)
+
+
+@pytest.mark.parametrize("E", [64, 256, 512, 1024])
+def test_decisions_beside_the_error_of_a_large_sum(env, E):
+    """One logit on top and all others as far below as makes a softmax's sum most uncertain, with biases that bring their
+    choices within a few units of FP32 of the one on top, and of one another."""
+    r = np.random.default_rng(E)
+    below = {64: 2.9, 256: 4.1, 512: 4.8, 1024: 5.44}[E]
+    T = 250
+    l = -below + r.standard_normal((T, E)) * 2.0**-12
+    l[:, 0] = r.standard_normal(T) * 2.0**-14
+    logits = env.device(l)
+    p = ref.scores(host(logits), "softmax")
+    bias = env.device(np.where(np.arange(E) == 0, 0, p[:, :1].mean() - p.mean(0)) + r.integers(-24, 25, E) * 2.0**-27)
+    for k, groups, top, best in ((3, 1, 1, 1), (12, 1, 1, 1), (6, 8, 3, 1), (6, 8, 3, 2), (1, 16, 1, 2)):
+        ids, w = env.gt.route_topk_f32(logits, k, bias, groups, top, best, "softmax", True)
+        want_ids, want_w = ref.topk(host(logits), k, host(bias), groups, top, best, "softmax", 1, 1.0)
+        np.testing.assert_array_equal(host(ids), want_ids)
+        near(host(w), want_w, ref.topk_slack(host(logits), want_ids, want_w))
+    ids = env.gt.route_topk_f32(logits, 6, None, 8, 3, 2, "softmax", True)[0]
+    np.testing.assert_array_equal(host(ids), ref.topk(host(logits), 6, None, 8, 3, 2, "softmax", 1, 1.0)[0])
+
+
+@FMT
+@pytest.mark.parametrize("E", [16, 64, 250, 256, 512, 1024])
+def test_a_bias_at_any_place(env, E, fmt):
+    """A bias that is only 4-byte aligned."""
+    r = np.random.default_rng(E)
+    l, b = env.device(r.standard_normal((40, E)), fmt), env.device(r.standard_normal(E) * 0.1)
+    want = env.call("route_topk", fmt)(l, 6, b, 2, 1, 2, "sigmoid")
+    for at in (1, 2, 3):
+        there = env.torch.full((E + 8,), 9.0, device="cuda")
+        there[at : at + E] = b
+        got = env.call("route_topk", fmt)(l, 6, there[at : at + E], 2, 1, 2, "sigmoid")
+        assert env.torch.equal(got[0], want[0]) and env.torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("fmt,T,E", [("f32", 1100000, 1024), ("bf16", 4300000, 512)])
+def test_tokens_beyond_32_bits(env, fmt, T, E):
+    """Logits and gradients beyond 2^32 bytes."""
+    t = env.torch
+    l = t.zeros(T, E, dtype=env.types[fmt], device="cuda")
+    rows = t.tensor([0, 1, T // 2, T - 2, T - 1], device="cuda")
+    r = np.random.default_rng(8)
+    few = env.device(r.standard_normal((5, E)), fmt)
+    l[rows] = few
+    ids, w = env.call("route_topk", fmt)(l, 8)
+    want_ids, want_w = env.call("route_topk", fmt)(few, 8)
+    assert t.equal(ids[rows], want_ids) and t.equal(w[rows], want_w)
+    other = t.ones(T, dtype=t.bool, device="cuda")
+    other[rows] = False
+    assert (ids[other] == t.arange(8, device="cuda")).all() and (w[other] == 0.125).all()
+    g = t.zeros(T, 8, device="cuda")
+    g[rows] = env.device(r.standard_normal((5, 8)))
+    d = env.call("route_topk_grad", fmt)(l, ids, g)
+    assert t.equal(d[rows], env.call("route_topk_grad", fmt)(few, want_ids, g[rows]))
+    assert int(d.count_nonzero()) == int(d[rows].count_nonzero())
