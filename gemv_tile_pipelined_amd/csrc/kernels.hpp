@@ -399,8 +399,9 @@ struct NormGradArgs {
   float *dweight, *workspace;
   int T, C;
 };
-// Rows of partial sums of dweight that the gradient of T rows leaves in its
-// workspace.
+// Rows of partial sums of dweight that the workspace of the gradient of T rows has
+// room for: the most that any of its launches leaves there (those of few rows
+// leave none, those of long ones half as many).
 int rmsnorm_grad_parts(int64_t T);
 hipError_t launch_rmsnorm_grad(int dtype, const NormGradArgs &a, hipStream_t stream);
 // route.hip; dtype kF16, kBF16 or kF32 (logits only).

@@ -395,7 +395,8 @@ rmsnorm_reduce_kernel(const float *__restrict__ partial, float *__restrict__ dwe
 // 48.3 and 46.3 to 48.
 constexpr int kNormGrid = 16384;
 // Workgroups of the gradient at most, each with a row of partial sums; half as many for
-// long rows, whose partial sums are bytes that count.
+// long rows, whose partial sums are bytes that count.  The workspace has room for
+// kNormParts of them, or one for each row, whatever the columns.
 constexpr int kNormParts = 512, kLongRowParts = 256;
 
 template <int DT, int LANES, int NV, int ROWS = 1>
@@ -437,6 +438,7 @@ hipError_t launch_grad(const NormGradArgs &a, hipStream_t stream) {
   // Few rows are one workgroup's, whose partial sums are the result: one launch
   // (us with one / two: 1 x 4096 2.6 / 4.7, 2 x 4096 3.2 / 4.9, 8 x 512 2.9 / 4.4, 64 x 64 3.0 / 4.4,
   // 2 x 32768 13.1 / 12.3).
+  static_assert(PARTS <= kNormParts && ROWS >= 1, "the partial sums fit rmsnorm_grad_parts rows");
   const int rounds = (a.T + ROWS - 1) / ROWS;
   const int parts = rounds <= 2 ? (rounds > 0 ? 1 : 0) : rounds < PARTS ? rounds : PARTS;
   if (parts > 0) {  // without rows dweight is a sum of nothing

@@ -722,8 +722,8 @@ int gemv_fp4_bf16(const void *x, const void *W, const void *scale_W, void *y, in
  *            overlaps nothing
  *   workspace  gemvtile_rmsnorm_grad_workspace(T, C) bytes of device memory, owned
  *            by the caller, 16-byte aligned; its contents do not matter.  Too small
- *            or NULL: GEMVTILE_ERR_INVALID_ARG.  Calls that share one have to be
- *            ordered, captured ones included
+ *            or NULL: GEMVTILE_ERR_INVALID_ARG, also where few rows make no use of it.
+ *            Calls that share one have to be ordered, captured ones included
  *   T, C     as above, C % 8 == 0.  T == 0 fills dweight with zeros.
  */
 int rmsnorm_f16(const void *x, const void *residual, const void *weight, void *h, void *y, float *rstd, int64_t T,
