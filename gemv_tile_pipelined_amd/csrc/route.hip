@@ -182,12 +182,19 @@ struct TopkArgs {
 
 // ---- the choice in FP64 --------------------------------------------------------
 // By a whole wave for one token: lane j < k gets the id of the j-th choice.  `buf`
-// holds E numbers of the wave's own.  Few tokens come here, so the code is never in
-// the instruction cache and its length is what it costs: loops, nothing unrolled.
+// holds E numbers of the wave's own, choices (their bits) and then keys.  Few tokens come
+// here, so the code is never in the instruction cache and its length is what it costs:
+// loops, nothing unrolled.
 template <int DT>
 __device__ __attribute__((always_inline)) inline int choose_exactly(const typename Element<DT>::type *row, const float *bias, TopkArgs a,
-                                                        double *buf) {
+                                                        uint64_t *buf) {
   typedef KeyOf<double> Keys;
+  const auto put = [&](int e, double v) { buf[e] = __builtin_bit_cast(uint64_t, v); };
+  const auto get = [&](int e) { return __builtin_bit_cast(double, buf[e]); };
+  // What the wave read of this memory before (another token's keys, numbers in FP32) has
+  // been read.
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
   const int lane = threadIdx.x & 63;
   const bool softmax = a.score == GEMVTILE_SCORE_SOFTMAX;
   const int size = a.E / a.groups;
@@ -216,7 +223,7 @@ __device__ __attribute__((always_inline)) inline int choose_exactly(const typena
       sum += p;
       v = softmax ? p : (l < 0 ? p : 1) / (1 + p);
     }
-    buf[e] = v;
+    put(e, v);
   }
   if (scored && softmax) {
     sum = wave_add(sum);
@@ -224,7 +231,7 @@ __device__ __attribute__((always_inline)) inline int choose_exactly(const typena
   }
 #pragma clang loop unroll(disable)
   for (int e = lane; e < a.E; e += 64)
-    if (scored) buf[e] = buf[e] / inv + (bias != nullptr ? static_cast<double>(bias[e]) : 0.0);
+    if (scored) put(e, get(e) / inv + (bias != nullptr ? static_cast<double>(bias[e]) : 0.0));
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
   uint64_t kept = 1;
@@ -232,11 +239,11 @@ __device__ __attribute__((always_inline)) inline int choose_exactly(const typena
     // Lane g works out group g.
     uint64_t gkey = 0;
     if (lane < a.groups) {
-      double first = buf[lane * size], second = 0;
+      double first = get(lane * size), second = 0;
       uint64_t k1 = Keys::of(first), k2 = 0;
 #pragma unroll 4
       for (int i = 1; i < size; ++i) {
-        const double v = buf[lane * size + i];
+        const double v = get(lane * size + i);
         const uint64_t kv = Keys::of(v);
         const bool ahead = kv > k1, next = kv > k2;
         second = ahead ? first : next ? v : second;
@@ -260,13 +267,12 @@ __device__ __attribute__((always_inline)) inline int choose_exactly(const typena
   }
   // Each lane has a run of experts; buf holds their keys from here on.
   const int run = (a.E + 63) / 64, e0 = lane * run;
-  uint64_t *keys = reinterpret_cast<uint64_t *>(buf);
   uint64_t best = 0;
   int at = 0;
 #pragma clang loop unroll(disable)
   for (int e = e0; e < e0 + run && e < a.E; ++e) {
-    const uint64_t key = (kept >> (e / size)) & 1 ? Keys::of(bias != nullptr ? buf[e] : static_cast<double>(widen_logit<DT>(row[e]))) : 0;
-    keys[e] = key;
+    const uint64_t key = (kept >> (e / size)) & 1 ? Keys::of(bias != nullptr ? get(e) : static_cast<double>(widen_logit<DT>(row[e]))) : 0;
+    buf[e] = key;
     at = key > best ? e : at;
     best = key > best ? key : best;
   }
@@ -278,11 +284,11 @@ __device__ __attribute__((always_inline)) inline int choose_exactly(const typena
     const int chosen = __builtin_amdgcn_readlane(at, from);
     if (lane == j) mine = chosen;
     if (lane == from) {
-      keys[chosen] = 0;
+      buf[chosen] = 0;
       best = 0;
 #pragma clang loop unroll(disable)
       for (int e = e0; e < e0 + run && e < a.E; ++e) {
-        const uint64_t key = keys[e];
+        const uint64_t key = buf[e];
         at = key > best ? e : at;
         best = key > best ? key : best;
       }
@@ -339,7 +345,7 @@ __device__ inline Best merge(Best a, float v) {
 constexpr int kMaxGroups = 64;
 template <int L, int V>
 union TopkShared {
-  double exact[L * V];  // of one token
+  uint64_t exact[L * V];  // of one token
   struct {
     float value[64 / L][L * V];
     float group[64 / L][kMaxGroups], error[64 / L][kMaxGroups];
