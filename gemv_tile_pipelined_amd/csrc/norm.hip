@@ -11,13 +11,13 @@
 // A row is held in registers between the sum of squares and the output, so each input
 // is read once and each output written once: bound by memory.  Rows of up to 1536
 // columns are a wave's or less, several to a workgroup, and need no barrier; longer
-// ones are a workgroup's.  The sum of squares and r are in FP64, which costs nothing
+// ones are a workgroup's.  eps, the sum of squares and r are in FP64, which costs nothing
 // here (8192 x 4096 with the residual, 8 bits out, takes 46 us either way) and makes the
-// e4m3 numbers those nearest to y / scale but for one in some 10^7: weight h is exact in
-// FP32, r / scale has 48 bits, and the product is rounded to odd before the conversion,
-// so that only real ties tie.  y in 16 bits and both gradients are FP32 until their one
-// rounding.  16 lanes hold a block of 128 columns, 8 each, so a block's largest number
-// is found within a lane row.
+// e4m3 numbers those nearest to y / scale: weight h is exact in FP32, r / scale has 48
+// bits, and the product is rounded to odd before the conversion, so that nothing ties that
+// is further than 2^-47 of itself from the middle of two.  y in 16 bits and both gradients
+// are FP32 until their one rounding.  16 lanes hold a block of 128 columns, 8 each, so a
+// block's largest number is found within a lane row.
 #include "fp8_common.hpp"
 #include "kernels.hpp"
 #include "wave_ops.hpp"
@@ -412,10 +412,10 @@ hipError_t launch_norm(const NormArgs &a, hipStream_t stream) {
 }
 
 // LANES, NV, ROWS for a row's pieces of 8 columns.  2^25 numbers, us without a residual /
-// with it / with 8 bits out (bytes at a large copy's rate: 25.3, 50.6, 44.3): C = 64 27 / 48 /
-// 46 (a wave a row 95 / 147 / 207), 128 27 / 48 / 45 (54 / 85 / 110), 256 27 / 48 / 46 (33 / 55 /
-// 62), 1024 25 / 48 / 45 (two waves a row 26 / 51 / 47), 1536 25 / 48 / 46 (four 30 / 49 / 49), 2048
-// 27 / 47 / 46 (a wave a row 25 / 47 / 47), 20480 29 / 57 / 61 (four pieces a thread 30 / 59 / 64).
+// with it / with 8 bits out (bytes at a large copy's rate: 25.3, 50.6, 44.3): C = 64 29 / 48 /
+// 47 (a wave a row 95 / 147 / 207), 128 27 / 48 / 48 (54 / 85 / 110), 256 26 / 48 / 47 (33 / 55 /
+// 62), 1024 25 / 48 / 46 (two waves a row 26 / 51 / 47), 1536 25 / 48 / 47 (four 30 / 49 / 49), 2048
+// 27 / 48 / 47 (a wave a row 25 / 47 / 47), 20480 30 / 57 / 62 (four pieces a thread 30 / 59 / 64).
 template <int DT>
 hipError_t launch_norm_dt(const NormArgs &a, hipStream_t stream) {
   const int vecs = a.C / 8;

@@ -16,7 +16,8 @@
 // and a maximum over the lanes through DPP; nothing is marked as taken, and the
 // key says whose it is.
 //
-// Bound by vector instructions, 280 a token of 256 experts (16384 tokens, 8 of 256 of
+// Bound by vector instructions, 280 a token of 256 experts, half of them in the rounds,
+// which pass over all of a lane's numbers, dropped groups' too (16384 tokens, 8 of 256 of
 // bf16 logits: 6.7 us, with a sigmoid and a bias 10.7, in 4 of 8 groups 12.1; with a
 // wave a token, as at 16 of 256, 13.2, 19.3 and 22.1).
 //

@@ -78,8 +78,8 @@ def _quantize_fp4(x, q, scale, stream, dtype, call):
 def quantize_fp4_f16(x, q=None, scale=None, stream=None):
     """(q, scale) of a weight x [N,K], or of each of x [E,N,K], fp16: q [..,N,K/2] uint8 with two e2m1 numbers a byte
     (the even column in the low half) and scale [..,N,K/32] uint8, byte s of 32 columns standing for 2^(s - 127): the
-    least with which no number is beyond 6.  K % 32 == 0.  Enqueued on `stream` (default: the current stream), not
-    synchronised."""
+    least with which no number is beyond 6.  K % 32 == 0.  gemv_fp4_* takes one matrix at a time (q[e], scale[e]).
+    Enqueued on `stream` (default: the current stream), not synchronised."""
     return _quantize_fp4(x, q, scale, stream, torch.float16, load_library().quantize_fp4_f16)
 
 
@@ -108,7 +108,8 @@ def _gemv_fp4(x, W, scale_W, y, stream, dtype, call):
 
 def gemv_fp4_f16(x, W, scale_W, y=None, stream=None):
     """y = x · (W scaled)ᵀ for one row x [K] or a decode batch x [M,K], fp16, rounded once: W [N,K/2] and scale_W
-    [N,K/32] uint8 as quantize_fp4_f16 gives them, y [N] or [M,N].  Up to 48 rows share a read of W."""
+    [N,K/32] uint8 as quantize_fp4_f16 gives them, y [N] or [M,N].  Up to 48 rows share a read of W; a prompt's hundreds
+    of rows are faster by gemm_f16 on 16-bit weights."""
     return _gemv_fp4(x, W, scale_W, y, stream, torch.float16, load_library().gemv_fp4_f16)
 
 
@@ -144,7 +145,7 @@ def _rmsnorm(x, weight, residual, eps, h, y, rstd, stream, dtype, call):
 def rmsnorm_f16(x, weight, residual=None, eps=1e-6, h=None, y=None, rstd=None, stream=None):
     """(y, h): h = x + residual rounded to fp16 (x itself without a residual), y = h / sqrt(mean(h²) + eps) · weight.
     x, residual, h, y [T,C], weight [C] fp16; C % 8 == 0, C <= 32768.  h may be x or residual; rstd [T] FP32 takes
-    1 / sqrt(mean(h²) + eps) for rmsnorm_grad_f16.  Enqueued on `stream`, not synchronised."""
+    1 / sqrt(mean(h²) + eps) for rmsnorm_grad_f16; eps, the sum and the root are FP64.  Enqueued on `stream`, not synchronised."""
     return _rmsnorm(x, weight, residual, eps, h, y, rstd, stream, torch.float16, load_library().rmsnorm_f16)
 
 

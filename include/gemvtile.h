@@ -643,7 +643,7 @@ int64_t gemvtile_group_unit(const int32_t *offsets, int64_t E, int64_t T, int64_
  * the router before the products by expert, and the rows' way there and back.
  * All of them are asynchronous, keep nothing between calls, allocate nothing,
  * use no atomics that decide an order (results are deterministic) and can be
- * captured.
+ * captured.  Outputs overlap neither inputs nor one another, but for a norm's h.
  *
  * "e2m1" is the 4-bit format with 2 exponent bits (bias 1) and 1 fraction bit:
  * 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives.  An operand [N,K] of them is
@@ -717,7 +717,8 @@ int gemv_fp4_bf16(const void *x, const void *W, const void *scale_W, void *y, in
  *                the gradient of x and of residual alike
  *   dweight[c] = sum_t dy h r                                        FP32
  *
- * The rows' shares of dweight are added in FP32, in an order that T and C alone decide.
+ * Products and sums are in FP32 (weight * dy, h * r and their product have to be in its
+ * range); the rows' shares of dweight are added in an order that T and C alone decide.
  *   dy, dh, h, weight, dx  16-byte aligned; rstd, dweight 4-byte aligned; dx
  *            overlaps nothing
  *   workspace  gemvtile_rmsnorm_grad_workspace(T, C) bytes of device memory, owned
@@ -757,7 +758,9 @@ enum gemvtile_score {
  *   ids [T,k] int32  the k largest choices of the kept groups, largest first, ties
  *                    to the lowest expert
  *   weights [T,k]    FP32: scale * score[id] (no bias), divided by the sum of the k
- *                    scores if norm is 1
+ *                    scores if norm is 1; worked out in FP32 (the ids are not), so a
+ *                    few units in the last place off, and in proportion to the logits
+ *                    where those are large
  *
  * Ids are those of choices computed in 64 bits, whatever the logits' type.  A logit
  * of -inf is an expert with score 0, chosen after all others unless a bias lifts it (a
