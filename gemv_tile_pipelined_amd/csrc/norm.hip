@@ -93,13 +93,15 @@ __device__ inline float product_to_odd(float p, float high, float low) {
 
 // Rows whose r is outside this are multiplied in FP64: below, it is no normal FP32 number;
 // above, a product weight h that FP32 does not hold exactly (below 2^-134) may stand for
-// more than a zero of e4m3 (2^-90 and less).  So are blocks whose weight h leaves FP32's
-// range, as y need not.
+// more than a zero of e4m3 (2^-90 and less).  So are blocks whose largest weight h is 2^100
+// or more: it may leave FP32's range, as y need not, and the lower half of r / scale would
+// be below the normal numbers.
 constexpr double kLeastRoot = 0x1p-126, kMostRoot = 0x1p40;
-// The power of two that brings r to 2^9 .. 2^10, and weight h r 2^-that (at most 2^136)
-// into FP32.
+constexpr uint32_t kLargeProduct = 0x71800000;  // 2^100, as bits
+// The power of two that brings r to 2^36 .. 2^37, and weight h r 2^-that, of which 2^-90 to
+// 2^136 matter, to 2^-127 and more (16 bits of it are exact there) and 2^100 and less.
 __device__ inline int root_exponent(double r) {
-  return r == 0.0 ? -300 : r < __builtin_inf() ? __builtin_amdgcn_frexp_exp(r) - 10 : 0;
+  return r == 0.0 ? -300 : r < __builtin_inf() ? __builtin_amdgcn_frexp_exp(r) - 37 : 0;
 }
 
 // A number in FP64, converted where it is needed: the compiler would otherwise keep those
@@ -207,7 +209,7 @@ rmsnorm_kernel(const uint16_t *x, const uint16_t *residual, const uint16_t *__re
 #pragma unroll
         for (int j = 0; j < 8; ++j) a[j] *= w[j];
         uint32_t top = block_max();
-        if (__builtin_expect(far || top >= 0x7f800000u, 0)) {  // a block's lanes alike
+        if (__builtin_expect(far || top >= kLargeProduct, 0)) {  // a block's lanes alike
           const int e = root_exponent(rd);
           root = __builtin_ldexp(rd, -e);
           widen8<DT>(hv[i], a);

@@ -62,14 +62,27 @@ def test_numbers_next_to_the_middle(env, T, C, fmt):
     """Each block's largest number is 1.75, or 448 / 256, and all others are such middles over 256; a block's columns have
     one weight.  y / scale is then off the middle by what the scale's rounding to FP32 is off, less than 2^-24 to either
     side."""
+    h, weight = _between(C, T)
+    between = _check(env, env.device(h, fmt), env.device(weight, fmt), fmt)
+    assert between >= 0.9 * T * C
+
+
+def _between(C, T):
     r = np.random.default_rng(C + 1)
     h = r.integers(8, 16, (T, C)) * 2 + 1.0  # 17 to 31: five bits, between two numbers of four
     h = h * np.ldexp(1.0, r.integers(-12, -4, (T, C))) * r.choice([-1, 1], (T, C))
     h = np.where(np.abs(h) < 1.75, h, h / 4)
     h[:, ::128] = 1.75
-    weight = np.repeat(r.integers(128, 256, -(-C // 128)) / 128, 128)[:C]  # eight bits
-    between = _check(env, env.device(h, fmt), env.device(weight, fmt), fmt)
-    assert between >= 0.9 * T * C
+    return h, np.repeat(r.integers(128, 256, -(-C // 128)) / 128, 128)[:C]  # weights of eight bits
+
+
+@pytest.mark.parametrize("C", [64, 256, 1536, 4096])
+def test_numbers_next_to_the_middle_of_every_size(env, C):
+    """The same with rows and weights of bf16's whole range: r / scale has its 48 bits wherever they lie."""
+    h, weight = _between(C, 300)
+    for eh, ew in ((60, 40), (60, 50), (60, 60), (100, 10), (0, 90), (0, 110), (0, 125), (120, -20), (-100, 0), (-100, 100), (-60, -10), (-120, 120)):
+        hd, wd = env.device(np.ldexp(h, eh), "bf16"), env.device(np.ldexp(weight, ew), "bf16")
+        assert _check(env, hd, wd, "bf16", 0.0) >= 0.9 * 300 * C
 
 
 @FMT
